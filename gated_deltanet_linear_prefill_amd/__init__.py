@@ -6,7 +6,11 @@ workspace with torch when the caller does not pass them, and hand raw device poi
 the current stream to the library. Every step of the computation runs in the library's
 HIP kernels; there is no Python or CPU fallback, and a missing libgdn.so is an error.
 
-Layouts (see include/gdn.h): q, k [n, t, h_qk, d]; v [n, t, h_v, d]; g, beta [n, t, h_v]
+For a hybrid stack's softmax-attention layers there are a paged key-value cache
+(gdn_kv_write, gdn_kv_read), attention over packed prompts (gdn_attn_prefill) and of one new
+token over the cache (gdn_attn_decode); their tensors are described at each function.
+
+Layouts of the recurrence (see include/gdn.h): q, k [n, t, h_qk, d]; v [n, t, h_v, d]; g, beta [n, t, h_v]
 fp32; state [n, h_v, d, d] fp32 with element [i][j] = S[j][i]; out [n, t, h_v, d] fp32.
 """
 import ctypes
@@ -21,10 +25,11 @@ __all__ = [
     "bind_prefill_chunked", "bind_prefill_scan", "bind_decode_step", "DecodeGraph",
     "gdn_prefill_segmented", "gdn_prefill_segmented_workspace_bytes", "gdn_prefill_scan_blockwise",
     "calib_mfma_bf16", "calib_stream_copy", "gdn_prefill_segmented_noalloc", "gdn_noalloc_scratch_bytes",
-    "debug_fill_lds",
+    "debug_fill_lds", "gdn_kv_write", "gdn_kv_read", "gdn_attn_prefill", "gdn_attn_decode",
+    "gdn_attn_decode_workspace_bytes", "KvCache", "AttnDims",
 ]
 
-GDN_F32, GDN_BF16 = 0, 1
+GDN_F32, GDN_BF16, GDN_FP8 = 0, 1, 2
 _DTYPES = {torch.float32: GDN_F32, torch.bfloat16: GDN_BF16}
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libgdn.so")
 _lib = None
@@ -35,6 +40,25 @@ class Dims(ctypes.Structure):
     _fields_ = [("n", ctypes.c_int64), ("t", ctypes.c_int64), ("h_qk", ctypes.c_int32),
                 ("h_v", ctypes.c_int32), ("d_k", ctypes.c_int32), ("d_v", ctypes.c_int32),
                 ("qkv_dtype", ctypes.c_int32), ("l2_eps", ctypes.c_float)]
+
+
+class KvCache(ctypes.Structure):
+    """gdn_kv_cache from include/gdn.h."""
+    _fields_ = [("n", ctypes.c_int64), ("num_pages", ctypes.c_int64), ("max_pages", ctypes.c_int64),
+                ("page_size", ctypes.c_int32), ("h_kv", ctypes.c_int32), ("d", ctypes.c_int32),
+                ("store", ctypes.c_int32), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("page_table", ctypes.c_void_p)]
+
+
+class AttnDims(ctypes.Structure):
+    """gdn_attn_dims from include/gdn.h."""
+    _fields_ = [("n", ctypes.c_int64), ("total_q", ctypes.c_int64), ("total_k", ctypes.c_int64),
+                ("h_q", ctypes.c_int32), ("h_kv", ctypes.c_int32), ("d", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("causal", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("q_token", ctypes.c_int64), ("q_head", ctypes.c_int64),
+                ("k_token", ctypes.c_int64), ("k_head", ctypes.c_int64),
+                ("v_token", ctypes.c_int64), ("v_head", ctypes.c_int64)]
 
 
 class GdnError(RuntimeError):
@@ -56,7 +80,8 @@ def _load():
                            "(the HIP library is required, there is no fallback)")
     lib = ctypes.CDLL(_LIB_PATH)
     P, D = ctypes.c_void_p, ctypes.POINTER(Dims)
-    i32, sz = ctypes.c_int32, ctypes.c_size_t
+    i32, i64, sz = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
+    K = ctypes.POINTER(KvCache)
     sig = {
         "gdn_abi_version": (i32, []),
         "gdn_status_str": (ctypes.c_char_p, [ctypes.c_int32]),
@@ -79,6 +104,12 @@ def _load():
         "gdn_noalloc_scratch_bytes": (sz, []),
         "gdn_calib_stream_copy": (ctypes.c_int, [P, P, ctypes.c_int64, ctypes.c_int32, P]),
         "gdn_prefill_segmented_noalloc": (ctypes.c_int, [D, ctypes.c_int64] + [P] * 9),
+        "gdn_kv_write": (ctypes.c_int, [K, i64, i32, P, i64, i64, P, i64, i64, P, P, P]),
+        "gdn_kv_read": (ctypes.c_int, [K, i64, i32, P, P, P, P, P]),
+        "gdn_attn_prefill": (ctypes.c_int, [ctypes.POINTER(AttnDims)] + [P] * 8),
+        "gdn_attn_decode_workspace_bytes": (sz, [K, i32, i64]),
+        "gdn_attn_decode": (ctypes.c_int, [K, i32, i32, ctypes.c_float, i64, P, i64, i64, P, P, P,
+                                           P, sz, P]),
         "gdn_debug_fill_lds": (ctypes.c_int, [ctypes.c_uint32, ctypes.c_int32, P, P]),
     }
     for name, (res, args) in sig.items():
@@ -441,3 +472,210 @@ class DecodeGraph:
             self.close()
         except Exception:
             pass
+
+
+# ---------------------------------------------------------------- attention layers
+
+_POOLS = {torch.float32: GDN_F32, torch.bfloat16: GDN_BF16, torch.float8_e4m3fn: GDN_FP8}
+_i32 = torch.int32
+
+
+def _rows(name, x, dtype, dev):
+    """(pointer, token stride, head stride) of a [tokens, heads, d] tensor with contiguous d. The
+    stride of a dimension of one entry means nothing to torch: a dense one stands for it."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 3:
+        raise ValueError(f"{name} must be a torch tensor [tokens, heads, d]")
+    if x.device != dev or not x.is_cuda:
+        raise ValueError(f"{name} must be a CUDA (HIP) tensor on {dev}")
+    if x.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {x.dtype}")
+    t, h, d = x.shape
+    st, sh, sd = x.stride()
+    if sd != 1 and d > 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    if h == 1:
+        sh = d
+    if t <= 1:
+        st = sh * h
+    return x.data_ptr(), st, sh
+
+
+def _index(name, x, shape, dev):
+    """A contiguous int32 tensor of this shape on dev, or None."""
+    if x is None:
+        return None
+    if not isinstance(x, torch.Tensor) or x.dtype != _i32 or x.device != dev or x.shape != shape \
+            or not x.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor {tuple(shape)} on {dev}")
+    return x.data_ptr()
+
+
+def _dense(name, x, shape, dtype, dev):
+    if not isinstance(x, torch.Tensor) or x.dtype != dtype or x.device != dev or x.shape != shape \
+            or not x.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)} on {dev}")
+    return x.data_ptr()
+
+
+def _cache_of(k_cache, v_cache, page_table, k_scale, v_scale) -> KvCache:
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4 or not k_cache.is_cuda:
+        raise ValueError("k_cache must be a CUDA (HIP) tensor [num_pages, h_kv, page_size, d]")
+    store = _POOLS.get(k_cache.dtype)
+    if store is None:
+        raise ValueError("the cache must be bfloat16, float32 or float8_e4m3fn")
+    dev, shape = k_cache.device, k_cache.shape
+    pages, h, size, d = shape
+    k = _dense("k_cache", k_cache, shape, k_cache.dtype, dev)
+    v = _dense("v_cache", v_cache, shape, k_cache.dtype, dev)
+    ks = vs = None
+    if store == GDN_FP8:
+        ks = _dense("k_scale", k_scale, (pages, h, size), torch.uint8, dev)
+        vs = _dense("v_scale", v_scale, (pages, h, size), torch.uint8, dev)
+    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+        raise ValueError("page_table must be an int32 tensor [n, max_pages]")
+    n, width = page_table.shape
+    table = _index("page_table", page_table, page_table.shape, dev)
+    return KvCache(n, pages, width, size, h, d, store, k, v, ks, vs, table)
+
+
+def _dtype_id(x):
+    t = _DTYPES.get(x.dtype) if isinstance(x, torch.Tensor) else None
+    if t is None:
+        raise ValueError("tensors of rows must be bfloat16 or float32")
+    return t
+
+
+def gdn_kv_write(k, v, k_cache, v_cache, page_table, start, cu_seqlens=None, *, k_scale=None,
+                 v_scale=None, stream=None):
+    """Write new tokens into a paged cache, quantised as they are written.
+
+    k, v [total, h_kv, d] (bfloat16 or float32; tokens and heads may be strided): the new tokens
+    of n sequences, packed; sequence s has rows cu_seqlens[s] to cu_seqlens[s + 1] - 1
+    (cu_seqlens int32 [n + 1]; None: one token per sequence) and its row i goes to position
+    start[s] + i (start int32 [n]). k_cache, v_cache [num_pages, h_kv, page_size, d]: of k's
+    dtype, or float8_e4m3fn with k_scale, v_scale uint8 [num_pages, h_kv, page_size].
+    page_table int32 [n, max_pages]; a page id of -1 is a page that is not there, and what
+    would go there is dropped. Updates the cache in place; returns nothing."""
+    t = _dtype_id(k)
+    c = _cache_of(k_cache, v_cache, page_table, k_scale, v_scale)
+    dev = k_cache.device
+    kp, kt, kh = _rows("k", k, k.dtype, dev)
+    vp, vt, vh = _rows("v", v, k.dtype, dev)
+    total = k.shape[0]
+    if k.shape[1:] != (c.h_kv, c.d) or v.shape != k.shape:
+        raise ValueError(f"k and v must have shape {(total, c.h_kv, c.d)}")
+    sp = _index("start", start, (c.n,), dev)
+    cp = _index("cu_seqlens", cu_seqlens, (c.n + 1,), dev)
+    st = _load().gdn_kv_write(ctypes.byref(c), total, t, kp, kt, kh, vp, vt, vh, sp, cp,
+                              _stream(dev, stream))
+    if st:
+        raise GdnError(st, "gdn_kv_write")
+
+
+def gdn_kv_read(k_cache, v_cache, page_table, start, cu_seqlens, total, *, dtype=torch.bfloat16,
+                k_scale=None, v_scale=None, k_out=None, v_out=None, stream=None):
+    """Read tokens back from a paged cache, packed: position start[s] + i of sequence s becomes
+    row cu_seqlens[s] + i of the returned k, v [total, h_kv, d] (of dtype; zeros from pages that
+    are not there). total is the packed length, cu_seqlens[n], which the host has to know
+    (cu_seqlens None: one token per sequence). Arguments as for gdn_kv_write."""
+    t = _DTYPES.get(dtype)
+    if t is None:
+        raise ValueError("dtype must be bfloat16 or float32")
+    c = _cache_of(k_cache, v_cache, page_table, k_scale, v_scale)
+    dev = k_cache.device
+    shape = (int(total), c.h_kv, c.d)
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=dtype, device=dev)
+    if v_out is None:
+        v_out = torch.empty(shape, dtype=dtype, device=dev)
+    st = _load().gdn_kv_read(
+        ctypes.byref(c), shape[0], t, _dense("k_out", k_out, shape, dtype, dev),
+        _dense("v_out", v_out, shape, dtype, dev), _index("start", start, (c.n,), dev),
+        _index("cu_seqlens", cu_seqlens, (c.n + 1,), dev), _stream(dev, stream))
+    if st:
+        raise GdnError(st, "gdn_kv_read")
+    return k_out, v_out
+
+
+def gdn_attn_prefill(q, k, v, cu_q, cu_k=None, *, causal=True, scale=None, out=None, lse=None,
+                     stream=None):
+    """Attention over packed prompts, with grouped heads.
+
+    q [total_q, h_q, d], k and v [total_k, h_kv, d] (bfloat16 or float32; tokens and heads may be
+    strided); cu_q, cu_k int32 [n + 1]: sequence s has query rows cu_q[s] to cu_q[s + 1] - 1 and
+    key rows cu_k[s] to cu_k[s + 1] - 1 (cu_k None: the same). With causal, a sequence's last
+    query sees its last key, so a segment of new tokens may follow a context. scale defaults to
+    1 / sqrt(d). Rows that see no key give 0. Pass lse (float32 [total_q, h_q]) to have the
+    logarithm of each row's sum written to it. Returns out [total_q, h_q, d] of q's dtype."""
+    t = _dtype_id(q)
+    dev = q.device
+    qp, qt, qh = _rows("q", q, q.dtype, dev)
+    kp, kt, kh = _rows("k", k, q.dtype, dev)
+    vp, vt, vh = _rows("v", v, q.dtype, dev)
+    tq, hq, d = q.shape
+    tk, hk, _ = k.shape
+    if k.shape[2] != d or v.shape != k.shape:
+        raise ValueError(f"k and v must have the same shape [tokens, heads, {d}]")
+    n = cu_q.shape[0] - 1 if isinstance(cu_q, torch.Tensor) and cu_q.dim() == 1 else -1
+    if n < 0:
+        raise ValueError("cu_q must be an int32 tensor [n + 1]")
+    if out is None:
+        out = torch.empty((tq, hq, d), dtype=q.dtype, device=dev)
+        op = out.data_ptr()
+    else:
+        op = _dense("out", out, (tq, hq, d), q.dtype, dev)
+    lp = None if lse is None else _dense("lse", lse, (tq, hq), torch.float32, dev)
+    dims = AttnDims(n, tq, tk, hq, hk, d, t, 1 if causal else 0, d ** -0.5 if scale is None else scale,
+                    qt, qh, kt, kh, vt, vh)
+    st = _load().gdn_attn_prefill(ctypes.byref(dims), qp, kp, vp, _index("cu_q", cu_q, (n + 1,), dev),
+                                  _index("cu_k", cu_k, (n + 1,), dev), op, lp, _stream(dev, stream))
+    if st:
+        raise GdnError(st, "gdn_attn_prefill")
+    return out
+
+
+def gdn_attn_decode_workspace_bytes(n, max_pages, page_size, h_q, h_kv, d, max_len,
+                                    store=torch.bfloat16) -> int:
+    """Workspace bytes of gdn_attn_decode for these sizes."""
+    c = KvCache(n, 0, max_pages, page_size, h_kv, d, _POOLS.get(store, -1))
+    return int(_load().gdn_attn_decode_workspace_bytes(ctypes.byref(c), h_q, max_len))
+
+
+def gdn_attn_decode(q, k_cache, v_cache, page_table, lens, *, max_len=None, k_scale=None,
+                    v_scale=None, scale=None, out=None, lse=None, workspace=None, stream=None):
+    """Attention of one new token per sequence over a paged cache.
+
+    q [n, h_q, d] (bfloat16 or float32; tokens and heads may be strided): row s attends to
+    positions 0 to lens[s] - 1 of sequence s (lens int32 [n]; the new token's own position,
+    written before by gdn_kv_write, is one of them). max_len is a bound on lens that the host
+    knows (default: what the page table can hold); positions from it on are not read. The cache
+    as for gdn_kv_write. scale defaults to 1 / sqrt(d); lse as for gdn_attn_prefill, [n, h_q].
+    Returns out [n, h_q, d] of q's dtype."""
+    t = _dtype_id(q)
+    c = _cache_of(k_cache, v_cache, page_table, k_scale, v_scale)
+    dev = k_cache.device
+    qp, qt, qh = _rows("q", q, q.dtype, dev)
+    n, hq, d = q.shape
+    if n != c.n or d != c.d:
+        raise ValueError(f"q must have shape [{c.n}, h_q, {c.d}]")
+    if max_len is None:
+        max_len = c.max_pages * c.page_size
+    if out is None:
+        out = torch.empty((n, hq, d), dtype=q.dtype, device=dev)
+        op = out.data_ptr()
+    else:
+        op = _dense("out", out, (n, hq, d), q.dtype, dev)
+    lp = None if lse is None else _dense("lse", lse, (n, hq), torch.float32, dev)
+    lib = _load()
+    if workspace is None:
+        need = lib.gdn_attn_decode_workspace_bytes(ctypes.byref(c), hq, max_len)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    wbytes = _check_workspace(workspace, dev)
+    st = lib.gdn_attn_decode(
+        ctypes.byref(c), hq, t, d ** -0.5 if scale is None else scale, max_len, qp, qt, qh,
+        _index("lens", lens, (n,), dev), op, lp, None if workspace is None else workspace.data_ptr(),
+        wbytes, _stream(dev, stream))
+    if st:
+        raise GdnError(st, "gdn_attn_decode")
+    return out

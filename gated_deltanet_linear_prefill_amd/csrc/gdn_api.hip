@@ -8,6 +8,7 @@
 #include <math.h>
 #include <string.h>
 
+#include "gdn_checks.hpp"
 #include "gdn_internal.hpp"
 
 // A recorded decode graph: the instantiated HIP graph it replays.
@@ -19,20 +20,6 @@ namespace gdn {
 namespace {
 
 #include "gdn_crossover.inc"  // kCrossover[]: measured scan/chunk choice by length
-
-struct Range {
-    uintptr_t lo, hi;  // [lo, hi); empty when lo == hi
-};
-
-bool overlap(Range a, Range b)
-{
-    return a.lo < a.hi && b.lo < b.hi && a.lo < b.hi && b.lo < a.hi;
-}
-
-bool mul_ok(int64_t a, int64_t b, int64_t* r)
-{
-    return !__builtin_mul_overflow(a, b, r);
-}
 
 bool supported_d(int32_t d)
 {
@@ -74,17 +61,6 @@ gdn_status check_dims(const gdn_dims* d, Sizes* s)
     if (d->t >= (INT64_C(1) << 40)) return GDN_ERR_SHAPE;
     s->esize = d->qkv_dtype == GDN_BF16 ? 2 : 4;
     return GDN_OK;
-}
-
-Range range_of(const void* p, int64_t elems, size_t esize)
-{
-    const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-    return Range{lo, p ? lo + (uintptr_t)elems * esize : lo};
-}
-
-bool aligned(const void* p, uintptr_t a)
-{
-    return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
 }
 
 size_t workspace_for(const gdn_dims* d, int32_t chunk)
@@ -155,11 +131,6 @@ gdn_status validate(const gdn_dims* d, int32_t mode, const void* q, const void* 
     *call = Call{d->n, d->t, d->h_qk, d->h_v, d->d_k, d->qkv_dtype, d->l2_eps,
                  q, k, v, g, beta, state_in, out, state_out, ws, ws_bytes, nullptr};
     return GDN_OK;
-}
-
-gdn_status finish(hipError_t e)
-{
-    return e == hipSuccess ? GDN_OK : GDN_ERR_HIP;
 }
 
 // Copy (or zero) the state for an empty segment, t == 0.

@@ -1,0 +1,94 @@
+// gdn_attn_internal.hpp -- shared host/device pieces of the attention entry points (not part
+// of the C ABI).
+#pragma once
+
+#include "gdn_internal.hpp"
+
+namespace gdn {
+
+// Validated calls: sizes and strides checked, pointers present, aligned and disjoint.
+struct KvCall {
+    gdn_kv_cache c;
+    int64_t total;
+    int32_t dtype;
+    const void *k, *v;  // written from
+    int64_t k_token, k_head, v_token, v_head;
+    void *k_out, *v_out;  // read into
+    const int32_t *start, *cu;
+    hipStream_t stream;
+};
+
+struct AttnCall {
+    gdn_attn_dims d;
+    const void *q, *k, *v;
+    const int32_t *cu_q, *cu_k;
+    void* out;
+    float* lse;
+    hipStream_t stream;
+};
+
+struct AttnDecodeCall {
+    gdn_kv_cache c;
+    int32_t h_q, dtype;
+    float scale;
+    int64_t max_len;
+    const void* q;
+    int64_t q_token, q_head;
+    const int32_t* lens;
+    void* out;
+    float* lse;
+    void* ws;
+    hipStream_t stream;
+};
+
+hipError_t launch_kv_write(const KvCall& c);
+hipError_t launch_kv_read(const KvCall& c);
+hipError_t launch_attn_prefill(const AttnCall& c);
+hipError_t launch_attn_decode(const AttnDecodeCall& c);
+
+// Query rows (positions x heads of a KV head) a prefill workgroup handles, for the grid bound.
+int attn_prefill_rows(int32_t d, int32_t dtype);
+// Workspace of a decode call (0: not split), from the sizes the host knows.
+size_t attn_decode_workspace(const gdn_kv_cache* c, int32_t h_q, int64_t max_len);
+
+// ---------------------------------------------------------------- device helpers
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x4_t __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef float f32x2_t __attribute__((ext_vector_type(2)));
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+
+// Two floats as packed bf16 (round to nearest even), the first in the low half.
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b)
+{
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{a, b}, bf16x2_t));
+}
+
+// 2^e for -126 <= e <= 127.
+__device__ __forceinline__ float exp2_int(int e)
+{
+    return __uint_as_float((uint32_t)(e + 127) << 23);
+}
+
+// The factor of a scale byte: 2^(b - 127); byte 0, which no write makes, counts as 0.
+__device__ __forceinline__ float scale_of(uint32_t b)
+{
+    return __uint_as_float(b << 23);
+}
+
+// The sequence a packed row belongs to: the last s in [0, n) with cu[s] <= row (0 if none).
+// Whatever cu holds, the answer is a valid sequence index.
+__device__ __forceinline__ int64_t find_seq(const int32_t* cu, int64_t n, int64_t row)
+{
+    int64_t lo = 0, hi = n;  // cu[lo] <= row (or lo == 0), cu[hi] > row (or hi == n)
+    while (hi - lo > 1) {
+        const int64_t mid = (lo + hi) >> 1;
+        if (cu[mid] <= row) lo = mid; else hi = mid;
+    }
+    return lo;
+}
+
+}  // namespace gdn

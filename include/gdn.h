@@ -1,6 +1,9 @@
 /*
  * gdn.h -- C ABI of libgdn.so: the Gated DeltaNet layer recurrence on AMD Instinct
- * MI355X (gfx950), prefill and batch-1 decode.
+ * MI355X (gfx950), prefill and batch-1 decode; and, for the softmax-attention layers that a
+ * hybrid model runs between those layers, a paged key-value cache (gdn_kv_*) and attention
+ * over it and over packed prompts (gdn_attn_*; their own section at the end, with the
+ * layouts and limits that differ from those stated here).
  *
  * Source of the operation: "Optimizing on-device inference for Apple Silicon"
  * (Perplexity, 2026).
@@ -81,7 +84,7 @@
 extern "C" {
 #endif
 
-#define GDN_ABI_VERSION 2
+#define GDN_ABI_VERSION 3
 
 typedef enum {
     GDN_OK = 0,
@@ -94,7 +97,8 @@ typedef enum {
     GDN_ERR_HIP = 7          /* the HIP runtime reported an error at launch               */
 } gdn_status;
 
-typedef enum { GDN_F32 = 0, GDN_BF16 = 1 } gdn_dtype;
+/* GDN_FP8 (e4m3 codes with power-of-two row scales) is a cache store only: see gdn_kv_cache. */
+typedef enum { GDN_F32 = 0, GDN_BF16 = 1, GDN_FP8 = 2 } gdn_dtype;
 
 typedef struct {
     int64_t n;         /* independent sequences (or stacked layers for decode)     */
@@ -335,6 +339,136 @@ gdn_status gdn_calib_stream_copy(const void* src, void* dst, int64_t bytes, int3
  * 0 < blocks <= 2^20, GDN_ERR_ALIGN for a sink not 4-byte aligned.
  */
 gdn_status gdn_debug_fill_lds(uint32_t pattern, int32_t blocks, uint32_t* sink, void* stream);
+
+/* ======================================================================================
+ * Attention layers: paged key-value cache, packed prefill attention, decode attention.
+ *
+ * A hybrid model runs softmax attention between its recurrent layers ("Qwen creates three
+ * distinct workload shapes"), with query heads that share key-value heads and a cache that
+ * grows by a token per step ("Read the attention cache efficiently"). Query head h reads KV
+ * head h / (h_q / h_kv). Everything said above about streams, ownership, capture, validation
+ * and errors holds here too: device pointers, caller-owned buffers, kernels only, nothing
+ * allocated or synchronised. Every argument the host can see is checked before anything is
+ * enqueued. What lies in device memory (cu_seqlens, start, lens, page_table) cannot be checked
+ * on the host: the kernels clamp it, so that a bad value gives a wrong result or an empty
+ * one, never an access outside the buffers described here.
+ *
+ * Supported: d in {64, 128, 256}; h_q a multiple of h_kv; page_size a power of two, 16 to
+ * 1024; q, k, v, out of one dtype (GDN_BF16 or GDN_F32); the store is that dtype or GDN_FP8.
+ *
+ * Packed rows. The tokens of n sequences lie one after another in one tensor; sequence s has
+ * rows cu_seqlens[s] .. cu_seqlens[s + 1] - 1 (int32, n + 1 entries, non-decreasing). Rows
+ * that belong to no sequence are not read and, in outputs, not written. Where cu_seqlens may
+ * be NULL, every sequence has one row, row s.
+ *
+ * Strides. q, k and v rows may be strided (a slice of a fused projection): *_token is the
+ * distance between tokens and *_head between heads, in elements; the d elements of a head are
+ * contiguous. Strides are positive multiples of 8 (bf16) or 4 (fp32) elements, and no two
+ * heads or tokens may overlap. out, lse and what gdn_kv_read writes are dense.
+ *
+ * Alignment. 16 bytes for q, k, v, out, the pools and workspace; 4 for int32 arrays and lse.
+ * Aliasing. An output that overlaps any other buffer of the call is GDN_ERR_ALIAS.
+ * ====================================================================================== */
+
+/*
+ * A paged cache of n sequences. Position p of sequence s lies in page
+ * page_table[s * max_pages + p / page_size], row p % page_size. A page id outside
+ * [0, num_pages) (-1, say) is a page that is not there: writes to it are dropped, reads give
+ * zeros, attention skips its positions. Pages may be in any order; two sequences may share
+ * one to read.
+ *   k, v              [num_pages][h_kv][page_size][d]  of the store's type
+ *   k_scale, v_scale  [num_pages][h_kv][page_size]     GDN_FP8 only (else ignored)
+ * GDN_FP8: a row of d values is kept as e4m3 codes (OCP: largest 448, no infinity) times
+ * 2^(scale - 127), one scale per (token, KV head): the smallest power of two, at least
+ * 2^-126, that brings the row's largest finite magnitude within 448 (127 for a row of zeros).
+ * Scaling by a power of two is exact, so a value is rounded once, to nearest even, as it is
+ * written, and not again when it is read (as bf16, unless it is below 2^-126). NaN and
+ * infinities become NaN.
+ */
+typedef struct {
+    int64_t n;         /* sequences: rows of page_table                             */
+    int64_t num_pages; /* pages in the pools                                        */
+    int64_t max_pages; /* entries of page_table per sequence                        */
+    int32_t page_size; /* tokens per page                                           */
+    int32_t h_kv;      /* key-value heads                                           */
+    int32_t d;         /* head dimension                                            */
+    int32_t store;     /* gdn_dtype of the pools                                    */
+    void* k;
+    void* v;
+    uint8_t* k_scale;
+    uint8_t* v_scale;
+    const int32_t* page_table;
+} gdn_kv_cache;
+
+/*
+ * Write new tokens into the cache, quantised as they are written: row cu_seqlens[s] + i of k
+ * and v ([total][h_kv][d], strided) goes to position start[s] + i of sequence s. total bounds
+ * the rows. cu_seqlens may be NULL (one token per sequence, total == n: a decode step).
+ * Positions beyond the page table, or on a page that is not there, are dropped. Two tokens
+ * with the same place leave either, not a mixture of rows of different tokens within one
+ * element. Everything else in the pools stays as it is.
+ */
+gdn_status gdn_kv_write(const gdn_kv_cache* cache, int64_t total, int32_t dtype, const void* k,
+                        int64_t k_token, int64_t k_head, const void* v, int64_t v_token,
+                        int64_t v_head, const int32_t* start, const int32_t* cu_seqlens,
+                        void* stream);
+
+/*
+ * Read tokens back: position start[s] + i of sequence s becomes row cu_seqlens[s] + i of k and
+ * v ([total][h_kv][d], dense, of dtype), for the rows that cu_seqlens gives. With start 0 and
+ * the sequences' lengths this is the whole context, in the packed form that gdn_attn_prefill
+ * reads. cu_seqlens may be NULL as for gdn_kv_write.
+ */
+gdn_status gdn_kv_read(const gdn_kv_cache* cache, int64_t total, int32_t dtype, void* k, void* v,
+                       const int32_t* start, const int32_t* cu_seqlens, void* stream);
+
+/*
+ * Attention over packed prompts. Per sequence with len_q query rows and len_k key rows, and
+ * per head:
+ *     s_ij = scale * q_i . k_j,  o_i = sum_j exp(s_ij - lse_i) v_j,  lse_i = ln sum_j exp(s_ij)
+ * over the keys j that row i may see: all, or with causal != 0 those with
+ * j <= i + len_k - len_q (the last query sees the last key: a segment of new tokens after
+ * len_k - len_q tokens of context). A row that sees no key has o = 0, lse = -inf. A key that a
+ * row may not see contributes nothing to it, whatever it holds (NaN included).
+ *   q [total_q][h_q][d], k, v [total_k][h_kv][d] (strided); out [total_q][h_q][d] of dtype;
+ *   lse [total_q][h_q] fp32, or NULL. cu_q, cu_k: the two packings (cu_k NULL: the same as
+ *   cu_q, and total_k == total_q).
+ * Scores, softmax statistics and sums are fp32; with bf16 inputs the softmax weights are
+ * rounded to bf16 for the matrix product with V, with fp32 inputs nothing is rounded.
+ */
+typedef struct {
+    int64_t n;       /* sequences                                                */
+    int64_t total_q; /* rows of q, out and lse                                   */
+    int64_t total_k; /* rows of k and v                                          */
+    int32_t h_q;     /* query heads, a multiple of h_kv                          */
+    int32_t h_kv;    /* key-value heads                                          */
+    int32_t d;       /* head dimension                                           */
+    int32_t dtype;   /* gdn_dtype of q, k, v and out                             */
+    int32_t causal;  /* 0 or 1                                                   */
+    float scale;     /* finite; 1 / sqrt(d) is usual                             */
+    int64_t q_token, q_head, k_token, k_head, v_token, v_head; /* strides, in elements */
+} gdn_attn_dims;
+
+gdn_status gdn_attn_prefill(const gdn_attn_dims* dims, const void* q, const void* k,
+                            const void* v, const int32_t* cu_q, const int32_t* cu_k, void* out,
+                            float* lse, void* stream);
+
+/*
+ * Attention of one new token per sequence over the cache: query row s of q ([n][h_q][d], its
+ * token and head strides in elements) attends to positions 0 .. lens[s] - 1 of sequence s (the
+ * new token's own, written before, among them). out [n][h_q][d] of dtype; lse [n][h_q] fp32
+ * or NULL. lens[s] <= 0 gives o = 0, lse = -inf. max_len is the caller's bound on lens, which
+ * the host cannot see: positions from max_len on are not read; the work is split over it.
+ * A long cache is split into ranges that are attended to separately and joined in a second
+ * pass, in a fixed order, so results are the same from run to run. workspace:
+ * gdn_attn_decode_workspace_bytes(cache, h_q, max_len) bytes (0 when nothing is split, and
+ * for invalid arguments).
+ */
+size_t gdn_attn_decode_workspace_bytes(const gdn_kv_cache* cache, int32_t h_q, int64_t max_len);
+gdn_status gdn_attn_decode(const gdn_kv_cache* cache, int32_t h_q, int32_t dtype, float scale,
+                           int64_t max_len, const void* q, int64_t q_token, int64_t q_head,
+                           const int32_t* lens, void* out, float* lse, void* workspace,
+                           size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }
