@@ -33,10 +33,11 @@ constexpr float kLn2 = 0.6931471805599453f;
 template <typename T, int D>
 struct Tile;
 
-// bf16: 32 query rows per wave, 64 keys per step
+// bf16: 32 query rows per wave; 64 keys per step, 32 where a row's registers (its share of O
+// and Q) take most of the 256 a wave has at two waves per SIMD
 template <int D>
 struct Tile<uint16_t, D> {
-    static constexpr int N = 64, M = 32 * kWaves;
+    static constexpr int N = D == 256 ? 32 : 64, M = 32 * kWaves;
 };
 
 // fp32: 32 query rows per wave, 32 keys per step
@@ -226,37 +227,130 @@ __device__ __forceinline__ void write_row(const AttnCall& p, const Work& w, int6
     if (p.lse && lane < 32) p.lse[row] = l > 0.f ? (st.m + __builtin_amdgcn_logf(l)) * kLn2 : (l == l ? -INFINITY : l);
 }
 
+// One step of a wave's 32 rows over N staged keys. MASKED: some of the keys may not be seen by
+// some of the rows: row `lane & 31` sees those below lim.
+template <int D, bool MASKED>
+__device__ __forceinline__ void bf16_step(const char* sk, const char* sv, const bf16x8_t (&q)[D / 16],
+                                          f32x16_t (&o)[D / 32], Stats& st, float c, int lim, int lane)
+{
+    constexpr int N = Tile<uint16_t, D>::N, CH = D / 8, ND = D / 32;
+    const int half = lane >> 5, l31 = lane & 31;
+    f32x16_t s[N / 32];
+#pragma unroll
+    for (int b = 0; b < N / 32; ++b) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[b][i] = 0.f;
+        const int row = 32 * b + l31;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+            const int ch = (2 * kk + half) ^ swz_k<CH>(row);
+            const bf16x8_t a = *reinterpret_cast<const bf16x8_t*>(sk + row * (D * 2) + ch * 16);
+            s[b] = mfma32(a, q[kk], s[b]);
+        }
+    }
+    // key of register i of block b: 32 b + 8 (i / 4) + 4 half + i % 4
+    float mx = -INFINITY;
+#pragma unroll
+    for (int b = 0; b < N / 32; ++b)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            if (MASKED) s[b][i] = 32 * b + 8 * (i / 4) + 4 * half + i % 4 < lim ? s[b][i] : -INFINITY;
+            mx = fmaxf(mx, s[b][i]);
+        }
+    mx = other_half_max(mx);
+    // the reference maximum moves only when weights would pass 2^8: O is then rescaled
+    const bool rise = mx > st.m && (st.m == -INFINITY || (mx - st.m) * c > 8.f);
+    if (__any(rise)) {
+        const float a = !rise ? 1.f : st.m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((st.m - mx) * c);
+        st.m = rise ? mx : st.m;
+        st.l *= a;
+#pragma unroll
+        for (int db = 0; db < ND; ++db)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[db][i] *= a;
+    }
+    const float ref = st.m == -INFINITY ? 0.f : st.m * c;
+#pragma unroll
+    for (int b = 0; b < N / 32; ++b)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[b][i], c, -ref));
+            if (MASKED) p = 32 * b + 8 * (i / 4) + 4 * half + i % 4 < lim ? p : 0.f;
+            s[b][i] = p;
+            st.l += p;
+        }
+#pragma unroll
+    for (int t = 0; t < N / 16; ++t) {
+        u32x4_t pw;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            pw[i] = pack_bf16(s[t / 2][8 * (t & 1) + 2 * i], s[t / 2][8 * (t & 1) + 2 * i + 1]);
+        const bf16x8_t pb = __builtin_bit_cast(bf16x8_t, pw);
+        const int i16 = lane & 15, gg = (lane >> 4) & 1;
+        const int row = 16 * t + 4 * half + (i16 >> 2);
+#pragma unroll
+        for (int db = 0; db < ND; ++db) {
+            const int ch = 4 * db + 2 * gg + ((i16 >> 1) & 1), in = 8 * (i16 & 1);
+            const bf16x4_t a0 = read_tr(sv + row * (D * 2) + (ch ^ swz_v<CH>(row)) * 16 + in);
+            const bf16x4_t a1 = read_tr(sv + (row + 8) * (D * 2) + (ch ^ swz_v<CH>(row + 8)) * 16 + in);
+            const bf16x8_t a = __builtin_shufflevector(a0, a1, 0, 1, 2, 3, 4, 5, 6, 7);
+            if (MASKED && any_not_finite(a)) {
+#pragma unroll 1
+                for (int key = 0; key < 16; ++key) {
+                    // key 8 (j / 4) + 4 half + j % 4 sits in slot j of this half
+                    const int slot = 4 * (key >> 3) + (key & 3);
+                    const bool mine = ((key >> 2) & 1) == half;
+                    u32x4_t one = __builtin_bit_cast(u32x4_t, a);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        one[i] &= mine && (slot >> 1) == i ? (slot & 1 ? 0xffff0000u : 0xffffu) : 0u;
+                    const f32x16_t x = mfma32(__builtin_bit_cast(bf16x8_t, one), pb, o[db]);
+                    const bool sees = 16 * t + key < lim;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) o[db][i] = sees ? x[i] : o[db][i];
+                }
+            } else {
+                o[db] = mfma32(a, pb, o[db]);
+            }
+        }
+    }
+}
+
 template <int D>
-__global__ void __launch_bounds__(64 * kWaves) prefill_bf16_kernel(AttnCall p)
+__global__ void __launch_bounds__(64 * kWaves, 2) prefill_bf16_kernel(AttnCall p)
 {
     constexpr int N = Tile<uint16_t, D>::N, M = Tile<uint16_t, D>::M, CH = D / 8, ND = D / 32;
-    __shared__ __align__(16) char s_k[N * D * 2];
-    __shared__ __align__(16) char s_v[N * D * 2];
+    __shared__ __align__(16) char s_k[2][N * D * 2];
+    __shared__ __align__(16) char s_v[2][N * D * 2];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int half = lane >> 5, l31 = lane & 31;
     Work w;
     if (!find_work<M>(p, blockIdx.x / p.d.h_kv, blockIdx.x % p.d.h_kv, &w)) return;
     const int g = p.d.h_q / p.d.h_kv;
 
     // this lane's query: row r of the sequence's packed rows
-    const int64_t r = w.row0 + 32 * wave + l31;
-    const int64_t pos = (r < w.rows ? r : w.rows - 1) / g, hh = (r < w.rows ? r : w.rows - 1) - pos * g;
-    const int64_t limit = key_limit(w, pos, p.d.causal);
+    const int64_t r = w.row0 + 32 * wave + (lane & 31);
+    const int64_t rc = r < w.rows ? r : w.rows - 1, pos = rc / g;
     const uint16_t* qp = static_cast<const uint16_t*>(p.q) + (w.q0 + pos) * p.d.q_token +
-                         ((int64_t)w.head * g + hh) * p.d.q_head + 8 * half;
+                         ((int64_t)w.head * g + (rc - pos * g)) * p.d.q_head + 8 * (lane >> 5);
+    // a negative scale becomes a positive one of the negated query: the maximum of the raw
+    // scores is then that of the scaled ones
+    const uint32_t flip = p.d.scale < 0.f ? 0x80008000u : 0u;
+    const float c = fabsf(p.d.scale) * kLog2e;
     bf16x8_t q[D / 16];
 #pragma unroll
-    for (int kk = 0; kk < D / 16; ++kk) q[kk] = *reinterpret_cast<const bf16x8_t*>(qp + 16 * kk);
+    for (int kk = 0; kk < D / 16; ++kk)
+        q[kk] = __builtin_bit_cast(bf16x8_t, *reinterpret_cast<const u32x4_t*>(qp + 16 * kk) ^ flip);
 
-    // keys the workgroup needs (its last row sees the most), and those all of the wave's rows see
+    // keys that the workgroup's last row sees, that all of its rows see, and per lane
     const int64_t last = (w.row0 + M < w.rows ? w.row0 + M : w.rows) - 1;
     const int64_t keys = key_limit(w, last / g, p.d.causal);
-    const int64_t wrow = w.row0 + 32 * wave;
-    const int64_t all = key_limit(w, (wrow < w.rows ? wrow : w.rows - 1) / g, p.d.causal);
+    const int64_t all = key_limit(w, w.row0 / g, p.d.causal);
+    const int64_t limit = key_limit(w, pos, p.d.causal);
+    const int64_t wlast = w.row0 + 32 * wave + 31 < w.rows ? w.row0 + 32 * wave + 31 : w.rows - 1;
+    const int64_t wkeys = key_limit(w, wlast / g, p.d.causal);
 
     const char* kb = static_cast<const char*>(p.k) + 2 * (w.k0 * p.d.k_token + w.head * p.d.k_head);
     const char* vb = static_cast<const char*>(p.v) + 2 * (w.k0 * p.d.v_token + w.head * p.d.v_head);
-    const float c = p.d.scale * kLog2e;
 
     f32x16_t o[ND];
 #pragma unroll
@@ -265,73 +359,33 @@ __global__ void __launch_bounds__(64 * kWaves) prefill_bf16_kernel(AttnCall p)
         for (int i = 0; i < 16; ++i) o[db][i] = 0.f;
     Stats st = {-INFINITY, 0.f};
 
-    for (int64_t j0 = 0; j0 < keys; j0 += N) {
-        __syncthreads();
-        stage<N, CH, false>(kb, j0, w.len_k, 2 * p.d.k_token, s_k, wave, lane);
-        stage<N, CH, true>(vb, j0, w.len_k, 2 * p.d.v_token, s_v, wave, lane);
-        __syncthreads();
-
-        float s[N / 2];
-#pragma unroll
-        for (int b = 0; b < N / 32; ++b) {
-            f32x16_t acc;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) acc[i] = 0.f;
-            const int row = 32 * b + l31;
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-                const int ch = (2 * kk + half) ^ swz_k<CH>(row);
-                const bf16x8_t a = *reinterpret_cast<const bf16x8_t*>(s_k + row * (D * 2) + ch * 16);
-                acc = mfma32(a, q[kk], acc);
-            }
-#pragma unroll
-            for (int i = 0; i < 16; ++i) s[16 * b + i] = acc[i] * c;
-        }
-        const bool masked = j0 + N > all;
-        if (masked) {
-            const int lim = (int)(limit - j0 < N ? limit - j0 : N);
-#pragma unroll
-            for (int i = 0; i < N / 2; ++i) {
-                const int key = 32 * (i / 16) + 8 * ((i % 16) / 4) + 4 * half + i % 4;
-                s[i] = key < lim ? s[i] : -INFINITY;
-            }
-        }
-        softmax_step<N / 2, ND>(s, o, &st);
-#pragma unroll
-        for (int t = 0; t < N / 16; ++t) {
-            u32x4_t pw;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) pw[i] = pack_bf16(s[8 * t + 2 * i], s[8 * t + 2 * i + 1]);
-            const bf16x8_t pb = __builtin_bit_cast(bf16x8_t, pw);
-            const int i16 = lane & 15, gg = (lane >> 4) & 1;
-            const int row = 16 * t + 4 * half + (i16 >> 2);
-#pragma unroll
-            for (int db = 0; db < ND; ++db) {
-                const int ch = 4 * db + 2 * gg + ((i16 >> 1) & 1), in = 8 * (i16 & 1);
-                const bf16x4_t a0 = read_tr(s_v + row * (D * 2) + (ch ^ swz_v<CH>(row)) * 16 + in);
-                const bf16x4_t a1 = read_tr(s_v + (row + 8) * (D * 2) + (ch ^ swz_v<CH>(row + 8)) * 16 + in);
-                const bf16x8_t a = __builtin_shufflevector(a0, a1, 0, 1, 2, 3, 4, 5, 6, 7);
-                if (masked && any_not_finite(a)) {
-                    const int lim = (int)(limit - j0 < N ? limit - j0 : N);
-                    for (int key = 0; key < 16; ++key) {
-                        // key 8 (j / 4) + 4 half + j % 4 sits in slot j of this half
-                        const int slot = 4 * (key >> 3) + (key & 3);
-                        const bool mine = ((key >> 2) & 1) == half;
-                        u32x4_t one = __builtin_bit_cast(u32x4_t, a);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            one[i] &= mine && (slot >> 1) == i ? (slot & 1 ? 0xffff0000u : 0xffffu) : 0u;
-                        const f32x16_t x = mfma32(__builtin_bit_cast(bf16x8_t, one), pb, o[db]);
-                        const bool sees = 16 * t + key < lim;
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) o[db][i] = sees ? x[i] : o[db][i];
-                    }
-                } else {
-                    o[db] = mfma32(a, pb, o[db]);
-                }
-            }
-        }
+    // Two buffers: while a step's keys are used the next step's arrive. The barrier at the top
+    // of a step has every wave's loads of it done, and every wave past the buffer refilled next.
+    const int64_t steps = (keys + N - 1) / N, plain = all / N;
+    if (steps > 0) {
+        stage<N, CH, false>(kb, 0, w.len_k, 2 * p.d.k_token, s_k[0], wave, lane);
+        stage<N, CH, true>(vb, 0, w.len_k, 2 * p.d.v_token, s_v[0], wave, lane);
     }
+    int64_t x = 0;
+    for (; x < plain; ++x) {
+        __syncthreads();
+        if (x + 1 < steps) {
+            stage<N, CH, false>(kb, (x + 1) * N, w.len_k, 2 * p.d.k_token, s_k[(x + 1) & 1], wave, lane);
+            stage<N, CH, true>(vb, (x + 1) * N, w.len_k, 2 * p.d.v_token, s_v[(x + 1) & 1], wave, lane);
+        }
+        bf16_step<D, false>(s_k[x & 1], s_v[x & 1], q, o, st, c, N, lane);
+    }
+    for (; x < steps; ++x) {
+        __syncthreads();
+        if (x + 1 < steps) {
+            stage<N, CH, false>(kb, (x + 1) * N, w.len_k, 2 * p.d.k_token, s_k[(x + 1) & 1], wave, lane);
+            stage<N, CH, true>(vb, (x + 1) * N, w.len_k, 2 * p.d.v_token, s_v[(x + 1) & 1], wave, lane);
+        }
+        if (x * N >= wkeys) continue;  // nothing here for this wave's rows
+        const int64_t left = limit - x * N;
+        bf16_step<D, true>(s_k[x & 1], s_v[x & 1], q, o, st, c, (int)(left < 0 ? 0 : left < N ? left : N), lane);
+    }
+    st.m *= c;
     write_row<uint16_t, D>(p, w, r, lane, o, st);
 }
 
@@ -407,6 +461,7 @@ __global__ void __launch_bounds__(64 * kWaves) prefill_f32_kernel(AttnCall p)
                 const float a = *reinterpret_cast<const float*>(s_v + row * (D * 4) +
                                                                 (ch ^ swz_k<CH>(row)) * 16 + 4 * (l31 & 3));
                 if (masked && __any(!(fabsf(a) <= 3.4028234e38f))) {
+#pragma unroll 1
                     for (int x = 0; x < 2; ++x) {  // the two keys of the product, one at a time
                         const f32x16_t y = __builtin_amdgcn_mfma_f32_32x32x2f32(half == x ? a : 0.f, s[i], o[db], 0, 0, 0);
                         const bool sees = 8 * (i / 4) + 4 * x + i % 4 < lim;
