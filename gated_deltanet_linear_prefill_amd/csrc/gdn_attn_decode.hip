@@ -2,7 +2,7 @@
 //
 // Bound by the bytes of the cache: every K and V row is read once per KV head, for all of its
 // G = h_q / h_kv query heads (up to 16 at a time). One workgroup takes one (sequence, KV head)
-// and one range of positions; its waves take 32-position steps of the range in turn, each with
+// and one range of positions; its waves take 32-position (16 for long rows) steps of the range in turn, each with
 // its own softmax state, and are joined in LDS. When the pairs alone would not fill the chip
 // the positions are split over more workgroups (ranges), whose sums go to the workspace and
 // are joined by a second kernel.
@@ -19,8 +19,8 @@
 namespace gdn {
 namespace {
 
-constexpr int kWaves = 4, kStep = 32;  // positions per wave and step
-constexpr int kRange = kWaves * kStep; // ranges are multiples of this
+constexpr int kWaves = 4;
+constexpr int kRange = 32 * kWaves;    // ranges are multiples of this: a step of every wave
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -38,10 +38,19 @@ Plan make_plan(const gdn_kv_cache* c, int32_t h_q, int64_t max_len)
     p.head_tiles = (h_q / c->h_kv + 15) / 16;
     const int64_t units = c->n * c->h_kv * p.head_tiles;
     const int64_t steps = len > 0 ? (len + kRange - 1) / kRange : 1;
-    int64_t ranges = units > 0 ? (1024 + units - 1) / units : 1;
-    if (ranges < (steps + 15) / 16) ranges = (steps + 15) / 16;
+    // Measured (us of a call, d = 256, 2 KV heads): 333 positions 13 in one range, 17.5 in three;
+    // 1024 positions 24 in one, 17.5 in four; so up to four steps stay together. A single
+    // sequence of 131072 fp8 positions 33 in 256 ranges (one workgroup a CU), 39 in 1024. A
+    // batch's lengths differ: 64 sequences of up to 8192, 8 KV heads, 198 in one range each,
+    // 187 in ranges of 2048, 176 of 1024, where late workgroups fill the CUs that are done.
+    const int64_t most = units * steps;
+    int64_t want = most / 8 < 4096 ? most / 8 : 4096;
+    if (want < 256 || c->n == 1) want = 256;
+    int64_t ranges = units > 0 ? (want + units - 1) / units : 1;
+    if (ranges > (steps + 1) / 2) ranges = (steps + 1) / 2;
+    if (steps <= 4) ranges = 1;
     if (units > 0 && ranges > 0x7fffffff / units) ranges = 0x7fffffff / units;  // one grid dimension
-    if (ranges > steps) ranges = steps;
+    if (ranges < 1) ranges = 1;
     const int64_t per = (steps + ranges - 1) / ranges;
     p.range = per * kRange;
     p.ranges = (steps + per - 1) / per;
@@ -63,6 +72,8 @@ struct Cfg {
     static constexpr int U = VL / EPL;
     static constexpr int KL = D * ES / 64;                     // 16-byte loads of a K row per lane
     static constexpr int EPK = 16 / ES;                        // elements of each
+    // 16-position blocks of a step: K and V rows of a step stay in registers
+    static constexpr int NB = D * ES > 512 ? 1 : 2, STEP = 16 * NB;
 };
 
 template <int BYTES>
@@ -85,7 +96,7 @@ __device__ __forceinline__ uint32_t cvt_bf16_fp8(uint32_t w, bool hi)
 }
 
 template <typename T, bool FP8, int D>
-__global__ void __launch_bounds__(64 * kWaves)
+__global__ void __launch_bounds__(64 * kWaves, 2)
 decode_attn_kernel(AttnDecodeCall p, int64_t range, int ranges, int head_tiles, int page_shift,
                    Partials part)
 {
@@ -97,13 +108,17 @@ decode_attn_kernel(AttnDecodeCall p, int64_t range, int ranges, int head_tiles, 
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 15, g = lane >> 4;
-    const int rg = blockIdx.x % ranges;
-    const int64_t unit = blockIdx.x / ranges;
+    // ranges of one index lie together in the grid: which XCD a workgroup runs on (its index
+    // modulo 8) then does not depend on its range, and late ranges, which few sequences have,
+    // spread over all XCDs
+    const int64_t units = gridDim.x / ranges;
+    const int rg = (int)(blockIdx.x / units);
+    const int64_t unit = blockIdx.x % units;
     const int ht = (int)(unit % head_tiles);
     const int kvh = (int)(unit / head_tiles % p.c.h_kv);
     const int64_t seq = unit / head_tiles / p.c.h_kv;
     const int G = p.h_q / p.c.h_kv, heads = G - 16 * ht < 16 ? G - 16 * ht : 16;
-    const int64_t cap = p.c.max_pages << page_shift;
+    const int64_t cap = p.c.num_pages > 0 ? p.c.max_pages << page_shift : 0;
     int64_t len = p.lens[seq];
     len = len < p.max_len ? len : p.max_len;
     len = len < cap ? len : cap;
@@ -133,48 +148,64 @@ decode_attn_kernel(AttnDecodeCall p, int64_t range, int ranges, int head_tiles, 
     const char* kpool = static_cast<const char*>(p.c.k);
     const char* vpool = static_cast<const char*>(p.c.v);
 
-    for (int64_t j0 = begin + wave * kStep; j0 < end; j0 += kWaves * kStep) {
-        float s[8];
-        u32x4_t kx[2][C::KL];
-        VP vx[8][C::U];
-        uint32_t sk[2], sv[2];
-        bool there[2];
+    u32x4_t kx[C::NB][C::KL];
+    VP vx[4 * C::NB][C::U];
+    uint32_t sk[C::NB], sv[C::NB];
+
+    // Row of the pools where block b of the step at j0 begins; absent pages read page 0 (and are
+    // masked), positions past the range's end the page of its last.
+    auto block_row = [&](int64_t j0, int b, bool* there) {
+        const int64_t pos = j0 + 16 * b;
+        const int64_t page = table[(pos < end ? pos : end - 1) >> page_shift];
+        *there = page >= 0 && page < p.c.num_pages;
+        return (((*there ? page : 0) * p.c.h_kv + kvh) << page_shift) + (pos & (p.c.page_size - 1));
+    };
+    auto load_k = [&](const int64_t* row) {
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-            const int64_t pos = j0 + 16 * b;
-            int64_t page = -1;
-            if (pos < end) page = table[pos >> page_shift];
-            there[b] = page >= 0 && page < p.c.num_pages;
-            const int64_t row = ((page * p.c.h_kv + kvh) << page_shift) + (pos & (p.c.page_size - 1));
-            if (there[b]) {
-                const char* kr = kpool + (row + c) * (D * C::ES) + g * 16;
+        for (int b = 0; b < C::NB; ++b) {
+            const char* kr = kpool + (row[b] + c) * (D * C::ES) + g * 16;
 #pragma unroll
-                for (int i = 0; i < C::KL; ++i) kx[b][i] = *reinterpret_cast<const u32x4_t*>(kr + i * 64);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const char* vr = vpool + (row + 4 * g + i) * (D * C::ES) + c * (C::EPL * C::ES);
-#pragma unroll
-                    for (int u = 0; u < C::U; ++u)
-                        vx[4 * b + i][u] = *reinterpret_cast<const VP*>(vr + u * (16 * C::EPL * C::ES));
-                }
-                if constexpr (FP8) {
-                    sk[b] = *reinterpret_cast<const uint32_t*>(p.c.k_scale + row + 4 * g);
-                    sv[b] = *reinterpret_cast<const uint32_t*>(p.c.v_scale + row + 4 * g);
-                }
-            } else {
-                sk[b] = sv[b] = 0;
-#pragma unroll
-                for (int i = 0; i < C::KL; ++i) kx[b][i] = u32x4_t{0, 0, 0, 0};
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int u = 0; u < C::U; ++u) vx[4 * b + i][u] = VP{};
-            }
+            for (int i = 0; i < C::KL; ++i) kx[b][i] = *reinterpret_cast<const u32x4_t*>(kr + i * 64);
+            if constexpr (FP8) sk[b] = *reinterpret_cast<const uint32_t*>(p.c.k_scale + row[b] + 4 * g);
         }
+    };
+    auto load_v = [&](const int64_t* row) {
+#pragma unroll
+        for (int b = 0; b < C::NB; ++b) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const char* vr = vpool + (row[b] + 4 * g + i) * (D * C::ES) + c * (C::EPL * C::ES);
+#pragma unroll
+                for (int u = 0; u < C::U; ++u)
+                    vx[4 * b + i][u] = *reinterpret_cast<const VP*>(vr + u * (16 * C::EPL * C::ES));
+            }
+            if constexpr (FP8) sv[b] = *reinterpret_cast<const uint32_t*>(p.c.v_scale + row[b] + 4 * g);
+        }
+    };
+
+    // The next step's K is loaded when this step's scores are done, its V when this step's sum
+    // is: the registers are free then, and a wave always has loads in flight.
+    int64_t row[C::NB];
+    bool there[C::NB];
+    const int64_t first = begin + wave * C::STEP;
+    if (first < end) {
+#pragma unroll
+        for (int b = 0; b < C::NB; ++b) row[b] = block_row(first, b, &there[b]);
+        load_k(row);
+        load_v(row);
+    }
+    for (int64_t j0 = first; j0 < end; j0 += kWaves * C::STEP) {
+        const int64_t next = j0 + kWaves * C::STEP;
+        int64_t nrow[C::NB] = {};
+        bool nthere[C::NB] = {};
+        if (next < end)
+#pragma unroll
+            for (int b = 0; b < C::NB; ++b) nrow[b] = block_row(next, b, &nthere[b]);
 
         // scores
+        float s[4 * C::NB];
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
+        for (int b = 0; b < C::NB; ++b) {
             f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int i = 0; i < C::KL; ++i) {
@@ -207,27 +238,34 @@ decode_attn_kernel(AttnDecodeCall p, int64_t range, int ranges, int head_tiles, 
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                float x = acc[i] * cs;
-                if constexpr (FP8) x *= scale_of((sk[b] >> (8 * i)) & 0xff);
-                const bool seen = there[b] && j0 + 16 * b + 4 * g + i < end;
-                s[4 * b + i] = seen ? x : -INFINITY;
-                // what lies behind the last position is anything: not into the product
-                if (!seen) {
-#pragma unroll
-                    for (int u = 0; u < C::U; ++u) vx[4 * b + i][u] = VP{};
-                    if constexpr (FP8) sv[b] &= ~(0xffu << (8 * i));
-                }
+                s[4 * b + i] = acc[i] * cs;
+                if constexpr (FP8) s[4 * b + i] *= scale_of((sk[b] >> (8 * i)) & 0xff);
             }
         }
+        if (next < end) load_k(nrow);
 
-        // softmax
+        const bool masked = j0 + C::STEP > end || !there[0] || !there[C::NB - 1];
+        if (masked)
+#pragma unroll
+            for (int i = 0; i < 4 * C::NB; ++i)
+                if (!there[i / 4] || j0 + 16 * (i / 4) + 4 * g + i % 4 >= end) {
+                    s[i] = -INFINITY;
+                    // what lies there is anything: not into the product
+#pragma unroll
+                    for (int u = 0; u < C::U; ++u) vx[i][u] = VP{};
+                    if constexpr (FP8) sv[i / 4] &= ~(0xffu << (8 * (i % 4)));
+                }
+
+        // softmax; the reference maximum moves only when weights would pass 2^8
         float mx = s[0];
 #pragma unroll
-        for (int i = 1; i < 8; ++i) mx = fmaxf(mx, s[i]);
-        mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
-        mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
-        if (__any(mx > m)) {
-            const float mn = fmaxf(m, mx);
+        for (int i = 1; i < 4 * C::NB; ++i) mx = fmaxf(mx, s[i]);
+        if (__any(mx > m && (m == -INFINITY || mx > m + 8.f))) {
+            const auto a16 = __builtin_amdgcn_permlane16_swap(__float_as_uint(mx), __float_as_uint(mx), false, false);
+            mx = fmaxf(__uint_as_float(a16[0]), __uint_as_float(a16[1]));
+            const auto a32 = __builtin_amdgcn_permlane32_swap(__float_as_uint(mx), __float_as_uint(mx), false, false);
+            mx = fmaxf(__uint_as_float(a32[0]), __uint_as_float(a32[1]));
+            const float mn = fmaxf(m, mx);  // the same in all lanes of a head
             const float a = mn == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m - mn);
             m = mn;
             l *= a;
@@ -236,7 +274,7 @@ decode_attn_kernel(AttnDecodeCall p, int64_t range, int ranges, int head_tiles, 
         }
         const float ref = m == -INFINITY ? 0.f : m;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < 4 * C::NB; ++i) {
             s[i] = __builtin_amdgcn_exp2f(s[i] - ref);
             l += s[i];
             if constexpr (FP8) s[i] *= scale_of((sv[i / 4] >> (8 * (i % 4))) & 0xff);
@@ -277,7 +315,7 @@ decode_attn_kernel(AttnDecodeCall p, int64_t range, int ranges, int head_tiles, 
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
+            for (int i = 0; i < 4 * C::NB; ++i)
 #pragma unroll
                 for (int u = 0; u < C::U; ++u)
 #pragma unroll
@@ -289,9 +327,12 @@ decode_attn_kernel(AttnDecodeCall p, int64_t range, int ranges, int head_tiles, 
                         o[u * C::EPL + j] = __builtin_amdgcn_mfma_f32_16x16x4f32(a, s[i], o[u * C::EPL + j], 0, 0, 0);
                     }
         }
+        if (next < end) load_v(nrow);
+#pragma unroll
+        for (int b = 0; b < C::NB; ++b) there[b] = nthere[b];
     }
 
-    // join the waves
+    // join the waves: weights relative to the largest maximum
     l += __shfl_xor(l, 16, 64);
     l += __shfl_xor(l, 32, 64);
     if (g == 0) {
@@ -303,13 +344,15 @@ decode_attn_kernel(AttnDecodeCall p, int64_t range, int ranges, int head_tiles, 
 #pragma unroll
     for (int x = 1; x < kWaves; ++x) mm = fmaxf(mm, s_m[x][c]);
     const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - mm);
+    if (c < heads) {
 #pragma unroll
-    for (int u = 0; u < C::U; ++u)
+        for (int u = 0; u < C::U; ++u)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int j = 0; j < C::EPL; ++j)
-                s_o[wave][c][16 * C::EPL * u + C::EPL * (4 * g + i) + j] = m == -INFINITY ? 0.f : o[u * C::EPL + j][i] * f;
+                for (int j = 0; j < C::EPL; ++j)
+                    s_o[wave][c][16 * C::EPL * u + C::EPL * (4 * g + i) + j] = m == -INFINITY ? 0.f : o[u * C::EPL + j][i] * f;
+    }
     __syncthreads();
     for (int x = threadIdx.x; x < heads * (D / 4); x += 64 * kWaves) {
         const int hd = x / (D / 4), el = x % (D / 4) * 4;
@@ -319,18 +362,18 @@ decode_attn_kernel(AttnDecodeCall p, int64_t range, int ranges, int head_tiles, 
         f32x4_t sum = {0.f, 0.f, 0.f, 0.f};
         float ls = 0.f;
 #pragma unroll
-        for (int y = 0; y < kWaves; ++y) {
-            sum += *reinterpret_cast<const f32x4_t*>(&s_o[y][hd][el]);
+        for (int y = 0; y < kWaves; ++y) sum += *reinterpret_cast<const f32x4_t*>(&s_o[y][hd][el]);
+#pragma unroll
+        for (int y = 0; y < kWaves; ++y)
             if (s_m[y][hd] != -INFINITY) ls += s_l[y][hd] * __builtin_amdgcn_exp2f(s_m[y][hd] - top);
-        }
         if (ranges == 1) {
-            const int64_t row = seq * p.h_q + kvh * G + 16 * ht + hd;
+            const int64_t orow = seq * p.h_q + kvh * G + 16 * ht + hd;
             const float inv = ls > 0.f ? 1.f / ls : (ls == ls ? 0.f : ls);
             sum *= inv;
-            T* out = static_cast<T*>(p.out) + row * D + el;
+            T* out = static_cast<T*>(p.out) + orow * D + el;
             if constexpr (BF) *reinterpret_cast<u32x2_t*>(out) = u32x2_t{pack_bf16(sum[0], sum[1]), pack_bf16(sum[2], sum[3])};
             else *reinterpret_cast<f32x4_t*>(out) = sum;
-            if (p.lse && el == 0) p.lse[row] = ls > 0.f ? (top + __builtin_amdgcn_logf(ls)) * kLn2 : (ls == ls ? -INFINITY : ls);
+            if (p.lse && el == 0) p.lse[orow] = ls > 0.f ? (top + __builtin_amdgcn_logf(ls)) * kLn2 : (ls == ls ? -INFINITY : ls);
         } else {
             const int64_t at = (unit * ranges + rg) * 16 + hd;
             *reinterpret_cast<f32x4_t*>(part.o + at * D + el) = sum;
@@ -339,59 +382,73 @@ decode_attn_kernel(AttnDecodeCall p, int64_t range, int ranges, int head_tiles, 
     }
 }
 
-// Joins the ranges of one (sequence, head): the rows' sums weighted by exp2(m - max m).
-template <typename T, int D>
-__global__ void __launch_bounds__(256) decode_join_kernel(AttnDecodeCall p, int64_t range, int ranges,
-                                                          int head_tiles, int page_shift, Partials part)
+// Joins the ranges of one (sequence, head), 64 elements of it: the ranges' sums weighted by
+// exp2(m - max m). 16 lanes hold the elements, the blockDim / 16 groups of them take the ranges
+// in turn (few ranges need few groups: see join_threads); the order of the additions depends on
+// the sizes only.
+constexpr int kJoinGroups = 64;  // at most
+
+int join_threads(int64_t ranges)
 {
-    constexpr int TPR = D / 4, RPB = 256 / TPR;  // threads per row, ranges at a time
-    __shared__ f32x4_t s_o[RPB][TPR];
-    __shared__ float s_l[RPB];
-    const int64_t seq = blockIdx.x / p.h_q;
-    const int hq = (int)(blockIdx.x - seq * p.h_q);
+    const int64_t t = (ranges + 3) / 4 * 16;  // about four ranges a group
+    return t < 64 ? 64 : t > 16 * kJoinGroups ? 16 * kJoinGroups : (int)((t + 63) / 64 * 64);
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(16 * kJoinGroups) decode_join_kernel(AttnDecodeCall p, int64_t range,
+                                                                       int ranges, int head_tiles,
+                                                                       int page_shift, Partials part)
+{
+    __shared__ f32x4_t s_o[kJoinGroups][16];
+    __shared__ float s_l[kJoinGroups], s_m[kJoinGroups / 4];
+    const int groups = blockDim.x / 16;
+    const int64_t hrow = blockIdx.x / (D / 64);
+    const int64_t seq = hrow / p.h_q;
+    const int hq = (int)(hrow - seq * p.h_q);
     const int G = p.h_q / p.c.h_kv, kvh = hq / G, hg = hq - kvh * G, ht = hg / 16, hd = hg % 16;
-    const int64_t cap = p.c.max_pages << page_shift;
+    const int64_t cap = p.c.num_pages > 0 ? p.c.max_pages << page_shift : 0;
     int64_t len = p.lens[seq];
     len = len < p.max_len ? len : p.max_len;
     len = len < cap ? len : cap;
     const int used = len <= 0 ? 0 : (int)((len + range - 1) / range);
     const int64_t unit = (seq * p.c.h_kv + kvh) * head_tiles + ht;
     const float2* ml = part.ml + unit * ranges * 16 + hd;
-    const float* po = part.o + (unit * ranges * 16 + hd) * D;
+    const int y = threadIdx.x / 16, el = (int)(blockIdx.x % (D / 64)) * 64 + threadIdx.x % 16 * 4;
+    const float* po = part.o + (unit * ranges * 16 + hd) * D + el;
 
-    const int lane = threadIdx.x & 63;
     float top = -INFINITY;
-    for (int x = lane; x < used; x += 64) top = fmaxf(top, ml[(int64_t)x * 16].x);
+    for (int x = threadIdx.x; x < used; x += blockDim.x) top = fmaxf(top, ml[(int64_t)x * 16].x);
 #pragma unroll
     for (int off = 32; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, 64));
+    if (threadIdx.x % 64 == 0) s_m[threadIdx.x / 64] = top;
+    __syncthreads();
+    for (int x = 0; x < (int)blockDim.x / 64; ++x) top = fmaxf(top, s_m[x]);
 
-    const int y = threadIdx.x / TPR, el = threadIdx.x % TPR * 4;
     f32x4_t sum = {0.f, 0.f, 0.f, 0.f};
     float ls = 0.f;
-    for (int x = y; x < used; x += RPB) {
+#pragma unroll 4
+    for (int x = y; x < used; x += groups) {
         const float2 v = ml[(int64_t)x * 16];
-        if (v.x == -INFINITY) continue;
-        const float f = __builtin_amdgcn_exp2f(v.x - top);
+        const f32x4_t a = *reinterpret_cast<const f32x4_t*>(po + (int64_t)x * 16 * D);
+        const float f = v.x == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(v.x - top);
         ls += v.y * f;
-        sum += *reinterpret_cast<const f32x4_t*>(po + (int64_t)x * 16 * D + el) * f;
+        sum += a * f;
     }
-    s_o[y][el / 4] = sum;
-    if (el == 0) s_l[y] = ls;
+    s_o[y][threadIdx.x % 16] = sum;
+    if (threadIdx.x % 16 == 0) s_l[y] = ls;
     __syncthreads();
     if (y != 0) return;
     float l = 0.f;
     f32x4_t o = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int x = 0; x < RPB; ++x) {
-        o += s_o[x][el / 4];
+    for (int x = 0; x < groups; ++x) {
+        o += s_o[x][threadIdx.x];
         l += s_l[x];
     }
-    const int64_t row = seq * p.h_q + hq;
     o *= l > 0.f ? 1.f / l : (l == l ? 0.f : l);
-    T* out = static_cast<T*>(p.out) + row * D + el;
+    T* out = static_cast<T*>(p.out) + hrow * D + el;
     if constexpr (sizeof(T) == 2) *reinterpret_cast<u32x2_t*>(out) = u32x2_t{pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3])};
     else *reinterpret_cast<f32x4_t*>(out) = o;
-    if (p.lse && el == 0) p.lse[row] = l > 0.f ? (top + __builtin_amdgcn_logf(l)) * kLn2 : (l == l ? -INFINITY : l);
+    if (p.lse && el == 0) p.lse[hrow] = l > 0.f ? (top + __builtin_amdgcn_logf(l)) * kLn2 : (l == l ? -INFINITY : l);
 }
 
 template <typename T, bool FP8, int D>
@@ -407,7 +464,7 @@ hipError_t launch_t(const AttnDecodeCall& c)
                        c.stream, c, pl.range, (int)pl.ranges, pl.head_tiles, shift, part);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || pl.ranges == 1) return e;
-    hipLaunchKernelGGL((decode_join_kernel<T, D>), dim3((unsigned)(c.c.n * c.h_q)), dim3(256), 0, c.stream, c,
+    hipLaunchKernelGGL((decode_join_kernel<T, D>), dim3((unsigned)(c.c.n * c.h_q * (D / 64))), dim3(join_threads(pl.ranges)), 0, c.stream, c,
                        pl.range, (int)pl.ranges, pl.head_tiles, shift, part);
     return hipGetLastError();
 }
