@@ -476,23 +476,28 @@ class DecodeGraph:
 
 # ---------------------------------------------------------------- attention layers
 
+# These calls are short (a few microseconds of GPU work at a decode step), so their checks are
+# written to cost little: a tensor's pointer comes out of the same function that checks it.
+
 _POOLS = {torch.float32: GDN_F32, torch.bfloat16: GDN_BF16, torch.float8_e4m3fn: GDN_FP8}
-_i32 = torch.int32
+_Tensor, _i32, _u8 = torch.Tensor, torch.int32, torch.uint8
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") \
+    else lambda index: torch.cuda.current_stream(index).cuda_stream
 
 
 def _rows(name, x, dtype, dev):
     """(pointer, token stride, head stride) of a [tokens, heads, d] tensor with contiguous d. The
     stride of a dimension of one entry means nothing to torch: a dense one stands for it."""
-    if not isinstance(x, torch.Tensor) or x.dim() != 3:
+    if not isinstance(x, _Tensor) or x.dim() != 3:
         raise ValueError(f"{name} must be a torch tensor [tokens, heads, d]")
     if x.device != dev or not x.is_cuda:
         raise ValueError(f"{name} must be a CUDA (HIP) tensor on {dev}")
     if x.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {x.dtype}")
-    t, h, d = x.shape
     st, sh, sd = x.stride()
-    if sd != 1 and d > 1:
+    if sd != 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
+    t, h, d = x.shape
     if h == 1:
         sh = d
     if t <= 1:
@@ -500,42 +505,42 @@ def _rows(name, x, dtype, dev):
     return x.data_ptr(), st, sh
 
 
-def _index(name, x, shape, dev):
-    """A contiguous int32 tensor of this shape on dev, or None."""
-    if x is None:
-        return None
-    if not isinstance(x, torch.Tensor) or x.dtype != _i32 or x.device != dev or x.shape != shape \
-            or not x.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int32 tensor {tuple(shape)} on {dev}")
-    return x.data_ptr()
-
-
 def _dense(name, x, shape, dtype, dev):
-    if not isinstance(x, torch.Tensor) or x.dtype != dtype or x.device != dev or x.shape != shape \
+    """Pointer of a contiguous tensor of this shape and dtype on dev."""
+    if not isinstance(x, _Tensor) or x.dtype != dtype or x.shape != shape or x.device != dev \
             or not x.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)} on {dev}")
     return x.data_ptr()
 
 
-def _cache_of(k_cache, v_cache, page_table, k_scale, v_scale) -> KvCache:
-    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4 or not k_cache.is_cuda:
+def _index(name, x, shape, dev):
+    """Pointer of an int32 tensor, or None."""
+    return None if x is None else _dense(name, x, shape, _i32, dev)
+
+
+def _cache_of(k_cache, v_cache, page_table, k_scale, v_scale):
+    """(gdn_kv_cache, device) of the pools and the page table."""
+    if not isinstance(k_cache, _Tensor) or not k_cache.is_cuda or k_cache.dim() != 4:
         raise ValueError("k_cache must be a CUDA (HIP) tensor [num_pages, h_kv, page_size, d]")
-    store = _POOLS.get(k_cache.dtype)
+    dtype, dev, shape = k_cache.dtype, k_cache.device, k_cache.shape
+    store = _POOLS.get(dtype)
     if store is None:
         raise ValueError("the cache must be bfloat16, float32 or float8_e4m3fn")
-    dev, shape = k_cache.device, k_cache.shape
     pages, h, size, d = shape
-    k = _dense("k_cache", k_cache, shape, k_cache.dtype, dev)
-    v = _dense("v_cache", v_cache, shape, k_cache.dtype, dev)
     ks = vs = None
     if store == GDN_FP8:
-        ks = _dense("k_scale", k_scale, (pages, h, size), torch.uint8, dev)
-        vs = _dense("v_scale", v_scale, (pages, h, size), torch.uint8, dev)
-    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+        ks = _dense("k_scale", k_scale, (pages, h, size), _u8, dev)
+        vs = _dense("v_scale", v_scale, (pages, h, size), _u8, dev)
+    if not isinstance(page_table, _Tensor) or page_table.dim() != 2:
         raise ValueError("page_table must be an int32 tensor [n, max_pages]")
     n, width = page_table.shape
-    table = _index("page_table", page_table, page_table.shape, dev)
-    return KvCache(n, pages, width, size, h, d, store, k, v, ks, vs, table)
+    return KvCache(n, pages, width, size, h, d, store, _dense("k_cache", k_cache, shape, dtype, dev),
+                   _dense("v_cache", v_cache, shape, dtype, dev), ks, vs,
+                   _dense("page_table", page_table, (n, width), _i32, dev)), dev
+
+
+def _queue(dev, stream):
+    return _raw_stream(dev.index) if stream is None else stream.cuda_stream
 
 
 def _dtype_id(x):
@@ -557,8 +562,7 @@ def gdn_kv_write(k, v, k_cache, v_cache, page_table, start, cu_seqlens=None, *, 
     page_table int32 [n, max_pages]; a page id of -1 is a page that is not there, and what
     would go there is dropped. Updates the cache in place; returns nothing."""
     t = _dtype_id(k)
-    c = _cache_of(k_cache, v_cache, page_table, k_scale, v_scale)
-    dev = k_cache.device
+    c, dev = _cache_of(k_cache, v_cache, page_table, k_scale, v_scale)
     kp, kt, kh = _rows("k", k, k.dtype, dev)
     vp, vt, vh = _rows("v", v, k.dtype, dev)
     total = k.shape[0]
@@ -567,7 +571,7 @@ def gdn_kv_write(k, v, k_cache, v_cache, page_table, start, cu_seqlens=None, *, 
     sp = _index("start", start, (c.n,), dev)
     cp = _index("cu_seqlens", cu_seqlens, (c.n + 1,), dev)
     st = _load().gdn_kv_write(ctypes.byref(c), total, t, kp, kt, kh, vp, vt, vh, sp, cp,
-                              _stream(dev, stream))
+                              _queue(dev, stream))
     if st:
         raise GdnError(st, "gdn_kv_write")
 
@@ -581,8 +585,7 @@ def gdn_kv_read(k_cache, v_cache, page_table, start, cu_seqlens, total, *, dtype
     t = _DTYPES.get(dtype)
     if t is None:
         raise ValueError("dtype must be bfloat16 or float32")
-    c = _cache_of(k_cache, v_cache, page_table, k_scale, v_scale)
-    dev = k_cache.device
+    c, dev = _cache_of(k_cache, v_cache, page_table, k_scale, v_scale)
     shape = (int(total), c.h_kv, c.d)
     if k_out is None:
         k_out = torch.empty(shape, dtype=dtype, device=dev)
@@ -591,7 +594,7 @@ def gdn_kv_read(k_cache, v_cache, page_table, start, cu_seqlens, total, *, dtype
     st = _load().gdn_kv_read(
         ctypes.byref(c), shape[0], t, _dense("k_out", k_out, shape, dtype, dev),
         _dense("v_out", v_out, shape, dtype, dev), _index("start", start, (c.n,), dev),
-        _index("cu_seqlens", cu_seqlens, (c.n + 1,), dev), _stream(dev, stream))
+        _index("cu_seqlens", cu_seqlens, (c.n + 1,), dev), _queue(dev, stream))
     if st:
         raise GdnError(st, "gdn_kv_read")
     return k_out, v_out
@@ -620,7 +623,7 @@ def gdn_attn_prefill(q, k, v, cu_q, cu_k=None, *, causal=True, scale=None, out=N
     if n < 0:
         raise ValueError("cu_q must be an int32 tensor [n + 1]")
     if out is None:
-        out = torch.empty((tq, hq, d), dtype=q.dtype, device=dev)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
         op = out.data_ptr()
     else:
         op = _dense("out", out, (tq, hq, d), q.dtype, dev)
@@ -628,7 +631,7 @@ def gdn_attn_prefill(q, k, v, cu_q, cu_k=None, *, causal=True, scale=None, out=N
     dims = AttnDims(n, tq, tk, hq, hk, d, t, 1 if causal else 0, d ** -0.5 if scale is None else scale,
                     qt, qh, kt, kh, vt, vh)
     st = _load().gdn_attn_prefill(ctypes.byref(dims), qp, kp, vp, _index("cu_q", cu_q, (n + 1,), dev),
-                                  _index("cu_k", cu_k, (n + 1,), dev), op, lp, _stream(dev, stream))
+                                  _index("cu_k", cu_k, (n + 1,), dev), op, lp, _queue(dev, stream))
     if st:
         raise GdnError(st, "gdn_attn_prefill")
     return out
@@ -652,8 +655,7 @@ def gdn_attn_decode(q, k_cache, v_cache, page_table, lens, *, max_len=None, k_sc
     as for gdn_kv_write. scale defaults to 1 / sqrt(d); lse as for gdn_attn_prefill, [n, h_q].
     Returns out [n, h_q, d] of q's dtype."""
     t = _dtype_id(q)
-    c = _cache_of(k_cache, v_cache, page_table, k_scale, v_scale)
-    dev = k_cache.device
+    c, dev = _cache_of(k_cache, v_cache, page_table, k_scale, v_scale)
     qp, qt, qh = _rows("q", q, q.dtype, dev)
     n, hq, d = q.shape
     if n != c.n or d != c.d:
@@ -661,7 +663,7 @@ def gdn_attn_decode(q, k_cache, v_cache, page_table, lens, *, max_len=None, k_sc
     if max_len is None:
         max_len = c.max_pages * c.page_size
     if out is None:
-        out = torch.empty((n, hq, d), dtype=q.dtype, device=dev)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
         op = out.data_ptr()
     else:
         op = _dense("out", out, (n, hq, d), q.dtype, dev)
@@ -671,11 +673,11 @@ def gdn_attn_decode(q, k_cache, v_cache, page_table, lens, *, max_len=None, k_sc
         need = lib.gdn_attn_decode_workspace_bytes(ctypes.byref(c), hq, max_len)
         if need:
             workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    wbytes = _check_workspace(workspace, dev)
+    wbytes = 0 if workspace is None else _check_workspace(workspace, dev)
     st = lib.gdn_attn_decode(
         ctypes.byref(c), hq, t, d ** -0.5 if scale is None else scale, max_len, qp, qt, qh,
         _index("lens", lens, (n,), dev), op, lp, None if workspace is None else workspace.data_ptr(),
-        wbytes, _stream(dev, stream))
+        wbytes, _queue(dev, stream))
     if st:
         raise GdnError(st, "gdn_attn_decode")
     return out
