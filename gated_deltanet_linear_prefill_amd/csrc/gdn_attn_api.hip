@@ -205,8 +205,9 @@ gdn_status gdn_attn_prefill(const gdn_attn_dims* d, const void* q, const void* k
     if (!attn_dtype(d->dtype) || !attn_d(d->d)) return GDN_ERR_UNSUPPORTED;
     const int64_t lim = INT64_C(1) << 31;
     int64_t rows, qe, ke, ve;
-    if (d->n >= lim || d->total_q >= lim || d->total_k >= lim) return GDN_ERR_SHAPE;
-    if (!mul_ok(d->total_q, d->h_q, &rows) || rows >= (INT64_C(1) << 40)) return GDN_ERR_SHAPE;
+    const int64_t rows_lim = lim - (1 << 16);  // the kernels count rows and keys in 32 bits
+    if (d->n >= lim || d->total_q >= rows_lim || d->total_k >= rows_lim) return GDN_ERR_SHAPE;
+    if (!mul_ok(d->total_q, d->h_q, &rows) || rows / d->h_kv >= rows_lim) return GDN_ERR_SHAPE;
     // the grid: (tiles of query rows) x (KV heads), see the kernel
     if ((rows / d->h_kv / attn_prefill_rows(d->d, d->dtype) + d->n) * d->h_kv >= lim) return GDN_ERR_SHAPE;
     if (!strided(d->total_q, d->h_q, d->d, d->q_token, d->q_head, d->dtype, &qe) ||

@@ -7,7 +7,7 @@
 //
 // Grid. The host does not know the sequences' lengths. Sequence s gets the tiles
 // [floor(cu_q[s] G / M) + s, floor(cu_q[s + 1] G / M) + s + 1), which are disjoint, in order
-// and enough for its ceil(len G / M); a workgroup finds its sequence by bisection and leaves
+// and enough for its ceil(len G / M); a workgroup looks its sequence up in them and leaves
 // if its tile is past the end. Tiles are taken last first within a sequence: under a causal
 // mask the last are the longest.
 //
@@ -55,56 +55,57 @@ struct Tile<float, D> {
     static constexpr int N = 32, M = 32 * kWaves;
 };
 
-// A workgroup's tile: its sequence, rows and key count.
+// A workgroup's tile: its sequence's rows and keys, and its own first row. The host keeps
+// rows and keys below 2^31 - 2^16.
 struct Work {
-    int64_t q0, k0;     // first packed rows of the sequence
-    int64_t len_q, len_k;
-    int64_t row0, rows; // first packed (position, head) row, and how many the sequence has
-    int head;           // KV head
+    int64_t q0, k0;    // first packed rows of the sequence
+    int len_q, len_k;
+    int row0, rows;    // first (position, head) row of the tile; how many the sequence has
+    int g, head;       // heads of the group; KV head
 };
 
-__device__ __forceinline__ int64_t clamp64(int64_t x, int64_t hi)
+__device__ __forceinline__ int clamp_to(int x, int hi)
 {
     return x < 0 ? 0 : (x > hi ? hi : x);
 }
 
-// floor(cu[s] G / M) + s, the first tile of sequence s
-__device__ __forceinline__ int64_t tile_base(const int32_t* cu, int64_t s, int64_t total, int g, int m)
-{
-    return clamp64(cu[s], total) * g / m + s;
-}
-
+// The workgroup's work, or false if there is none. floor(cu[s] G / M) + s, the first tile of
+// sequence s, is looked for 64 sequences at a time, one a lane.
 template <int M>
-__device__ __forceinline__ bool find_work(const AttnCall& p, int64_t tile, int head, Work* w)
+__device__ __forceinline__ bool find_work(const AttnCall& p, int tile, int head, int lane, Work* w)
 {
     const gdn_attn_dims& d = p.d;
-    const int g = d.h_q / d.h_kv;
-    int64_t lo = 0, hi = d.n;
-    while (hi - lo > 1) {
-        const int64_t mid = (lo + hi) >> 1;
-        if (tile_base(p.cu_q, mid, d.total_q, g, M) <= tile) lo = mid; else hi = mid;
+    const int g = d.h_q / d.h_kv, n = (int)d.n, total_q = (int)d.total_q, total_k = (int)d.total_k;
+    auto base = [&](int s) { return (int)((int64_t)clamp_to(p.cu_q[s], total_q) * g / M) + s; };
+    int s = 0;
+    for (int span = n; span > 1;) {  // the sequence is in [s, s + span)
+        const int step = (span + 63) / 64, at = s + lane * step;
+        const bool before = lane * step < span && (lane == 0 || base(at) <= tile);
+        const int x = 63 - __builtin_clzll(__ballot(before) | 1);  // the last lane not past the tile
+        s += x * step;
+        span = span - x * step < step ? span - x * step : step;
     }
-    const int64_t qa = clamp64(p.cu_q[lo], d.total_q), qb = clamp64(p.cu_q[lo + 1], d.total_q);
-    const int64_t ka = clamp64(p.cu_k[lo], d.total_k), kb = clamp64(p.cu_k[lo + 1], d.total_k);
+    s = __builtin_amdgcn_readfirstlane(s);
+    const int qa = clamp_to(p.cu_q[s], total_q), qb = clamp_to(p.cu_q[s + 1], total_q);
+    const int ka = clamp_to(p.cu_k[s], total_k), kb = clamp_to(p.cu_k[s + 1], total_k);
     w->q0 = qa;
     w->k0 = ka;
     w->len_q = qb - qa;
     w->len_k = kb > ka ? kb - ka : 0;
     w->rows = w->len_q * g;
+    w->g = g;
     w->head = head;
     if (w->len_q <= 0) return false;
-    const int64_t tiles = (w->rows + M - 1) / M, local = tile - tile_base(p.cu_q, lo, d.total_q, g, M);
+    const int tiles = (w->rows + M - 1) / M, local = tile - ((int)((int64_t)qa * g / M) + s);
     if (local < 0 || local >= tiles) return false;
     w->row0 = (tiles - 1 - local) * M;
     return true;
 }
 
 // Keys that a query row at position pos sees: [0, limit).
-__device__ __forceinline__ int64_t key_limit(const Work& w, int64_t pos, int causal)
+__device__ __forceinline__ int key_limit(const Work& w, int pos, int causal)
 {
-    if (!causal) return w.len_k;
-    const int64_t lim = pos + 1 + w.len_k - w.len_q;
-    return lim < 0 ? 0 : (lim > w.len_k ? w.len_k : lim);
+    return causal ? clamp_to(pos + 1 + w.len_k - w.len_q, w.len_k) : w.len_k;
 }
 
 __device__ __forceinline__ float other_half_max(float x)
@@ -150,15 +151,15 @@ __device__ __forceinline__ void stage_f32(const char* base, int64_t row, int64_t
 // bytes; zeros from `valid` rows on. `off` is this lane's byte offset within a group's rows in
 // memory.
 template <int D, int GROUP>
-__device__ __forceinline__ void stage(const char* base, int64_t row, int64_t valid, int64_t stride,
+__device__ __forceinline__ void stage(const char* base, int row, int valid, int64_t stride,
                                       char* lds, int wave, int off)
 {
     using C = Tile<uint16_t, D>;
 #pragma unroll
     for (int i = 0; i < 32 / C::WAVES; ++i) {
         const int x = i * C::WAVES + wave;
-        const int64_t first = row + x * C::ROWS;
-        const int64_t left = valid - first, have = left < C::ROWS ? left : C::ROWS;
+        const int first = row + x * C::ROWS;
+        const int left = valid - first, have = left < C::ROWS ? left : C::ROWS;
         const __amdgpu_buffer_rsrc_t r =
             make_rsrc(base + first * stride, have <= 0 ? 0 : (have - 1) * stride + C::ROWB);
         load_to_lds(r, lds + x * GROUP, off);
@@ -225,13 +226,13 @@ __device__ __forceinline__ void softmax_step(float* s, f32x16_t (&o)[ND], Stats*
 
 // Writes a row's output: this lane's 4-element pieces of O^T, divided by the sum.
 template <typename T, int D>
-__device__ __forceinline__ void write_row(const AttnCall& p, const Work& w, int64_t r, int lane,
+__device__ __forceinline__ void write_row(const AttnCall& p, const Work& w, int r, int lane,
                                           const f32x16_t* o, const Stats& st)
 {
-    const int g = p.d.h_q / p.d.h_kv;
     const float l = other_half_sum(st.l), e = other_half_sum(st.exact);
     if (r >= w.rows) return;
-    const int64_t pos = r / g, row = (w.q0 + pos) * p.d.h_q + (int64_t)w.head * g + (r - pos * g);
+    const int pos = (int)((uint32_t)r / (uint32_t)w.g);
+    const int64_t row = (w.q0 + pos) * p.d.h_q + w.head * w.g + (r - pos * w.g);
     const float inv = l > 0.f ? 1.f / l : (l == l ? 0.f : l);
     T* out = static_cast<T*>(p.out) + row * D + 4 * (lane >> 5);
 #pragma unroll
@@ -395,32 +396,7 @@ __global__ void __launch_bounds__(64 * kBf16Waves, 2) prefill_bf16_kernel(AttnCa
     const int half = lane >> 5;
     const int rw = wave % (C::WAVES / SPLIT), turn = wave / (C::WAVES / SPLIT);  // 32 rows, steps
     Work w;
-    if (!find_work<M>(p, blockIdx.x / p.d.h_kv, blockIdx.x % p.d.h_kv, &w)) return;
-    const int g = p.d.h_q / p.d.h_kv;
-
-    // this lane's query: row r of the sequence's packed rows
-    const int64_t r = w.row0 + 32 * rw + (lane & 31);
-    const int64_t rc = r < w.rows ? r : w.rows - 1, pos = rc / g;
-    const uint16_t* qp = static_cast<const uint16_t*>(p.q) + (w.q0 + pos) * p.d.q_token +
-                         ((int64_t)w.head * g + (rc - pos * g)) * p.d.q_head + 8 * half;
-    // A negative scale becomes a positive one of the negated query: the maximum of the raw scores
-    // is then that of the scaled ones. Zero becomes so small a one that every weight is 1, and
-    // a masked score, -infinity, stays so.
-    const uint32_t flip = p.d.scale < 0.f ? 0x80008000u : 0u;
-    const float c = fmaxf(fabsf(p.d.scale) * kLog2e, 1e-37f);
-    bf16x8_t q[D / 16];
-#pragma unroll
-    for (int kk = 0; kk < D / 16; ++kk)
-        q[kk] = __builtin_bit_cast(bf16x8_t, *reinterpret_cast<const u32x4_t*>(qp + 16 * kk) ^ flip);
-
-    // keys that the workgroup's last row sees, and all of its rows; that all of the wave's rows see,
-    // and its last; and this lane's
-    const int64_t last = w.rows - 1, wfirst = w.row0 + 32 * rw;
-    const int64_t keys = key_limit(w, (w.row0 + M - 1 < last ? w.row0 + M - 1 : last) / g, p.d.causal);
-    const int64_t all = key_limit(w, w.row0 / g, p.d.causal);
-    const int64_t wall = key_limit(w, (wfirst < last ? wfirst : last) / g, p.d.causal);
-    const int64_t wkeys = wfirst > last ? 0 : key_limit(w, (wfirst + 31 < last ? wfirst + 31 : last) / g, p.d.causal);
-    const int limit = (int)key_limit(w, pos, p.d.causal);
+    if (!find_work<M>(p, blockIdx.x / p.d.h_kv, blockIdx.x % p.d.h_kv, lane, &w)) return;
 
     const int64_t ks = 2 * p.d.k_token, vs = 2 * p.d.v_token;
     const char* kb = static_cast<const char*>(p.k) + w.k0 * ks + 2 * w.head * p.d.k_head;
@@ -431,20 +407,45 @@ __global__ void __launch_bounds__(64 * kBf16Waves, 2) prefill_bf16_kernel(AttnCa
     // 16 lanes cover groups 4 half + 0..3, 16 elements of each, the next 16 lanes the next 16
     const int klane = (lane & 15) * C::KG + ((lane >> 4) & 1) * C::ROWB + half * 16;
     const int vlane = (4 * half + ((lane >> 2) & 3)) * C::VG + ((lane >> 4) & 1) * 32 + (lane & 3) * 8;
-
-    f32x16_t o[ND];
-    Stats st;
-    auto fetch = [&](int64_t row, char* sk, char* sv) __attribute__((always_inline)) {
+    auto fetch = [&](int row, char* sk, char* sv) __attribute__((always_inline)) {
         stage<D, C::KG>(kb, row, w.len_k, ks, sk, wave, koff);
         stage<D, C::VG>(vb, row, w.len_k, vs, sv, wave, voff);
     };
+
+    // keys that a row sees: the workgroup's last row and all of its rows; the last of the wave's
+    // and all of the wave's; this lane's
+    auto limit_of = [&](int row) {
+        return key_limit(w, (int)((uint32_t)(row < w.rows ? row : w.rows - 1) / (uint32_t)w.g), p.d.causal);
+    };
+    const int wfirst = w.row0 + 32 * rw;
+    const int keys = limit_of(w.row0 + M - 1), all = limit_of(w.row0);
+    if (keys > 0) fetch(0, s_k0, s_v0);
+    const int wkeys = wfirst < w.rows ? limit_of(wfirst + 31) : 0, wall = limit_of(wfirst);
+
+    // this lane's query: row r of the sequence's packed rows
+    const int r = wfirst + (lane & 31), rc = r < w.rows ? r : w.rows - 1, pos = (int)((uint32_t)rc / (uint32_t)w.g);
+    const int limit = key_limit(w, pos, p.d.causal);
+    const uint16_t* qp = static_cast<const uint16_t*>(p.q) + (w.q0 + pos) * p.d.q_token +
+                         (w.head * w.g + (rc - pos * w.g)) * p.d.q_head + 8 * half;
+    // A negative scale becomes a positive one of the negated query: the maximum of the raw scores
+    // is then that of the scaled ones. Zero becomes so small a one that every weight is 1, and
+    // a masked score, -infinity, stays so.
+    const uint32_t flip = p.d.scale < 0.f ? 0x80008000u : 0u;
+    const float c = fmaxf(fabsf(p.d.scale) * kLog2e, 1e-37f);
+    bf16x8_t q[D / 16];
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk)
+        q[kk] = __builtin_bit_cast(bf16x8_t, *reinterpret_cast<const u32x4_t*>(qp + 16 * kk) ^ flip);
+
+    f32x16_t o[ND];
+    Stats st;
     bool odd = false;
-    auto step = [&](auto mode, const char* sk, const char* sv, int64_t j0) __attribute__((always_inline)) {
+    auto step = [&](auto mode, const char* sk, const char* sv, int j0) __attribute__((always_inline)) {
         constexpr int MODE = decltype(mode)::value;
         if (MODE != kPlain && j0 >= wkeys) return;  // nothing there for this wave's rows
-        bf16_step<D, LSE, MODE>(sk, sv, klane, vlane, q, o, st, c, j0 + N > wall, limit - (int)j0, lane, odd);
+        bf16_step<D, LSE, MODE>(sk, sv, klane, vlane, q, o, st, c, j0 + N > wall, limit - j0, lane, odd);
     };
-    auto pair = [&](auto mode, const char* sk, const char* sv, int64_t j0) __attribute__((always_inline)) {
+    auto pair = [&](auto mode, const char* sk, const char* sv, int j0) __attribute__((always_inline)) {
         if constexpr (SPLIT == 1) {
 #pragma unroll 1
             for (int t = 0; t < 2; ++t) step(mode, sk + t * 16 * C::KG, sv + t * 16 * C::VG, j0 + t * N);
@@ -454,7 +455,7 @@ __global__ void __launch_bounds__(64 * kBf16Waves, 2) prefill_bf16_kernel(AttnCa
     };
     // Two buffers: while a pair of steps is used the next one arrives. The barrier before a pair
     // has every wave's loads of it done, and every wave past the buffer that is refilled next.
-    auto run = [&](auto mode, int64_t j0) __attribute__((always_inline)) {
+    auto run = [&](auto mode, int j0) __attribute__((always_inline)) {
         for (; j0 < keys; j0 += 4 * N) {
             __syncthreads();
             if (j0 + 2 * N < keys) fetch(j0 + 2 * N, s_k1, s_v1);
@@ -473,8 +474,7 @@ __global__ void __launch_bounds__(64 * kBf16Waves, 2) prefill_bf16_kernel(AttnCa
         st = Stats{-INFINITY, 0.f, 0.f};
     };
     clear();
-    if (keys > 0) fetch(0, s_k0, s_v0);
-    int64_t j0 = 0;
+    int j0 = 0;
     for (; j0 + 4 * N <= all; j0 += 4 * N) {  // keys that all rows see
         __syncthreads();
         fetch(j0 + 2 * N, s_k1, s_v1);
@@ -536,22 +536,21 @@ __global__ void __launch_bounds__(64 * kWaves) prefill_f32_kernel(AttnCall p)
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int half = lane >> 5, l31 = lane & 31;
     Work w;
-    if (!find_work<M>(p, blockIdx.x / p.d.h_kv, blockIdx.x % p.d.h_kv, &w)) return;
-    const int g = p.d.h_q / p.d.h_kv;
+    if (!find_work<M>(p, blockIdx.x / p.d.h_kv, blockIdx.x % p.d.h_kv, lane, &w)) return;
+    const int g = w.g;
 
-    const int64_t r = w.row0 + 32 * wave + l31;
-    const int64_t pos = (r < w.rows ? r : w.rows - 1) / g, hh = (r < w.rows ? r : w.rows - 1) - pos * g;
-    const int64_t limit = key_limit(w, pos, p.d.causal);
+    const int r = w.row0 + 32 * wave + l31, rc = r < w.rows ? r : w.rows - 1, pos = rc / g;
+    const int limit = key_limit(w, pos, p.d.causal);
     const float* qp = static_cast<const float*>(p.q) + (w.q0 + pos) * p.d.q_token +
-                      ((int64_t)w.head * g + hh) * p.d.q_head + 4 * half;
+                      (w.head * g + (rc - pos * g)) * p.d.q_head + 4 * half;
     f32x4_t q[D / 8];  // slot e of step kk: element 8 kk + 4 half + e
 #pragma unroll
     for (int kk = 0; kk < D / 8; ++kk) q[kk] = *reinterpret_cast<const f32x4_t*>(qp + 8 * kk);
 
-    const int64_t last = (w.row0 + M < w.rows ? w.row0 + M : w.rows) - 1;
-    const int64_t keys = key_limit(w, last / g, p.d.causal);
-    const int64_t wrow = w.row0 + 32 * wave;
-    const int64_t all = key_limit(w, (wrow < w.rows ? wrow : w.rows - 1) / g, p.d.causal);
+    const int last = (w.row0 + M < w.rows ? w.row0 + M : w.rows) - 1;
+    const int keys = key_limit(w, last / g, p.d.causal);
+    const int wrow = w.row0 + 32 * wave;
+    const int all = key_limit(w, (wrow < w.rows ? wrow : w.rows - 1) / g, p.d.causal);
 
     const char* kb = static_cast<const char*>(p.k) + 4 * (w.k0 * p.d.k_token + w.head * p.d.k_head);
     const char* vb = static_cast<const char*>(p.v) + 4 * (w.k0 * p.d.v_token + w.head * p.d.v_head);
@@ -564,7 +563,7 @@ __global__ void __launch_bounds__(64 * kWaves) prefill_f32_kernel(AttnCall p)
         for (int i = 0; i < 16; ++i) o[db][i] = 0.f;
     Stats st = {-INFINITY, 0.f, 0.f};
 
-    for (int64_t j0 = 0; j0 < keys; j0 += N) {
+    for (int j0 = 0; j0 < keys; j0 += N) {
         __syncthreads();
         stage_f32<N, CH>(kb, j0, w.len_k, 4 * p.d.k_token, s_k, wave, lane);
         stage_f32<N, CH>(vb, j0, w.len_k, 4 * p.d.v_token, s_v, wave, lane);
@@ -582,7 +581,7 @@ __global__ void __launch_bounds__(64 * kWaves) prefill_f32_kernel(AttnCall p)
             for (int e = 0; e < 4; ++e) acc = __builtin_amdgcn_mfma_f32_32x32x2f32(a[e], q[kk][e], acc, 0, 0, 0);
         }
         const bool masked = j0 + N > all;
-        const int lim = (int)(limit - j0 < N ? limit - j0 : N);
+        const int lim = limit - j0;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             const int key = 8 * (i / 4) + 4 * half + i % 4;
