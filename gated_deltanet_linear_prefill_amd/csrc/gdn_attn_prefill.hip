@@ -139,6 +139,19 @@ __device__ __forceinline__ void stage(const char* base, int row, int valid, int6
     }
 }
 
+// The same where all of the keys exist: `base` is this wave's first group's memory, `ahead` the
+// bytes from a group of the wave to its next.
+template <typename T, int D, int GROUP>
+__device__ __forceinline__ void stage_whole(const char* base, int ahead, char* lds, int wave, int off)
+{
+    using C = Tile<T, D>;
+    const __amdgpu_buffer_rsrc_t r = make_rsrc(base, 0x7fffffff);
+#pragma unroll
+    for (int i = 0; i < C::STEPS * C::GROUPS / C::WAVES; ++i)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            r, (__attribute__((address_space(3))) void*)(lds + (i * C::WAVES + wave) * GROUP), 16, off, i * ahead, 0, 0);
+}
+
 __device__ __forceinline__ bf16x4_t read_tr(const char* p)
 {
     typedef __attribute__((__vector_size__(4 * sizeof(__bf16)))) __bf16 v4;
@@ -467,13 +480,23 @@ __global__ void __launch_bounds__(64 * waves_of(sizeof(T), D), waves_of(sizeof(T
         st = Stats{-INFINITY, 0.f, 0.f};
     };
     clear();
+    // keys that all rows see; here the next keys to fetch always exist
+    const int kahead = (int)(C::WAVES * C::ROWS * ks), vahead = (int)(C::WAVES * C::ROWS * vs);
+    const char* kw = kb + (UNIT + wave * C::ROWS) * ks;
+    const char* vw = vb + (UNIT + wave * C::ROWS) * vs;
+    auto fetch_whole = [&](char* sk, char* sv) __attribute__((always_inline)) {
+        stage_whole<T, D, C::KG>(kw, kahead, sk, wave, koff);
+        stage_whole<T, D, C::VG>(vw, vahead, sv, wave, voff);
+        kw += UNIT * ks;
+        vw += UNIT * vs;
+    };
     int j0 = 0;
-    for (; j0 + 2 * UNIT <= all; j0 += 2 * UNIT) {  // keys that all rows see
+    for (; j0 + 3 * UNIT <= all; j0 += 2 * UNIT) {
         __syncthreads();
-        fetch(j0 + UNIT, s_k1, s_v1);
+        fetch_whole(s_k1, s_v1);
         use(std::integral_constant<int, kPlain>{}, s_k0, s_v0, j0);
         __syncthreads();
-        if (j0 + 2 * UNIT < keys) fetch(j0 + 2 * UNIT, s_k0, s_v0);
+        fetch_whole(s_k0, s_v0);
         use(std::integral_constant<int, kPlain>{}, s_k1, s_v1, j0 + UNIT);
     }
     run(std::integral_constant<int, kMasks>{}, j0);
