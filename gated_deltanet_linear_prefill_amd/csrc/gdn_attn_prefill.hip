@@ -44,17 +44,25 @@ struct Tile {
     static constexpr int GROUPS = ROWS == 1 ? 32 : 16, N = GROUPS * ROWS, BLOCKS = N / 32;
     static constexpr int PLACES = 32 / GROUPS;  // places that a 32-key block takes of every group
     static constexpr int KG = 1024 + 16, VG = 1024 + (ES == 2 ? 64 : 32);  // bytes of a padded group
-    // Eight waves, two a SIMD, and keys staged two steps at a time; where a wave's O and Q take all
-    // of 256 registers, and a step a quarter of the LDS, four waves and one step.
-    static constexpr bool SMALL = ROWS == 1;
-    static constexpr int WAVES = SMALL ? 4 : 8, STEPS = SMALL ? 1 : 2;
     static constexpr int PER = 16 / ES;  // elements of a 16-byte operand piece
 };
 
-constexpr int waves_of(int esize, int d)  // Tile::WAVES, for launch bounds
-{
-    return esize * d > 512 ? 4 : 8;
-}
+// How a workgroup is made up: its waves, the steps that are staged at a time, and over how many
+// groups of waves the steps are divided.
+template <int WAVES_, int STEPS_, int SPLIT_, int PER_SIMD_>
+struct Shape {
+    static constexpr int WAVES = WAVES_, STEPS = STEPS_, SPLIT = SPLIT_, ROWS = 32 * WAVES / SPLIT;
+    static constexpr int PER_SIMD = PER_SIMD_;  // waves that a SIMD should hold
+};
+// 256 rows share every staged key: the least traffic, for long work.
+using Wide = Shape<8, 2, 1, 2>;
+// 128 rows; half the waves take the first of two steps and half the second, and are joined at the
+// end: half the time per workgroup, for calls that have too few tiles to keep all CUs busy evenly.
+using Split = Shape<8, 2, 2, 2>;
+// 128 rows, two workgroups a CU: one starts and ends while the other computes, for many short tiles.
+using Twin = Shape<4, 1, 1, 2>;
+// fp32 with d = 256, where a wave's O and Q take all of 256 registers.
+using Lone = Shape<4, 1, 1, 1>;
 
 // A workgroup's tile: its sequence's rows and keys, and its own first row. The host keeps
 // rows and keys below 2^31 - 2^16.
@@ -123,14 +131,14 @@ __device__ __forceinline__ float other_half_sum(float x)
 
 // The keys [row, row + STEPS N) of a strided tensor into LDS, in padded groups of GROUP bytes;
 // zeros from `valid` rows on. `off` is this lane's byte offset within a group's rows in memory.
-template <typename T, int D, int GROUP>
+template <typename T, int D, typename S, int GROUP>
 __device__ __forceinline__ void stage(const char* base, int row, int valid, int64_t stride,
                                       char* lds, int wave, int off)
 {
     using C = Tile<T, D>;
 #pragma unroll
-    for (int i = 0; i < C::STEPS * C::GROUPS / C::WAVES; ++i) {
-        const int x = i * C::WAVES + wave;
+    for (int i = 0; i < S::STEPS * C::GROUPS / S::WAVES; ++i) {
+        const int x = i * S::WAVES + wave;
         const int first = row + x * C::ROWS;
         const int left = valid - first, have = left < C::ROWS ? left : C::ROWS;
         const __amdgpu_buffer_rsrc_t r =
@@ -141,15 +149,15 @@ __device__ __forceinline__ void stage(const char* base, int row, int valid, int6
 
 // The same where all of the keys exist: `base` is this wave's first group's memory, `ahead` the
 // bytes from a group of the wave to its next.
-template <typename T, int D, int GROUP>
+template <typename T, int D, typename S, int GROUP>
 __device__ __forceinline__ void stage_whole(const char* base, int ahead, char* lds, int wave, int off)
 {
     using C = Tile<T, D>;
     const __amdgpu_buffer_rsrc_t r = make_rsrc(base, 0x7fffffff);
 #pragma unroll
-    for (int i = 0; i < C::STEPS * C::GROUPS / C::WAVES; ++i)
+    for (int i = 0; i < S::STEPS * C::GROUPS / S::WAVES; ++i)
         __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            r, (__attribute__((address_space(3))) void*)(lds + (i * C::WAVES + wave) * GROUP), 16, off, i * ahead, 0, 0);
+            r, (__attribute__((address_space(3))) void*)(lds + (i * S::WAVES + wave) * GROUP), 16, off, i * ahead, 0, 0);
 }
 
 __device__ __forceinline__ bf16x4_t read_tr(const char* p)
@@ -211,29 +219,48 @@ struct Stats {
     float exact;  // the same before rounding, if lse is wanted and weights are rounded
 };
 
-// Writes a row's output: this lane's 4-element pieces of O^T, divided by the sum.
+// Writes a wave's 32 rows, divided by their sums. A lane holds 4-element pieces of its own row: they
+// go through the wave's part of LDS (256 bytes a row at a time, padded), so that 16 bytes of each
+// of 16 lanes are one stretch of memory. `first` is the first of the rows.
 template <typename T, int D>
-__device__ __forceinline__ void write_row(const AttnCall& p, const Work& w, int r, int lane,
-                                          const f32x16_t* o, const Stats& st)
+__device__ __forceinline__ void write_rows(const AttnCall& p, const Work& w, int first, int lane,
+                                           const f32x16_t* o, const Stats& st, char* lds)
 {
+    constexpr int ROWB = sizeof(T) * D, PASS = ROWB < 256 ? ROWB : 256, STRIDE = PASS + 16, LPR = PASS / 16;
+    constexpr int BLOCKS = PASS / (32 * (int)sizeof(T));  // 32-element blocks of O^T in a pass
     const float l = other_half_sum(st.l), e = sizeof(T) == 2 ? other_half_sum(st.exact) : l;
-    if (r >= w.rows) return;
-    const int pos = (int)((uint32_t)r / (uint32_t)w.g);
-    const int64_t row = (w.q0 + pos) * p.d.h_q + w.head * w.g + (r - pos * w.g);
+    const int half = lane >> 5, r = first + (lane & 31), rc = r < w.rows ? r : w.rows - 1;
+    const int pos = (int)((uint32_t)rc / (uint32_t)w.g);
+    const int64_t row = (w.q0 + pos) * p.d.h_q + w.head * w.g + (rc - pos * w.g);
+    if (p.lse && lane < 32 && r < w.rows)
+        p.lse[row] = e > 0.f ? (st.m + __builtin_amdgcn_logf(e)) * kLn2 : (e == e ? -INFINITY : e);
     const float inv = l > 0.f ? 1.f / l : (l == l ? 0.f : l);
-    T* out = static_cast<T*>(p.out) + row * D + 4 * (lane >> 5);
 #pragma unroll
-    for (int db = 0; db < D / 32; ++db)
+    for (int pass = 0; pass < ROWB / PASS; ++pass) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float a = o[db][4 * i] * inv, b = o[db][4 * i + 1] * inv;
-            const float c = o[db][4 * i + 2] * inv, f = o[db][4 * i + 3] * inv;
-            if constexpr (sizeof(T) == 2)
-                *reinterpret_cast<u32x2_t*>(out + 32 * db + 8 * i) = u32x2_t{pack_bf16(a, b), pack_bf16(c, f)};
-            else
-                *reinterpret_cast<f32x4_t*>(out + 32 * db + 8 * i) = f32x4_t{a, b, c, f};
+        for (int x = 0; x < BLOCKS; ++x) {
+            const f32x16_t v = o[pass * BLOCKS + x] * inv;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                char* at = lds + (lane & 31) * STRIDE + (32 * x + 8 * i + 4 * half) * (int)sizeof(T);
+                if constexpr (sizeof(T) == 2)
+                    *reinterpret_cast<u32x2_t*>(at) = u32x2_t{pack_bf16(v[4 * i], v[4 * i + 1]), pack_bf16(v[4 * i + 2], v[4 * i + 3])};
+                else
+                    *reinterpret_cast<f32x4_t*>(at) = f32x4_t{v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]};
+            }
         }
-    if (p.lse && lane < 32) p.lse[row] = e > 0.f ? (st.m + __builtin_amdgcn_logf(e)) * kLn2 : (e == e ? -INFINITY : e);
+        // the wave's own writes, read by its other lanes
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll
+        for (int i = 0; i < 32 * LPR / 64; ++i) {
+            const int at = i * (64 / LPR) + lane / LPR;  // of the 32 rows
+            const u32x4_t x = *reinterpret_cast<const u32x4_t*>(lds + at * STRIDE + lane % LPR * 16);
+            const int64_t to = __shfl(row, at, 64);
+            if (first + at < w.rows)
+                *reinterpret_cast<u32x4_t*>(static_cast<char*>(p.out) + to * ROWB + pass * PASS + lane % LPR * 16) = x;
+        }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    }
 }
 
 // kPlain: every row sees every key. kMasks: where `masked`, some rows may not see some keys, and
@@ -382,24 +409,19 @@ __device__ __forceinline__ void attn_step(const char* sk, const char* sv, int kl
     }
 }
 
-// SPLIT 1: the waves have 32 rows each, and take every step; a staged key serves all of them.
-// SPLIT 2: half the rows; half the waves take the first of two steps and half the second, and
-// are joined at the end: half the time per workgroup, for calls that have too few tiles to keep
-// all CUs busy evenly.
-template <typename T, int D, bool LSE, int SPLIT>
-__global__ void __launch_bounds__(64 * waves_of(sizeof(T), D), waves_of(sizeof(T), D) / 4) prefill_kernel(AttnCall p)
+template <typename T, int D, bool LSE, typename S>
+__global__ void __launch_bounds__(64 * S::WAVES, S::PER_SIMD) prefill_kernel(AttnCall p)
 {
     using C = Tile<T, D>;
-    static_assert(C::WAVES == waves_of(sizeof(T), D) && SPLIT <= C::STEPS, "tiling");
-    constexpr int N = C::N, UNIT = C::STEPS * N, M = 32 * C::WAVES / SPLIT, ND = D / 32;
+    constexpr int N = C::N, UNIT = S::STEPS * N, M = S::ROWS, ND = D / 32, SPLIT = S::SPLIT;
     constexpr int ES = C::ES;
     // separate arrays: the compiler then knows that reading one need not wait for the loads that
     // are filling another
-    __shared__ __align__(16) char s_k0[C::STEPS * C::GROUPS * C::KG], s_k1[C::STEPS * C::GROUPS * C::KG];
-    __shared__ __align__(16) char s_v0[C::STEPS * C::GROUPS * C::VG], s_v1[C::STEPS * C::GROUPS * C::VG];
+    __shared__ __align__(16) char s_k0[S::STEPS * C::GROUPS * C::KG], s_k1[S::STEPS * C::GROUPS * C::KG];
+    __shared__ __align__(16) char s_v0[S::STEPS * C::GROUPS * C::VG], s_v1[S::STEPS * C::GROUPS * C::VG];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int half = lane >> 5;
-    const int rw = wave % (C::WAVES / SPLIT), turn = wave / (C::WAVES / SPLIT);  // 32 rows, steps
+    const int rw = wave % (S::WAVES / SPLIT), turn = wave / (S::WAVES / SPLIT);  // 32 rows, steps
     Work w;
     if (!find_work<M>(p, blockIdx.x / p.d.h_kv, blockIdx.x % p.d.h_kv, lane, &w)) return;
 
@@ -415,8 +437,8 @@ __global__ void __launch_bounds__(64 * waves_of(sizeof(T), D), waves_of(sizeof(T
     const int vlane = ES == 2 ? (4 * half + ((lane >> 2) & 3)) * C::VG + ((lane >> 4) & 1) * 32 + (lane & 3) * 8
                               : 4 * half * C::VG + lane % 32 * 4;
     auto fetch = [&](int row, char* sk, char* sv) __attribute__((always_inline)) {
-        stage<T, D, C::KG>(kb, row, w.len_k, ks, sk, wave, koff);
-        stage<T, D, C::VG>(vb, row, w.len_k, vs, sv, wave, voff);
+        stage<T, D, S, C::KG>(kb, row, w.len_k, ks, sk, wave, koff);
+        stage<T, D, S, C::VG>(vb, row, w.len_k, vs, sv, wave, voff);
     };
 
     // keys that a row sees: the workgroup's last row and all of its rows; the last of the wave's
@@ -456,7 +478,7 @@ __global__ void __launch_bounds__(64 * waves_of(sizeof(T), D), waves_of(sizeof(T
             step(mode, sk + turn * C::GROUPS * C::KG, sv + turn * C::GROUPS * C::VG, j0 + turn * N);
         } else {
 #pragma unroll 1
-            for (int t = 0; t < C::STEPS; ++t) step(mode, sk + t * C::GROUPS * C::KG, sv + t * C::GROUPS * C::VG, j0 + t * N);
+            for (int t = 0; t < S::STEPS; ++t) step(mode, sk + t * C::GROUPS * C::KG, sv + t * C::GROUPS * C::VG, j0 + t * N);
         }
     };
     // Two buffers: while the steps in one are used those in the other arrive. The barrier before
@@ -481,12 +503,12 @@ __global__ void __launch_bounds__(64 * waves_of(sizeof(T), D), waves_of(sizeof(T
     };
     clear();
     // keys that all rows see; here the next keys to fetch always exist
-    const int kahead = (int)(C::WAVES * C::ROWS * ks), vahead = (int)(C::WAVES * C::ROWS * vs);
+    const int kahead = (int)(S::WAVES * C::ROWS * ks), vahead = (int)(S::WAVES * C::ROWS * vs);
     const char* kw = kb + (UNIT + wave * C::ROWS) * ks;
     const char* vw = vb + (UNIT + wave * C::ROWS) * vs;
     auto fetch_whole = [&](char* sk, char* sv) __attribute__((always_inline)) {
-        stage_whole<T, D, C::KG>(kw, kahead, sk, wave, koff);
-        stage_whole<T, D, C::VG>(vw, vahead, sv, wave, voff);
+        stage_whole<T, D, S, C::KG>(kw, kahead, sk, wave, koff);
+        stage_whole<T, D, S, C::VG>(vw, vahead, sv, wave, voff);
         kw += UNIT * ks;
         vw += UNIT * vs;
     };
@@ -504,12 +526,13 @@ __global__ void __launch_bounds__(64 * waves_of(sizeof(T), D), waves_of(sizeof(T
         clear();
         fetch(0, s_k0, s_v0);
         run(std::integral_constant<int, kOdd>{}, 0);
+        __syncthreads();  // the buffers are written to below
     }
 
     if constexpr (SPLIT == 2) {
         // O of the second steps' waves through LDS: D / 2 registers of 64 lanes a wave, in the
         // buffers of K and V, a row group in each
-        static_assert(D / 2 * 256 <= C::STEPS * C::GROUPS * C::KG, "a wave's O fits a buffer");
+        static_assert(D / 2 * 256 <= S::STEPS * C::GROUPS * C::KG, "a wave's O fits a buffer");
         float* so = reinterpret_cast<float*>(rw == 0 ? s_k0 : rw == 1 ? s_k1 : rw == 2 ? s_v0 : s_v1);
         __syncthreads();
         if (turn == 1) {
@@ -538,41 +561,50 @@ __global__ void __launch_bounds__(64 * waves_of(sizeof(T), D), waves_of(sizeof(T
 #pragma unroll
             for (int i = 0; i < 16; ++i) o[db][i] = a0 * o[db][i] + a1 * so[(16 * db + i) * 64 + lane];
     }
+    // All waves have met since the last use of K and V: each has a part of the buffers to itself (with
+    // SPLIT 2 in the one where it read the other half's O).
+    constexpr int PART = 32 * ((C::ROWB < 256 ? C::ROWB : 256) + 16), PER_BUFFER = M / 32 / 4;
+    static_assert(PER_BUFFER * PART <= S::STEPS * C::GROUPS * C::KG, "the waves' parts fit the buffers");
+    const int buffer = rw / PER_BUFFER;
+    char* part = buffer == 0 ? s_k0 : buffer == 1 ? s_k1 : buffer == 2 ? s_v0 : s_v1;
     st.m *= c;
-    write_row<T, D>(p, w, r, lane, o, st);
+    write_rows<T, D>(p, w, wfirst, lane, o, st, part + rw % PER_BUFFER * PART);
 }
 
-template <typename T, int D, bool LSE, int SPLIT>
+template <typename T, int D, bool LSE, typename S>
 hipError_t launch_kernel(const AttnCall& c)
 {
-    constexpr int WAVES = waves_of(sizeof(T), D);
-    const int64_t tiles = c.d.total_q * (c.d.h_q / c.d.h_kv) / (32 * WAVES / SPLIT) + c.d.n;
-    hipLaunchKernelGGL((prefill_kernel<T, D, LSE, SPLIT>), dim3((unsigned)(tiles * c.d.h_kv)), dim3(64 * WAVES), 0,
+    const int64_t tiles = c.d.total_q * (c.d.h_q / c.d.h_kv) / S::ROWS + c.d.n;
+    hipLaunchKernelGGL((prefill_kernel<T, D, LSE, S>), dim3((unsigned)(tiles * c.d.h_kv)), dim3(64 * S::WAVES), 0,
                        c.stream, c);
     return hipGetLastError();
 }
 
 template <typename T, int D, bool LSE>
-hipError_t launch_split(const AttnCall& c)
+hipError_t launch_shape(const AttnCall& c)
 {
-    if constexpr (Tile<T, D>::STEPS == 1) {
-        return launch_kernel<T, D, LSE, 1>(c);
+    if constexpr (Tile<T, D>::ROWS == 1) {
+        return launch_kernel<T, D, LSE, Lone>(c);
     } else {
-        // Whole tiles of 256 rows where they fill the CUs, evenly: under a causal mask a prompt's
-        // last tiles take twice the average, so there should be two for every CU. Measured (us,
-        // whole against split): bf16, d = 256, 16/2 heads, 4096-token prompt (256 tiles) 236 /
-        // 178, 8192 (512) 526 / 622, 4096 tokens after 28672 (256 equal tiles) 1910 / 2112.
-        const int64_t tiles = c.d.total_q * c.d.h_q / 256;
-        return tiles < (c.d.causal && c.d.total_k < 2 * c.d.total_q ? 512 : 256) ? launch_kernel<T, D, LSE, 2>(c)
-                                                                                 : launch_kernel<T, D, LSE, 1>(c);
+        // Measured (us, bf16, Wide / Split / Twin; tiles of 256 rows). Few tiles of many keys, where
+        // one workgroup's time is the call's: d = 256, 16/2 heads, 4096-token prompt (256 tiles)
+        // 190 / 144 / 169, 2048 (128) 98 / 62 / 74; d = 128, 16/16 heads, 4096 (256) 109 / 79 / 91.
+        // Few keys: 32 prompts of 64, 32/8 heads (256) 21 / 30 / 18; many tiles: 16 of 1024 (2048)
+        // 205 / 270 / 193, 8192 (1024) 513 / 542 / 504. Long rows and many keys, where the traffic
+        // of staging counts: d = 256, 8192 (512) 472 / 508 / 512, 16 of 1024 197 / 270 / 191.
+        const int64_t tiles = c.d.total_q * c.d.h_q / 256, keys = c.d.total_k / c.d.n;
+        if (tiles <= 256 && keys >= 1024) return launch_kernel<T, D, LSE, Split>(c);
+        if constexpr (Tile<T, D>::ROWS == 2 && sizeof(T) == 2)
+            if (keys >= 8192) return launch_kernel<T, D, LSE, Wide>(c);
+        return launch_kernel<T, D, LSE, Twin>(c);
     }
 }
 
 template <int D>
 hipError_t launch_d(const AttnCall& c)
 {
-    if (c.d.dtype == GDN_F32) return launch_split<float, D, false>(c);
-    return c.lse ? launch_split<uint16_t, D, true>(c) : launch_split<uint16_t, D, false>(c);
+    if (c.d.dtype == GDN_F32) return launch_shape<float, D, false>(c);
+    return c.lse ? launch_shape<uint16_t, D, true>(c) : launch_shape<uint16_t, D, false>(c);
 }
 
 }  // namespace
