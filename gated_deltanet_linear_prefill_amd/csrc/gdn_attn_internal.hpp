@@ -79,16 +79,23 @@ __device__ __forceinline__ float scale_of(uint32_t b)
     return __uint_as_float(b << 23);
 }
 
-// The sequence a packed row belongs to: the last s in [0, n) with cu[s] <= row (0 if none).
-// Whatever cu holds, the answer is a valid sequence index.
-__device__ __forceinline__ int64_t find_seq(const int32_t* cu, int64_t n, int64_t row)
+// The sequence a packed row belongs to: the last s in [0, n) with cu[s] <= row (0 if none), for a
+// wave whose lanes' rows start at `first` and lie close together: 64 sequences are compared with
+// the first row at a time, one a lane, and each lane goes on from there. Whatever cu holds, the
+// answer is a valid sequence index.
+__device__ __forceinline__ int find_seq(const int32_t* cu, int n, int first, int row)
 {
-    int64_t lo = 0, hi = n;  // cu[lo] <= row (or lo == 0), cu[hi] > row (or hi == n)
-    while (hi - lo > 1) {
-        const int64_t mid = (lo + hi) >> 1;
-        if (cu[mid] <= row) lo = mid; else hi = mid;
+    const int lane = threadIdx.x & 63;
+    int s = 0;
+    for (int span = n; span > 1;) {  // the sequence is in [s, s + span)
+        const int step = (span + 63) / 64;
+        const bool before = lane * step < span && (lane == 0 || cu[s + lane * step] <= first);
+        const int x = 63 - __builtin_clzll(__ballot(before) | 1);  // the last lane not past the row
+        s += x * step;
+        span = span - x * step < step ? span - x * step : step;
     }
-    return lo;
+    while (s + 1 < n && cu[s + 1] <= row) ++s;
+    return s;
 }
 
 }  // namespace gdn
