@@ -123,7 +123,8 @@ decode_attn_kernel(AttnDecodeCall p, int64_t range, int ranges, int head_tiles, 
     len = len < p.max_len ? len : p.max_len;
     len = len < cap ? len : cap;
     const int64_t begin = rg * range;
-    if (ranges > 1 && begin >= len) return;  // the join does not read this range
+    if (rg > 0 && begin >= len) return;  // the join does not read this range
+    const bool whole = len <= range;     // nothing to join
     const int64_t end = begin + range < len ? begin + range : len;
 
     // Q as the B operand: column c is head 16 ht + c (heads past the group repeat the last)
@@ -366,7 +367,7 @@ decode_attn_kernel(AttnDecodeCall p, int64_t range, int ranges, int head_tiles, 
 #pragma unroll
         for (int y = 0; y < kWaves; ++y)
             if (s_m[y][hd] != -INFINITY) ls += s_l[y][hd] * __builtin_amdgcn_exp2f(s_m[y][hd] - top);
-        if (ranges == 1) {
+        if (whole) {
             const int64_t orow = seq * p.h_q + kvh * G + 16 * ht + hd;
             const float inv = ls > 0.f ? 1.f / ls : (ls == ls ? 0.f : ls);
             sum *= inv;
@@ -410,7 +411,8 @@ __global__ void __launch_bounds__(16 * kJoinGroups) decode_join_kernel(AttnDecod
     int64_t len = p.lens[seq];
     len = len < p.max_len ? len : p.max_len;
     len = len < cap ? len : cap;
-    const int used = len <= 0 ? 0 : (int)((len + range - 1) / range);
+    if (len <= range) return;  // written by its only range
+    const int used = (int)((len + range - 1) / range);
     const int64_t unit = (seq * p.c.h_kv + kvh) * head_tiles + ht;
     const float2* ml = part.ml + unit * ranges * 16 + hd;
     const int y = threadIdx.x / 16, el = (int)(blockIdx.x % (D / 64)) * 64 + threadIdx.x % 16 * 4;

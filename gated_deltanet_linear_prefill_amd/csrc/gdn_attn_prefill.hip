@@ -160,6 +160,13 @@ __device__ __forceinline__ void stage_whole(const char* base, int ahead, char* l
             r, (__attribute__((address_space(3))) void*)(lds + (i * S::WAVES + wave) * GROUP), 16, off, i * ahead, 0, 0);
 }
 
+// Every wave's loads to LDS have landed, and every wave is past its reads of LDS. A plain barrier
+// does not wait for loads to LDS: each wave has to wait for its own before it.
+__device__ __forceinline__ void staged_barrier()
+{
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
 __device__ __forceinline__ bf16x4_t read_tr(const char* p)
 {
     typedef __attribute__((__vector_size__(4 * sizeof(__bf16)))) __bf16 v4;
@@ -482,14 +489,14 @@ __global__ void __launch_bounds__(64 * S::WAVES, S::PER_SIMD) prefill_kernel(Att
         }
     };
     // Two buffers: while the steps in one are used those in the other arrive. The barrier before
-    // a use has every wave's loads of it done, and every wave past the buffer refilled next.
+    // a use has every wave's loads of it landed, and every wave past the buffer refilled next.
     auto run = [&](auto mode, int j0) __attribute__((always_inline)) {
         for (; j0 < keys; j0 += 2 * UNIT) {
-            __syncthreads();
+            staged_barrier();
             if (j0 + UNIT < keys) fetch(j0 + UNIT, s_k1, s_v1);
             use(mode, s_k0, s_v0, j0);
             if (j0 + UNIT >= keys) break;
-            __syncthreads();
+            staged_barrier();
             if (j0 + 2 * UNIT < keys) fetch(j0 + 2 * UNIT, s_k0, s_v0);
             use(mode, s_k1, s_v1, j0 + UNIT);
         }
@@ -514,10 +521,10 @@ __global__ void __launch_bounds__(64 * S::WAVES, S::PER_SIMD) prefill_kernel(Att
     };
     int j0 = 0;
     for (; j0 + 3 * UNIT <= all; j0 += 2 * UNIT) {
-        __syncthreads();
+        staged_barrier();
         fetch_whole(s_k1, s_v1);
         use(std::integral_constant<int, kPlain>{}, s_k0, s_v0, j0);
-        __syncthreads();
+        staged_barrier();
         fetch_whole(s_k0, s_v0);
         use(std::integral_constant<int, kPlain>{}, s_k1, s_v1, j0 + UNIT);
     }
