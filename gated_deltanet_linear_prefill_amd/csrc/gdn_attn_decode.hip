@@ -57,10 +57,10 @@ Plan make_plan(const gdn_kv_cache* c, int32_t h_q, int64_t max_len)
     return p;
 }
 
-// Workspace of one call: O sums [unit][range][G][D] fp32, then (m, l) pairs.
+// Workspace of one call: O sums [unit][range][16][D] fp32, then (m, l, exact l, -) of each.
 struct Partials {
     float* o;
-    float2* ml;
+    float4* ml;
 };
 
 template <typename T, bool FP8, int D>
@@ -74,6 +74,8 @@ struct Cfg {
     static constexpr int EPK = 16 / ES;                        // elements of each
     // 16-position blocks of a step: K and V rows of a step stay in registers
     static constexpr int NB = D * ES > 512 ? 1 : 2, STEP = 16 * NB;
+    static constexpr bool QLDS = D * ES >= 512;                // Q in LDS, rows of QSTRIDE bytes
+    static constexpr int QSTRIDE = D * (int)sizeof(T) + 16;
 };
 
 template <int BYTES>
@@ -87,6 +89,11 @@ __device__ __forceinline__ uint32_t word(const P& p, int i)
 {
     if constexpr (sizeof(P) == 4) return p;
     else return p[i];
+}
+
+__device__ __forceinline__ float round_bf16(float x)
+{
+    return (float)(__bf16)x;
 }
 
 __device__ __forceinline__ uint32_t cvt_bf16_fp8(uint32_t w, bool hi)
@@ -103,8 +110,11 @@ decode_attn_kernel(AttnDecodeCall p, int64_t range, int ranges, int head_tiles, 
     using C = Cfg<T, FP8, D>;
     using VP = typename Piece<C::EPL * C::ES>::type;
     constexpr bool BF = sizeof(T) == 2;
-    __shared__ float s_o[kWaves][16][D + 4];
-    __shared__ float s_m[kWaves][16], s_l[kWaves][16];
+    __shared__ __align__(16) float s_o[kWaves][16][D + 4];
+    static_assert(16 * C::QSTRIDE <= (int)sizeof(s_o), "Q fits");
+    __shared__ float s_m[kWaves][16];
+    __shared__ float2 s_l[kWaves][16];
+    char* const s_q = reinterpret_cast<char*>(&s_o[0][0][0]);  // until the waves are joined
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 15, g = lane >> 4;
@@ -127,23 +137,41 @@ decode_attn_kernel(AttnDecodeCall p, int64_t range, int ranges, int head_tiles, 
     const bool whole = len <= range;     // nothing to join
     const int64_t end = begin + range < len ? begin + range : len;
 
-    // Q as the B operand: column c is head 16 ht + c (heads past the group repeat the last)
-    const int head = kvh * G + 16 * ht + (c < heads ? c : heads - 1);
-    const T* qp = static_cast<const T*>(p.q) + seq * p.q_token + (int64_t)head * p.q_head;
-    // element order of a K piece: load i brings elements (i * 4 + g) * EPK ..
-    T q[D / 4];
-#pragma unroll
-    for (int i = 0; i < C::KL; ++i)
-#pragma unroll
-        for (int e = 0; e < C::EPK; e += 16 / (int)sizeof(T)) {
-            const u32x4_t x = *reinterpret_cast<const u32x4_t*>(qp + (i * 4 + g) * C::EPK + e);
-            __builtin_memcpy(q + i * C::EPK + e, &x, 16);
+    // Q as the B operand: column c is head 16 ht + c (heads past the group repeat the last), piece x
+    // of element order (i * 4 + g) * EPK .. for load i of a K row. In registers, or in LDS where a
+    // row's K, V and O leave no room.
+    const T* qrow = static_cast<const T*>(p.q) + seq * p.q_token;
+    const int head0 = kvh * G + 16 * ht;
+    constexpr int QP = C::EPK * (int)sizeof(T) / 16;  // 16-byte pieces of a load's elements
+    u32x4_t q[C::QLDS ? 1 : C::KL * QP];
+    if constexpr (C::QLDS) {
+        constexpr int CH = D * (int)sizeof(T) / 16;
+        for (int x = threadIdx.x; x < 16 * CH; x += 64 * kWaves) {
+            const int h = x / CH < heads ? x / CH : heads - 1;
+            *reinterpret_cast<u32x4_t*>(s_q + x / CH * C::QSTRIDE + x % CH * 16) =
+                *reinterpret_cast<const u32x4_t*>(qrow + (head0 + h) * p.q_head + x % CH * (16 / (int)sizeof(T)));
         }
+    } else {
+        const T* qp = qrow + (head0 + (c < heads ? c : heads - 1)) * p.q_head;
+#pragma unroll
+        for (int i = 0; i < C::KL; ++i)
+#pragma unroll
+            for (int x = 0; x < QP; ++x)
+                q[i * QP + x] = *reinterpret_cast<const u32x4_t*>(qp + (i * 4 + g) * C::EPK + x * (16 / (int)sizeof(T)));
+    }
+    int qoff = c * C::QSTRIDE + g * C::EPK * (int)sizeof(T);
+    auto q_at = [&](int i, int x) __attribute__((always_inline)) {
+        if constexpr (C::QLDS)
+            return *reinterpret_cast<const u32x4_t*>(s_q + qoff + i * 4 * C::EPK * (int)sizeof(T) + x * 16);
+        else
+            return q[i * QP + x];
+    };
+    if constexpr (C::QLDS) __syncthreads();
 
     f32x4_t o[C::VL];
 #pragma unroll
     for (int j = 0; j < C::VL; ++j) o[j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    float m = -INFINITY, l = 0.f;
+    float m = -INFINITY, l = 0.f, exact = 0.f;
     const float cs = p.scale * kLog2e;
     const int32_t* table = p.c.page_table + seq * p.c.max_pages;
     const char* kpool = static_cast<const char*>(p.c.k);
@@ -204,6 +232,7 @@ decode_attn_kernel(AttnDecodeCall p, int64_t range, int ranges, int head_tiles, 
             for (int b = 0; b < C::NB; ++b) nrow[b] = block_row(next, b, &nthere[b]);
 
         // scores
+        if constexpr (C::QLDS) asm volatile("" : "+v"(qoff));  // read again in every step, not kept
         float s[4 * C::NB];
 #pragma unroll
         for (int b = 0; b < C::NB; ++b) {
@@ -211,29 +240,27 @@ decode_attn_kernel(AttnDecodeCall p, int64_t range, int ranges, int head_tiles, 
 #pragma unroll
             for (int i = 0; i < C::KL; ++i) {
                 if constexpr (BF && !FP8) {
-                    bf16x8_t qq;
-                    __builtin_memcpy(&qq, q + i * 8, 16);
-                    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, kx[b][i]), qq, acc, 0, 0, 0);
+                    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, kx[b][i]), __builtin_bit_cast(bf16x8_t, q_at(i, 0)), acc, 0, 0, 0);
                 } else if constexpr (BF) {
 #pragma unroll
                     for (int f = 0; f < 2; ++f) {
-                        bf16x8_t qq;
-                        __builtin_memcpy(&qq, q + i * 16 + f * 8, 16);
                         const u32x4_t a = {cvt_bf16_fp8(kx[b][i][2 * f], false), cvt_bf16_fp8(kx[b][i][2 * f], true),
                                            cvt_bf16_fp8(kx[b][i][2 * f + 1], false), cvt_bf16_fp8(kx[b][i][2 * f + 1], true)};
-                        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), qq, acc, 0, 0, 0);
+                        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, q_at(i, f)), acc, 0, 0, 0);
                     }
                 } else if constexpr (!FP8) {
+                    const u32x4_t qq = q_at(i, 0);
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        acc = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(kx[b][i][e]), q[i * 4 + e], acc, 0, 0, 0);
+                        acc = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(kx[b][i][e]), __uint_as_float(qq[e]), acc, 0, 0, 0);
                 } else {
 #pragma unroll
                     for (int e = 0; e < 16; e += 2) {
+                        const u32x4_t qq = q_at(i, e / 4);
                         const f32x2_t a = e & 2 ? __builtin_amdgcn_cvt_pk_f32_fp8((int)kx[b][i][e / 4], true)
                                                 : __builtin_amdgcn_cvt_pk_f32_fp8((int)kx[b][i][e / 4], false);
-                        acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a[0], q[i * 16 + e], acc, 0, 0, 0);
-                        acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a[1], q[i * 16 + e + 1], acc, 0, 0, 0);
+                        acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a[0], __uint_as_float(qq[e % 4]), acc, 0, 0, 0);
+                        acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a[1], __uint_as_float(qq[e % 4 + 1]), acc, 0, 0, 0);
                     }
                 }
             }
@@ -270,13 +297,18 @@ decode_attn_kernel(AttnDecodeCall p, int64_t range, int ranges, int head_tiles, 
             const float a = mn == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m - mn);
             m = mn;
             l *= a;
+            exact *= a;
 #pragma unroll
             for (int j = 0; j < C::VL; ++j) o[j] *= a;
         }
         const float ref = m == -INFINITY ? 0.f : m;
+        // Weights. For the product with bf16 V they are rounded to bf16; l is of what V is multiplied
+        // by, so that a rounding that all elements share cancels; lse is of the unrounded sum.
 #pragma unroll
         for (int i = 0; i < 4 * C::NB; ++i) {
             s[i] = __builtin_amdgcn_exp2f(s[i] - ref);
+            exact += s[i];
+            if constexpr (BF) s[i] = round_bf16(s[i]);
             l += s[i];
             if constexpr (FP8) s[i] *= scale_of((sv[i / 4] >> (8 * (i % 4))) & 0xff);
         }
@@ -285,6 +317,9 @@ decode_attn_kernel(AttnDecodeCall p, int64_t range, int ranges, int head_tiles, 
         if constexpr (BF) {
             const u32x4_t pw = {pack_bf16(s[0], s[1]), pack_bf16(s[2], s[3]), pack_bf16(s[4], s[5]), pack_bf16(s[6], s[7])};
             const bf16x8_t pb = __builtin_bit_cast(bf16x8_t, pw);
+            auto add = [&](int at, u32x4_t a) __attribute__((always_inline)) {
+                o[at] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), pb, o[at], 0, 0, 0);
+            };
 #pragma unroll
             for (int u = 0; u < C::U; ++u) {
                 if constexpr (!FP8) {
@@ -295,7 +330,7 @@ decode_attn_kernel(AttnDecodeCall p, int64_t range, int ranges, int head_tiles, 
                         for (int x = 0; x < 4; ++x)
                             a[x] = __builtin_amdgcn_perm(word(vx[2 * x + 1][u], j / 2), word(vx[2 * x][u], j / 2),
                                                          j & 1 ? 0x07060302u : 0x05040100u);
-                        o[u * C::EPL + j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), pb, o[u * C::EPL + j], 0, 0, 0);
+                        add(u * C::EPL + j, a);
                     }
                 } else {
 #pragma unroll
@@ -309,8 +344,8 @@ decode_attn_kernel(AttnDecodeCall p, int64_t range, int ranges, int head_tiles, 
                             a0[x] = cvt_bf16_fp8(y, false);
                             a1[x] = cvt_bf16_fp8(y, true);
                         }
-                        o[u * C::EPL + j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a0), pb, o[u * C::EPL + j], 0, 0, 0);
-                        o[u * C::EPL + j + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a1), pb, o[u * C::EPL + j + 1], 0, 0, 0);
+                        add(u * C::EPL + j, a0);
+                        add(u * C::EPL + j + 1, a1);
                     }
                 }
             }
@@ -336,9 +371,11 @@ decode_attn_kernel(AttnDecodeCall p, int64_t range, int ranges, int head_tiles, 
     // join the waves: weights relative to the largest maximum
     l += __shfl_xor(l, 16, 64);
     l += __shfl_xor(l, 32, 64);
+    exact += __shfl_xor(exact, 16, 64);
+    exact += __shfl_xor(exact, 32, 64);
     if (g == 0) {
         s_m[wave][c] = m;
-        s_l[wave][c] = l;
+        s_l[wave][c] = make_float2(l, exact);
     }
     __syncthreads();
     float mm = s_m[0][c];
@@ -361,12 +398,16 @@ decode_attn_kernel(AttnDecodeCall p, int64_t range, int ranges, int head_tiles, 
 #pragma unroll
         for (int y = 1; y < kWaves; ++y) top = fmaxf(top, s_m[y][hd]);
         f32x4_t sum = {0.f, 0.f, 0.f, 0.f};
-        float ls = 0.f;
+        float ls = 0.f, le = 0.f;
 #pragma unroll
         for (int y = 0; y < kWaves; ++y) sum += *reinterpret_cast<const f32x4_t*>(&s_o[y][hd][el]);
 #pragma unroll
         for (int y = 0; y < kWaves; ++y)
-            if (s_m[y][hd] != -INFINITY) ls += s_l[y][hd] * __builtin_amdgcn_exp2f(s_m[y][hd] - top);
+            if (s_m[y][hd] != -INFINITY) {
+                const float w = __builtin_amdgcn_exp2f(s_m[y][hd] - top);
+                ls += s_l[y][hd].x * w;
+                le += s_l[y][hd].y * w;
+            }
         if (whole) {
             const int64_t orow = seq * p.h_q + kvh * G + 16 * ht + hd;
             const float inv = ls > 0.f ? 1.f / ls : (ls == ls ? 0.f : ls);
@@ -374,11 +415,11 @@ decode_attn_kernel(AttnDecodeCall p, int64_t range, int ranges, int head_tiles, 
             T* out = static_cast<T*>(p.out) + orow * D + el;
             if constexpr (BF) *reinterpret_cast<u32x2_t*>(out) = u32x2_t{pack_bf16(sum[0], sum[1]), pack_bf16(sum[2], sum[3])};
             else *reinterpret_cast<f32x4_t*>(out) = sum;
-            if (p.lse && el == 0) p.lse[orow] = ls > 0.f ? (top + __builtin_amdgcn_logf(ls)) * kLn2 : (ls == ls ? -INFINITY : ls);
+            if (p.lse && el == 0) p.lse[orow] = le > 0.f ? (top + __builtin_amdgcn_logf(le)) * kLn2 : (le == le ? -INFINITY : le);
         } else {
             const int64_t at = (unit * ranges + rg) * 16 + hd;
             *reinterpret_cast<f32x4_t*>(part.o + at * D + el) = sum;
-            if (el == 0) part.ml[at] = make_float2(top, ls);
+            if (el == 0) part.ml[at] = make_float4(top, ls, le, 0.f);
         }
     }
 }
@@ -401,7 +442,8 @@ __global__ void __launch_bounds__(16 * kJoinGroups) decode_join_kernel(AttnDecod
                                                                        int page_shift, Partials part)
 {
     __shared__ f32x4_t s_o[kJoinGroups][16];
-    __shared__ float s_l[kJoinGroups], s_m[kJoinGroups / 4];
+    __shared__ float2 s_l[kJoinGroups];
+    __shared__ float s_m[kJoinGroups / 4];
     const int groups = blockDim.x / 16;
     const int64_t hrow = blockIdx.x / (D / 64);
     const int64_t seq = hrow / p.h_q;
@@ -414,7 +456,7 @@ __global__ void __launch_bounds__(16 * kJoinGroups) decode_join_kernel(AttnDecod
     if (len <= range) return;  // written by its only range
     const int used = (int)((len + range - 1) / range);
     const int64_t unit = (seq * p.c.h_kv + kvh) * head_tiles + ht;
-    const float2* ml = part.ml + unit * ranges * 16 + hd;
+    const float4* ml = part.ml + unit * ranges * 16 + hd;
     const int y = threadIdx.x / 16, el = (int)(blockIdx.x % (D / 64)) * 64 + threadIdx.x % 16 * 4;
     const float* po = part.o + (unit * ranges * 16 + hd) * D + el;
 
@@ -427,30 +469,32 @@ __global__ void __launch_bounds__(16 * kJoinGroups) decode_join_kernel(AttnDecod
     for (int x = 0; x < (int)blockDim.x / 64; ++x) top = fmaxf(top, s_m[x]);
 
     f32x4_t sum = {0.f, 0.f, 0.f, 0.f};
-    float ls = 0.f;
+    float ls = 0.f, le = 0.f;
 #pragma unroll 4
     for (int x = y; x < used; x += groups) {
-        const float2 v = ml[(int64_t)x * 16];
+        const float4 v = ml[(int64_t)x * 16];
         const f32x4_t a = *reinterpret_cast<const f32x4_t*>(po + (int64_t)x * 16 * D);
         const float f = v.x == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(v.x - top);
         ls += v.y * f;
+        le += v.z * f;
         sum += a * f;
     }
     s_o[y][threadIdx.x % 16] = sum;
-    if (threadIdx.x % 16 == 0) s_l[y] = ls;
+    if (threadIdx.x % 16 == 0) s_l[y] = make_float2(ls, le);
     __syncthreads();
     if (y != 0) return;
-    float l = 0.f;
+    float l = 0.f, e = 0.f;
     f32x4_t o = {0.f, 0.f, 0.f, 0.f};
     for (int x = 0; x < groups; ++x) {
         o += s_o[x][threadIdx.x];
-        l += s_l[x];
+        l += s_l[x].x;
+        e += s_l[x].y;
     }
     o *= l > 0.f ? 1.f / l : (l == l ? 0.f : l);
     T* out = static_cast<T*>(p.out) + hrow * D + el;
     if constexpr (sizeof(T) == 2) *reinterpret_cast<u32x2_t*>(out) = u32x2_t{pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3])};
     else *reinterpret_cast<f32x4_t*>(out) = o;
-    if (p.lse && el == 0) p.lse[hrow] = l > 0.f ? (top + __builtin_amdgcn_logf(l)) * kLn2 : (l == l ? -INFINITY : l);
+    if (p.lse && el == 0) p.lse[hrow] = e > 0.f ? (top + __builtin_amdgcn_logf(e)) * kLn2 : (e == e ? -INFINITY : e);
 }
 
 template <typename T, bool FP8, int D>
@@ -461,7 +505,7 @@ hipError_t launch_t(const AttnDecodeCall& c)
     const int shift = __builtin_ctz((unsigned)c.c.page_size);
     Partials part;
     part.o = static_cast<float*>(c.ws);
-    part.ml = reinterpret_cast<float2*>(part.o + units * pl.ranges * 16 * D);
+    part.ml = reinterpret_cast<float4*>(part.o + units * pl.ranges * 16 * D);
     hipLaunchKernelGGL((decode_attn_kernel<T, FP8, D>), dim3((unsigned)(units * pl.ranges)), dim3(64 * kWaves), 0,
                        c.stream, c, pl.range, (int)pl.ranges, pl.head_tiles, shift, part);
     const hipError_t e = hipGetLastError();
@@ -494,7 +538,7 @@ size_t attn_decode_workspace(const gdn_kv_cache* c, int32_t h_q, int64_t max_len
 {
     const Plan pl = make_plan(c, h_q, max_len);
     if (pl.ranges == 1) return 0;
-    return (size_t)(c->n * c->h_kv * pl.head_tiles * pl.ranges) * 16 * (c->d * sizeof(float) + sizeof(float2));
+    return (size_t)(c->n * c->h_kv * pl.head_tiles * pl.ranges) * 16 * (c->d * sizeof(float) + sizeof(float4));
 }
 
 hipError_t launch_attn_decode(const AttnDecodeCall& c)
