@@ -485,15 +485,21 @@ _raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_get
     else lambda index: torch.cuda.current_stream(index).cuda_stream
 
 
-def _rows(name, x, dtype, dev):
-    """(pointer, token stride, head stride) of a [tokens, heads, d] tensor with contiguous d. The
-    stride of a dimension of one entry means nothing to torch: a dense one stands for it."""
-    if not isinstance(x, _Tensor) or x.dim() != 3:
-        raise ValueError(f"{name} must be a torch tensor [tokens, heads, d]")
-    if x.device != dev or not x.is_cuda:
-        raise ValueError(f"{name} must be a CUDA (HIP) tensor on {dev}")
-    if x.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {x.dtype}")
+def _bad(name, x, what):
+    """Why x is not `what`."""
+    if not isinstance(x, _Tensor):
+        raise ValueError(f"{name} must be a torch tensor: {what}")
+    if not x.is_cuda:
+        raise ValueError(f"{name} must be a CUDA (HIP) tensor: {what}")
+    raise ValueError(f"{name} must be {what}; got {x.dtype} {tuple(x.shape)}, strides {x.stride()}, on {x.device}")
+
+
+def _rows(name, x, dtype, index):
+    """(pointer, token stride, head stride) of a [tokens, heads, d] tensor with contiguous d on the
+    GPU of this index. The stride of a dimension of one entry means nothing to torch: a dense one
+    stands for it."""
+    if not isinstance(x, _Tensor) or x.dtype != dtype or x.dim() != 3 or x.get_device() != index:
+        _bad(name, x, f"{dtype} [tokens, heads, d] on GPU {index}")
     st, sh, sd = x.stride()
     if sd != 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
@@ -505,42 +511,45 @@ def _rows(name, x, dtype, dev):
     return x.data_ptr(), st, sh
 
 
-def _dense(name, x, shape, dtype, dev):
-    """Pointer of a contiguous tensor of this shape and dtype on dev."""
-    if not isinstance(x, _Tensor) or x.dtype != dtype or x.shape != shape or x.device != dev \
+def _dense(name, x, shape, dtype, index):
+    """Pointer of a contiguous tensor of this shape and dtype on the GPU of this index."""
+    if not isinstance(x, _Tensor) or x.dtype != dtype or x.shape != shape or x.get_device() != index \
             or not x.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)} on {dev}")
+        _bad(name, x, f"contiguous {dtype} {tuple(shape)} on GPU {index}")
     return x.data_ptr()
 
 
-def _index(name, x, shape, dev):
+def _index(name, x, shape, index):
     """Pointer of an int32 tensor, or None."""
-    return None if x is None else _dense(name, x, shape, _i32, dev)
+    return None if x is None else _dense(name, x, shape, _i32, index)
 
 
 def _cache_of(k_cache, v_cache, page_table, k_scale, v_scale):
-    """(gdn_kv_cache, device) of the pools and the page table."""
-    if not isinstance(k_cache, _Tensor) or not k_cache.is_cuda or k_cache.dim() != 4:
-        raise ValueError("k_cache must be a CUDA (HIP) tensor [num_pages, h_kv, page_size, d]")
-    dtype, dev, shape = k_cache.dtype, k_cache.device, k_cache.shape
-    store = _POOLS.get(dtype)
-    if store is None:
-        raise ValueError("the cache must be bfloat16, float32 or float8_e4m3fn")
+    """(gdn_kv_cache, GPU index, [h_kv, d]) of the pools and the page table."""
+    store = _POOLS.get(k_cache.dtype) if isinstance(k_cache, _Tensor) else None
+    if store is None or k_cache.dim() != 4 or not k_cache.is_contiguous() or not k_cache.is_cuda:
+        _bad("k_cache", k_cache, "contiguous bfloat16, float32 or float8_e4m3fn [num_pages, h_kv, page_size, d]")
+    index, shape = k_cache.get_device(), k_cache.shape
     pages, h, size, d = shape
+    v = _dense("v_cache", v_cache, shape, k_cache.dtype, index)
     ks = vs = None
     if store == GDN_FP8:
-        ks = _dense("k_scale", k_scale, (pages, h, size), _u8, dev)
-        vs = _dense("v_scale", v_scale, (pages, h, size), _u8, dev)
-    if not isinstance(page_table, _Tensor) or page_table.dim() != 2:
-        raise ValueError("page_table must be an int32 tensor [n, max_pages]")
+        ks = _dense("k_scale", k_scale, shape[:3], _u8, index)
+        vs = _dense("v_scale", v_scale, shape[:3], _u8, index)
+    if not isinstance(page_table, _Tensor) or page_table.dtype != _i32 or page_table.dim() != 2 \
+            or page_table.get_device() != index or not page_table.is_contiguous():
+        _bad("page_table", page_table, f"contiguous int32 [n, max_pages] on GPU {index}")
     n, width = page_table.shape
-    return KvCache(n, pages, width, size, h, d, store, _dense("k_cache", k_cache, shape, dtype, dev),
-                   _dense("v_cache", v_cache, shape, dtype, dev), ks, vs,
-                   _dense("page_table", page_table, (n, width), _i32, dev)), dev
+    return KvCache(n, pages, width, size, h, d, store, k_cache.data_ptr(), v, ks, vs, page_table.data_ptr()), index
 
 
-def _queue(dev, stream):
-    return _raw_stream(dev.index) if stream is None else stream.cuda_stream
+def _queue(index, stream):
+    return _raw_stream(index) if stream is None else stream.cuda_stream
+
+
+def _gpu(x):
+    """Index of x's GPU; a tensor elsewhere gives -1, which no other tensor's matches."""
+    return x.get_device() if isinstance(x, _Tensor) and x.is_cuda else -2
 
 
 def _dtype_id(x):
@@ -562,16 +571,16 @@ def gdn_kv_write(k, v, k_cache, v_cache, page_table, start, cu_seqlens=None, *, 
     page_table int32 [n, max_pages]; a page id of -1 is a page that is not there, and what
     would go there is dropped. Updates the cache in place; returns nothing."""
     t = _dtype_id(k)
-    c, dev = _cache_of(k_cache, v_cache, page_table, k_scale, v_scale)
-    kp, kt, kh = _rows("k", k, k.dtype, dev)
-    vp, vt, vh = _rows("v", v, k.dtype, dev)
+    c, gpu = _cache_of(k_cache, v_cache, page_table, k_scale, v_scale)
+    kp, kt, kh = _rows("k", k, k.dtype, gpu)
+    vp, vt, vh = _rows("v", v, k.dtype, gpu)
     total = k.shape[0]
     if k.shape[1:] != (c.h_kv, c.d) or v.shape != k.shape:
         raise ValueError(f"k and v must have shape {(total, c.h_kv, c.d)}")
-    sp = _index("start", start, (c.n,), dev)
-    cp = _index("cu_seqlens", cu_seqlens, (c.n + 1,), dev)
+    sp = _index("start", start, (c.n,), gpu)
+    cp = _index("cu_seqlens", cu_seqlens, (c.n + 1,), gpu)
     st = _load().gdn_kv_write(ctypes.byref(c), total, t, kp, kt, kh, vp, vt, vh, sp, cp,
-                              _queue(dev, stream))
+                              _queue(gpu, stream))
     if st:
         raise GdnError(st, "gdn_kv_write")
 
@@ -585,16 +594,16 @@ def gdn_kv_read(k_cache, v_cache, page_table, start, cu_seqlens, total, *, dtype
     t = _DTYPES.get(dtype)
     if t is None:
         raise ValueError("dtype must be bfloat16 or float32")
-    c, dev = _cache_of(k_cache, v_cache, page_table, k_scale, v_scale)
+    c, gpu = _cache_of(k_cache, v_cache, page_table, k_scale, v_scale)
     shape = (int(total), c.h_kv, c.d)
     if k_out is None:
-        k_out = torch.empty(shape, dtype=dtype, device=dev)
+        k_out = torch.empty(shape, dtype=dtype, device=k_cache.device)
     if v_out is None:
-        v_out = torch.empty(shape, dtype=dtype, device=dev)
+        v_out = torch.empty_like(k_out)
     st = _load().gdn_kv_read(
-        ctypes.byref(c), shape[0], t, _dense("k_out", k_out, shape, dtype, dev),
-        _dense("v_out", v_out, shape, dtype, dev), _index("start", start, (c.n,), dev),
-        _index("cu_seqlens", cu_seqlens, (c.n + 1,), dev), _queue(dev, stream))
+        ctypes.byref(c), shape[0], t, _dense("k_out", k_out, shape, dtype, gpu),
+        _dense("v_out", v_out, shape, dtype, gpu), _index("start", start, (c.n,), gpu),
+        _index("cu_seqlens", cu_seqlens, (c.n + 1,), gpu), _queue(gpu, stream))
     if st:
         raise GdnError(st, "gdn_kv_read")
     return k_out, v_out
@@ -611,10 +620,10 @@ def gdn_attn_prefill(q, k, v, cu_q, cu_k=None, *, causal=True, scale=None, out=N
     1 / sqrt(d). Rows that see no key give 0. Pass lse (float32 [total_q, h_q]) to have the
     logarithm of each row's sum written to it. Returns out [total_q, h_q, d] of q's dtype."""
     t = _dtype_id(q)
-    dev = q.device
-    qp, qt, qh = _rows("q", q, q.dtype, dev)
-    kp, kt, kh = _rows("k", k, q.dtype, dev)
-    vp, vt, vh = _rows("v", v, q.dtype, dev)
+    gpu = _gpu(q)
+    qp, qt, qh = _rows("q", q, q.dtype, gpu)
+    kp, kt, kh = _rows("k", k, q.dtype, gpu)
+    vp, vt, vh = _rows("v", v, q.dtype, gpu)
     tq, hq, d = q.shape
     tk, hk, _ = k.shape
     if k.shape[2] != d or v.shape != k.shape:
@@ -626,12 +635,12 @@ def gdn_attn_prefill(q, k, v, cu_q, cu_k=None, *, causal=True, scale=None, out=N
         out = torch.empty_like(q, memory_format=torch.contiguous_format)
         op = out.data_ptr()
     else:
-        op = _dense("out", out, (tq, hq, d), q.dtype, dev)
-    lp = None if lse is None else _dense("lse", lse, (tq, hq), torch.float32, dev)
+        op = _dense("out", out, (tq, hq, d), q.dtype, gpu)
+    lp = None if lse is None else _dense("lse", lse, (tq, hq), torch.float32, gpu)
     dims = AttnDims(n, tq, tk, hq, hk, d, t, 1 if causal else 0, d ** -0.5 if scale is None else scale,
                     qt, qh, kt, kh, vt, vh)
-    st = _load().gdn_attn_prefill(ctypes.byref(dims), qp, kp, vp, _index("cu_q", cu_q, (n + 1,), dev),
-                                  _index("cu_k", cu_k, (n + 1,), dev), op, lp, _queue(dev, stream))
+    st = _load().gdn_attn_prefill(ctypes.byref(dims), qp, kp, vp, _index("cu_q", cu_q, (n + 1,), gpu),
+                                  _index("cu_k", cu_k, (n + 1,), gpu), op, lp, _queue(gpu, stream))
     if st:
         raise GdnError(st, "gdn_attn_prefill")
     return out
@@ -655,8 +664,8 @@ def gdn_attn_decode(q, k_cache, v_cache, page_table, lens, *, max_len=None, k_sc
     as for gdn_kv_write. scale defaults to 1 / sqrt(d); lse as for gdn_attn_prefill, [n, h_q].
     Returns out [n, h_q, d] of q's dtype."""
     t = _dtype_id(q)
-    c, dev = _cache_of(k_cache, v_cache, page_table, k_scale, v_scale)
-    qp, qt, qh = _rows("q", q, q.dtype, dev)
+    c, gpu = _cache_of(k_cache, v_cache, page_table, k_scale, v_scale)
+    qp, qt, qh = _rows("q", q, q.dtype, gpu)
     n, hq, d = q.shape
     if n != c.n or d != c.d:
         raise ValueError(f"q must have shape [{c.n}, h_q, {c.d}]")
@@ -666,18 +675,18 @@ def gdn_attn_decode(q, k_cache, v_cache, page_table, lens, *, max_len=None, k_sc
         out = torch.empty_like(q, memory_format=torch.contiguous_format)
         op = out.data_ptr()
     else:
-        op = _dense("out", out, (n, hq, d), q.dtype, dev)
-    lp = None if lse is None else _dense("lse", lse, (n, hq), torch.float32, dev)
+        op = _dense("out", out, (n, hq, d), q.dtype, gpu)
+    lp = None if lse is None else _dense("lse", lse, (n, hq), torch.float32, gpu)
     lib = _load()
     if workspace is None:
         need = lib.gdn_attn_decode_workspace_bytes(ctypes.byref(c), hq, max_len)
         if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    wbytes = 0 if workspace is None else _check_workspace(workspace, dev)
+            workspace = torch.empty(need, dtype=_u8, device=q.device)
+    wbytes = 0 if workspace is None else _check_workspace(workspace, q.device)
     st = lib.gdn_attn_decode(
         ctypes.byref(c), hq, t, d ** -0.5 if scale is None else scale, max_len, qp, qt, qh,
-        _index("lens", lens, (n,), dev), op, lp, None if workspace is None else workspace.data_ptr(),
-        wbytes, _queue(dev, stream))
+        _index("lens", lens, (n,), gpu), op, lp, None if workspace is None else workspace.data_ptr(),
+        wbytes, _queue(gpu, stream))
     if st:
         raise GdnError(st, "gdn_attn_decode")
     return out
