@@ -547,6 +547,17 @@ def _queue(index, stream):
     return _raw_stream(index) if stream is None else stream.cuda_stream
 
 
+def _empty(shape, dtype, index, stream):
+    """A new tensor that the call's stream may write and the current one read: the allocator gives
+    memory out again in the order of the stream it was allocated on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=torch.device("cuda", index))
+    with torch.cuda.stream(stream):
+        x = torch.empty(shape, dtype=dtype, device=torch.device("cuda", index))
+    x.record_stream(torch.cuda.current_stream(index))
+    return x
+
+
 def _gpu(x):
     """Index of x's GPU; a tensor elsewhere gives -1, which no other tensor's matches."""
     return x.get_device() if isinstance(x, _Tensor) and x.is_cuda else -2
@@ -597,9 +608,9 @@ def gdn_kv_read(k_cache, v_cache, page_table, start, cu_seqlens, total, *, dtype
     c, gpu = _cache_of(k_cache, v_cache, page_table, k_scale, v_scale)
     shape = (int(total), c.h_kv, c.d)
     if k_out is None:
-        k_out = torch.empty(shape, dtype=dtype, device=k_cache.device)
+        k_out = _empty(shape, dtype, gpu, stream)
     if v_out is None:
-        v_out = torch.empty_like(k_out)
+        v_out = torch.empty_like(k_out) if stream is None else _empty(shape, dtype, gpu, stream)
     st = _load().gdn_kv_read(
         ctypes.byref(c), shape[0], t, _dense("k_out", k_out, shape, dtype, gpu),
         _dense("v_out", v_out, shape, dtype, gpu), _index("start", start, (c.n,), gpu),
@@ -632,7 +643,8 @@ def gdn_attn_prefill(q, k, v, cu_q, cu_k=None, *, causal=True, scale=None, out=N
     if n < 0:
         raise ValueError("cu_q must be an int32 tensor [n + 1]")
     if out is None:
-        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format) if stream is None \
+            else _empty(q.shape, q.dtype, gpu, stream)
         op = out.data_ptr()
     else:
         op = _dense("out", out, (tq, hq, d), q.dtype, gpu)
@@ -672,7 +684,8 @@ def gdn_attn_decode(q, k_cache, v_cache, page_table, lens, *, max_len=None, k_sc
     if max_len is None:
         max_len = c.max_pages * c.page_size
     if out is None:
-        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format) if stream is None \
+            else _empty(q.shape, q.dtype, gpu, stream)
         op = out.data_ptr()
     else:
         op = _dense("out", out, (n, hq, d), q.dtype, gpu)
@@ -681,7 +694,7 @@ def gdn_attn_decode(q, k_cache, v_cache, page_table, lens, *, max_len=None, k_sc
     if workspace is None:
         need = lib.gdn_attn_decode_workspace_bytes(ctypes.byref(c), hq, max_len)
         if need:
-            workspace = torch.empty(need, dtype=_u8, device=q.device)
+            workspace = _empty(need, _u8, gpu, stream)
     wbytes = 0 if workspace is None else _check_workspace(workspace, q.device)
     st = lib.gdn_attn_decode(
         ctypes.byref(c), hq, t, d ** -0.5 if scale is None else scale, max_len, qp, qt, qh,

@@ -366,6 +366,10 @@ gdn_status gdn_debug_fill_lds(uint32_t pattern, int32_t blocks, uint32_t* sink, 
  * contiguous. Strides are positive multiples of 8 (bf16) or 4 (fp32) elements, and no two
  * heads or tokens may overlap. out, lse and what gdn_kv_read writes are dense.
  *
+ * Limits (beyond them GDN_ERR_SHAPE). Token strides stay below 2^22 elements; n, num_pages,
+ * total * h_kv, n * h_q and max_pages * page_size below 2^31; for gdn_attn_prefill total_k and
+ * total_q * h_q / h_kv below 2^31 - 2^16. Pools and tensors themselves may pass 2^32 bytes.
+ *
  * Alignment. 16 bytes for q, k, v, out, the pools and workspace; 4 for int32 arrays and lse.
  * Aliasing. An output that overlaps any other buffer of the call is GDN_ERR_ALIAS.
  * ====================================================================================== */
@@ -404,9 +408,9 @@ typedef struct {
  * Write new tokens into the cache, quantised as they are written: row cu_seqlens[s] + i of k
  * and v ([total][h_kv][d], strided) goes to position start[s] + i of sequence s. total bounds
  * the rows. cu_seqlens may be NULL (one token per sequence, total == n: a decode step).
- * Positions beyond the page table, or on a page that is not there, are dropped. Two tokens
- * with the same place leave either, not a mixture of rows of different tokens within one
- * element. Everything else in the pools stays as it is.
+ * Positions beyond the page table, or on a page that is not there, are dropped. Two tokens must
+ * not have the same place (what it holds is then unspecified). Everything else in the pools
+ * stays as it is.
  */
 gdn_status gdn_kv_write(const gdn_kv_cache* cache, int64_t total, int32_t dtype, const void* k,
                         int64_t k_token, int64_t k_head, const void* v, int64_t v_token,
@@ -434,7 +438,9 @@ gdn_status gdn_kv_read(const gdn_kv_cache* cache, int64_t total, int32_t dtype, 
  *   lse [total_q][h_q] fp32, or NULL. cu_q, cu_k: the two packings (cu_k NULL: the same as
  *   cu_q, and total_k == total_q).
  * Scores, softmax statistics and sums are fp32; with bf16 inputs the softmax weights are
- * rounded to bf16 for the matrix product with V, with fp32 inputs nothing is rounded.
+ * rounded to bf16 for the matrix product with V, with fp32 inputs nothing is rounded. A row is
+ * divided by the sum of the weights that were multiplied, so that they add up to 1. A NaN
+ * among what a row sees reaches its output.
  */
 typedef struct {
     int64_t n;       /* sequences                                                */
@@ -459,10 +465,10 @@ gdn_status gdn_attn_prefill(const gdn_attn_dims* dims, const void* q, const void
  * new token's own, written before, among them). out [n][h_q][d] of dtype; lse [n][h_q] fp32
  * or NULL. lens[s] <= 0 gives o = 0, lse = -inf. max_len is the caller's bound on lens, which
  * the host cannot see: positions from max_len on are not read; the work is split over it.
- * A long cache is split into ranges that are attended to separately and joined in a second
- * pass, in a fixed order, so results are the same from run to run. workspace:
- * gdn_attn_decode_workspace_bytes(cache, h_q, max_len) bytes (0 when nothing is split, and
- * for invalid arguments).
+ * A long cache is split into ranges that are attended to separately and joined by a second
+ * kernel, in a fixed order, so results are the same from run to run. Rounding and NaN as for
+ * gdn_attn_prefill. workspace: gdn_attn_decode_workspace_bytes(cache, h_q, max_len) bytes (0
+ * when nothing is split, and for invalid arguments).
  */
 size_t gdn_attn_decode_workspace_bytes(const gdn_kv_cache* cache, int32_t h_q, int64_t max_len);
 gdn_status gdn_attn_decode(const gdn_kv_cache* cache, int32_t h_q, int32_t dtype, float scale,

@@ -183,6 +183,35 @@ def test_the_same_twice_and_in_a_graph():
         assert torch.equal(out, want), step
 
 
+def test_memory_of_a_call_on_another_stream():
+    """With stream=, the outputs and workspace that a call makes are that stream's: what the current
+    stream allocates and writes while the call waits there does not reach them, and the call
+    does not write what the current stream has freed and still reads."""
+    lens = [3000, 2000]
+    cache = Cache(lens, 64, 2, 128, BF)
+    fill(cache, 12)
+    q = queries(2, 16, 128, BF).to(DEV)
+    ln, start, cu = ints(lens), ints([0, 0]), ints([0, 3000, 5000])
+    want = gdn.gdn_attn_decode(q, *cache.args(), ln, max_len=3000)
+    wk, wv = gdn.gdn_kv_read(*cache.args(), start, cu, 5000)
+    wp = gdn.gdn_attn_prefill(wk.repeat(1, 8, 1), wk, wv, cu)
+    long_q = wk.repeat(1, 8, 1)
+    torch.cuda.synchronize()
+    need = gdn.gdn_attn_decode_workspace_bytes(2, cache.page_table.shape[1], 64, 16, 2, 128, 3000)
+    assert need > 0
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(10_000_000)  # some milliseconds: the calls below wait behind it
+    out = gdn.gdn_attn_decode(q, *cache.args(), ln, max_len=3000, stream=s)
+    k, v = gdn.gdn_kv_read(*cache.args(), start, cu, 5000, stream=s)
+    p = gdn.gdn_attn_prefill(long_q, wk, wv, cu, stream=s)
+    bad = [torch.full((size,), 0xff, dtype=torch.uint8, device=DEV)
+           for size in (need, need, out.numel() * 2, k.numel() * 2, k.numel() * 2, p.numel() * 2)]
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and torch.equal(k, wk) and torch.equal(v, wv) and torch.equal(p, wp)
+    assert all(bool((x == 0xff).all()) for x in bad)
+
+
 def test_refusals():
     cache = Cache([40], 16, 2, 64, BF)
     q = torch.zeros(1, 4, 64, dtype=BF, device=DEV)
