@@ -106,7 +106,8 @@ def _load():
         "gdn_prefill_segmented_noalloc": (ctypes.c_int, [D, ctypes.c_int64] + [P] * 9),
         "gdn_kv_write": (ctypes.c_int, [K, i64, i32, P, i64, i64, P, i64, i64, P, P, P]),
         "gdn_kv_read": (ctypes.c_int, [K, i64, i32, P, P, P, P, P]),
-        "gdn_attn_prefill": (ctypes.c_int, [ctypes.POINTER(AttnDims)] + [P] * 8),
+        "gdn_attn_prefill_workspace_bytes": (sz, [ctypes.POINTER(AttnDims)]),
+        "gdn_attn_prefill": (ctypes.c_int, [ctypes.POINTER(AttnDims)] + [P] * 8 + [sz, P]),
         "gdn_attn_decode_workspace_bytes": (sz, [K, i32, i64]),
         "gdn_attn_decode": (ctypes.c_int, [K, i32, i32, ctypes.c_float, i64, P, i64, i64, P, P, P,
                                            P, sz, P]),
@@ -621,7 +622,7 @@ def gdn_kv_read(k_cache, v_cache, page_table, start, cu_seqlens, total, *, dtype
 
 
 def gdn_attn_prefill(q, k, v, cu_q, cu_k=None, *, causal=True, scale=None, out=None, lse=None,
-                     stream=None):
+                     workspace=None, stream=None):
     """Attention over packed prompts, with grouped heads.
 
     q [total_q, h_q, d], k and v [total_k, h_kv, d] (bfloat16 or float32; tokens and heads may be
@@ -651,8 +652,15 @@ def gdn_attn_prefill(q, k, v, cu_q, cu_k=None, *, causal=True, scale=None, out=N
     lp = None if lse is None else _dense("lse", lse, (tq, hq), torch.float32, gpu)
     dims = AttnDims(n, tq, tk, hq, hk, d, t, 1 if causal else 0, d ** -0.5 if scale is None else scale,
                     qt, qh, kt, kh, vt, vh)
-    st = _load().gdn_attn_prefill(ctypes.byref(dims), qp, kp, vp, _index("cu_q", cu_q, (n + 1,), gpu),
-                                  _index("cu_k", cu_k, (n + 1,), gpu), op, lp, _queue(gpu, stream))
+    lib = _load()
+    if workspace is None:
+        need = lib.gdn_attn_prefill_workspace_bytes(ctypes.byref(dims))
+        if need:
+            workspace = _empty(need, _u8, gpu, stream)
+    wbytes = 0 if workspace is None else _check_workspace(workspace, q.device)
+    st = lib.gdn_attn_prefill(ctypes.byref(dims), qp, kp, vp, _index("cu_q", cu_q, (n + 1,), gpu),
+                              _index("cu_k", cu_k, (n + 1,), gpu), op, lp,
+                              None if workspace is None else workspace.data_ptr(), wbytes, _queue(gpu, stream))
     if st:
         raise GdnError(st, "gdn_attn_prefill")
     return out

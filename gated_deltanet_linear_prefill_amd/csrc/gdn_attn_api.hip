@@ -120,6 +120,29 @@ gdn_status check_rows(const gdn_kv_cache* c, int64_t total, int32_t dtype, const
     return GDN_OK;
 }
 
+// What the sizes and strides of a prefill call have to be; *rows the query rows, *qe, *ke, *ve the
+// tensors' extents.
+gdn_status check_prefill(const gdn_attn_dims* d, int64_t* rows, int64_t* qe, int64_t* ke, int64_t* ve)
+{
+    if (!d) return GDN_ERR_NULL;
+    if (d->n < 0 || d->total_q < 0 || d->total_k < 0 || d->h_q <= 0 || d->h_kv <= 0 || d->d <= 0)
+        return GDN_ERR_SHAPE;
+    if (d->h_q % d->h_kv != 0 || (d->causal != 0 && d->causal != 1) || !isfinite(d->scale))
+        return GDN_ERR_SHAPE;
+    if (!attn_dtype(d->dtype) || !attn_d(d->d)) return GDN_ERR_UNSUPPORTED;
+    const int64_t lim = INT64_C(1) << 31;
+    const int64_t rows_lim = lim - (1 << 16);  // the kernels count rows and keys in 32 bits
+    if (d->n >= lim || d->total_q >= rows_lim || d->total_k >= rows_lim) return GDN_ERR_SHAPE;
+    if (!mul_ok(d->total_q, d->h_q, rows) || *rows / d->h_kv >= rows_lim) return GDN_ERR_SHAPE;
+    // the grid: (tiles of query rows) x (KV heads), see the kernel
+    if ((*rows / d->h_kv / attn_prefill_rows(d->d, d->dtype) + d->n) * d->h_kv >= lim) return GDN_ERR_SHAPE;
+    if (!strided(d->total_q, d->h_q, d->d, d->q_token, d->q_head, d->dtype, qe) ||
+        !strided(d->total_k, d->h_kv, d->d, d->k_token, d->k_head, d->dtype, ke) ||
+        !strided(d->total_k, d->h_kv, d->d, d->v_token, d->v_head, d->dtype, ve))
+        return GDN_ERR_SHAPE;
+    return GDN_OK;
+}
+
 }  // namespace
 }  // namespace gdn
 
@@ -192,41 +215,36 @@ gdn_status gdn_kv_read(const gdn_kv_cache* c, int64_t total, int32_t dtype, void
     return finish(launch_kv_read(call));
 }
 
-gdn_status gdn_attn_prefill(const gdn_attn_dims* d, const void* q, const void* k, const void* v,
-                            const int32_t* cu_q, const int32_t* cu_k, void* out, float* lse,
-                            void* stream)
+size_t gdn_attn_prefill_workspace_bytes(const gdn_attn_dims* d)
 {
-    if (!d) return GDN_ERR_NULL;
-    if (d->n < 0 || d->total_q < 0 || d->total_k < 0 || d->h_q <= 0 || d->h_kv <= 0 || d->d <= 0)
-        return GDN_ERR_SHAPE;
-    if (d->h_q % d->h_kv != 0 || (d->causal != 0 && d->causal != 1) || !isfinite(d->scale))
-        return GDN_ERR_SHAPE;
-    if (!cu_k && d->total_k != d->total_q) return GDN_ERR_SHAPE;
-    if (!attn_dtype(d->dtype) || !attn_d(d->d)) return GDN_ERR_UNSUPPORTED;
-    const int64_t lim = INT64_C(1) << 31;
     int64_t rows, qe, ke, ve;
-    const int64_t rows_lim = lim - (1 << 16);  // the kernels count rows and keys in 32 bits
-    if (d->n >= lim || d->total_q >= rows_lim || d->total_k >= rows_lim) return GDN_ERR_SHAPE;
-    if (!mul_ok(d->total_q, d->h_q, &rows) || rows / d->h_kv >= rows_lim) return GDN_ERR_SHAPE;
-    // the grid: (tiles of query rows) x (KV heads), see the kernel
-    if ((rows / d->h_kv / attn_prefill_rows(d->d, d->dtype) + d->n) * d->h_kv >= lim) return GDN_ERR_SHAPE;
-    if (!strided(d->total_q, d->h_q, d->d, d->q_token, d->q_head, d->dtype, &qe) ||
-        !strided(d->total_k, d->h_kv, d->d, d->k_token, d->k_head, d->dtype, &ke) ||
-        !strided(d->total_k, d->h_kv, d->d, d->v_token, d->v_head, d->dtype, &ve))
-        return GDN_ERR_SHAPE;
+    return check_prefill(d, &rows, &qe, &ke, &ve) == GDN_OK ? attn_prefill_workspace(*d) : 0;
+}
+
+gdn_status gdn_attn_prefill(const gdn_attn_dims* d, const void* q, const void* k, const void* v,
+                            const int32_t* cu_q, const int32_t* cu_k, void* out, float* lse, void* ws,
+                            size_t ws_bytes, void* stream)
+{
+    int64_t rows, qe, ke, ve;
+    const gdn_status st = check_prefill(d, &rows, &qe, &ke, &ve);
+    if (st != GDN_OK) return st;
+    if (!cu_k && d->total_k != d->total_q) return GDN_ERR_SHAPE;
     const bool work = d->n > 0 && d->total_q > 0;
     if (work && (!q || !out || !cu_q || (d->total_k > 0 && (!k || !v)))) return GDN_ERR_NULL;
-    for (const void* p : {q, k, v, (const void*)out})
+    for (const void* p : {q, k, v, (const void*)out, (const void*)ws})
         if (!aligned(p, 16)) return GDN_ERR_ALIGN;
     if (!aligned(cu_q, 4) || !aligned(cu_k, 4) || !aligned(lse, 4)) return GDN_ERR_ALIGN;
     const size_t es = elem(d->dtype);
+    const size_t need = work ? attn_prefill_workspace(*d) : 0;
+    if (need > 0 && (!ws || ws_bytes < need)) return GDN_ERR_WORKSPACE;
     const Range r[] = {range_of(out, rows * d->d, es), range_of(lse, lse ? rows : 0, 4),
-                       range_of(q, qe, es), range_of(k, ke, es), range_of(v, ve, es),
+                       range_of(need ? ws : nullptr, (int64_t)need, 1), range_of(q, qe, es), range_of(k, ke, es), range_of(v, ve, es),
                        range_of(cu_q, work ? d->n + 1 : 0, 4), range_of(cu_k, cu_k && work ? d->n + 1 : 0, 4)};
-    if (any_overlap(r[0], r + 1, 6) || any_overlap(r[1], r + 2, 5)) return GDN_ERR_ALIAS;
+    for (int i = 0; i < 3; ++i)
+        if (any_overlap(r[i], r + i + 1, 7 - i)) return GDN_ERR_ALIAS;
     if (!work) return GDN_OK;
-    const AttnCall call = {*d, q, k, v, cu_q, cu_k ? cu_k : cu_q, out, lse,
-                           static_cast<hipStream_t>(stream)};
+    const AttnCall call = {*d, q, k, v, cu_q, cu_k ? cu_k : cu_q, out, lse, ws,
+                           static_cast<hipStream_t>(stream), 1, nullptr, nullptr};
     (void)hipGetLastError();
     return finish(launch_attn_prefill(call));
 }

@@ -24,7 +24,13 @@ struct AttnCall {
     const int32_t *cu_q, *cu_k;
     void* out;
     float* lse;
+    void* ws;
     hipStream_t stream;
+    // Set by the launcher: ranges of a tile's keys, and where their sums go, [unit][range][row]: o
+    // [d] and (m, l, exact l, -).
+    int ranges;
+    float* part_o;
+    float4* part_ml;
 };
 
 struct AttnDecodeCall {
@@ -48,6 +54,8 @@ hipError_t launch_attn_decode(const AttnDecodeCall& c);
 
 // Query rows (positions x heads of a KV head) a prefill workgroup handles, for the grid bound.
 int attn_prefill_rows(int32_t d, int32_t dtype);
+// Workspace of a checked prefill call with n > 0 (0: not split).
+size_t attn_prefill_workspace(const gdn_attn_dims& d);
 // Workspace of a decode call (0: not split), from the sizes the host knows.
 size_t attn_decode_workspace(const gdn_kv_cache* c, int32_t h_q, int64_t max_len);
 

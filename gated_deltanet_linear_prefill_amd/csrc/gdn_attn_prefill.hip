@@ -49,20 +49,24 @@ struct Tile {
 
 // How a workgroup is made up: its waves, the steps that are staged at a time, and over how many
 // groups of waves the steps are divided.
-template <int WAVES_, int STEPS_, int SPLIT_, int PER_SIMD_>
+template <int WAVES_, int STEPS_, int SPLIT_, int PER_SIMD_, bool RANGES_ = false>
 struct Shape {
     static constexpr int WAVES = WAVES_, STEPS = STEPS_, SPLIT = SPLIT_, ROWS = 32 * WAVES / SPLIT;
     static constexpr int PER_SIMD = PER_SIMD_;  // waves that a SIMD should hold
+    static constexpr bool RANGES = RANGES_;     // a tile's keys may be divided over workgroups
 };
 // 256 rows share every staged key: the least traffic, for long work.
 using Wide = Shape<8, 2, 1, 2>;
 // 128 rows; half the waves take the first of two steps and half the second, and are joined at the
 // end: half the time per workgroup, for calls that have too few tiles to keep all CUs busy evenly.
 using Split = Shape<8, 2, 2, 2>;
+// 64 rows in the same way, one wave a SIMD, and the keys of a tile over several workgroups whose
+// sums are joined by a second kernel: for calls whose few tiles leave most CUs idle.
+using Few = Shape<4, 2, 2, 1, true>;
 // 128 rows, two workgroups a CU: one starts and ends while the other computes, for many short tiles.
 using Twin = Shape<4, 1, 1, 2>;
 // fp32 with d = 256, where a wave's O and Q take all of 256 registers.
-using Lone = Shape<4, 1, 1, 1>;
+using Lone = Shape<4, 1, 1, 1, true>;
 
 // A workgroup's tile: its sequence's rows and keys, and its own first row. The host keeps
 // rows and keys below 2^31 - 2^16.
@@ -115,6 +119,14 @@ __device__ __forceinline__ bool find_work(const AttnCall& p, int tile, int head,
 __device__ __forceinline__ int key_limit(const Work& w, int pos, int causal)
 {
     return causal ? clamp_to(pos + 1 + w.len_k - w.len_q, w.len_k) : w.len_k;
+}
+
+// Keys of one of `ranges` ranges of a tile's keys: whole units, not below 256. ranges is at most 64,
+// so that the end of the last stays below 2^31.
+__device__ __forceinline__ int range_keys(int keys, int ranges, int unit)
+{
+    const int per = (keys + ranges - 1) / ranges;
+    return ((per < 256 ? 256 : per) + unit - 1) / unit * unit;
 }
 
 __device__ __forceinline__ float other_half_max(float x)
@@ -430,7 +442,8 @@ __global__ void __launch_bounds__(64 * S::WAVES, S::PER_SIMD) prefill_kernel(Att
     const int half = lane >> 5;
     const int rw = wave % (S::WAVES / SPLIT), turn = wave / (S::WAVES / SPLIT);  // 32 rows, steps
     Work w;
-    if (!find_work<M>(p, blockIdx.x / p.d.h_kv, blockIdx.x % p.d.h_kv, lane, &w)) return;
+    const int units = S::RANGES ? gridDim.x / p.ranges : gridDim.x, unit = blockIdx.x % units, rg = blockIdx.x / units;
+    if (!find_work<M>(p, unit / p.d.h_kv, unit % p.d.h_kv, lane, &w)) return;
 
     const int64_t ks = ES * p.d.k_token, vs = ES * p.d.v_token;
     const char* kb = static_cast<const char*>(p.k) + w.k0 * ks + ES * w.head * p.d.k_head;
@@ -443,9 +456,10 @@ __global__ void __launch_bounds__(64 * S::WAVES, S::PER_SIMD) prefill_kernel(Att
     const int klane = lane % C::GROUPS * C::KG + lane % 32 / C::GROUPS * C::ROWB + half * 16;
     const int vlane = ES == 2 ? (4 * half + ((lane >> 2) & 3)) * C::VG + ((lane >> 4) & 1) * 32 + (lane & 3) * 8
                               : 4 * half * C::VG + lane % 32 * 4;
+    int valid = w.len_k;
     auto fetch = [&](int row, char* sk, char* sv) __attribute__((always_inline)) {
-        stage<T, D, S, C::KG>(kb, row, w.len_k, ks, sk, wave, koff);
-        stage<T, D, S, C::VG>(vb, row, w.len_k, vs, sv, wave, voff);
+        stage<T, D, S, C::KG>(kb, row, valid, ks, sk, wave, koff);
+        stage<T, D, S, C::VG>(vb, row, valid, vs, sv, wave, voff);
     };
 
     // keys that a row sees: the workgroup's last row and all of its rows; the last of the wave's
@@ -454,13 +468,27 @@ __global__ void __launch_bounds__(64 * S::WAVES, S::PER_SIMD) prefill_kernel(Att
         return key_limit(w, (int)((uint32_t)(row < w.rows ? row : w.rows - 1) / (uint32_t)w.g), p.d.causal);
     };
     const int wfirst = w.row0 + 32 * rw;
-    const int keys = limit_of(w.row0 + M - 1), all = limit_of(w.row0);
+    int keys = limit_of(w.row0 + M - 1), all = limit_of(w.row0);
+    // With ranges: from here on a key's number is its distance from `begin`, the range's first.
+    int begin = 0;
+    bool whole = true;
+    if constexpr (S::RANGES) {
+        const int per = range_keys(keys, p.ranges, UNIT);
+        begin = rg * per;
+        if (rg > 0 && begin >= keys) return;  // the join does not read this range
+        whole = keys <= per;
+        keys = keys - begin < per ? keys - begin : per;
+        all = all - begin < keys ? all - begin : keys;
+        valid -= begin;
+        kb += begin * ks;
+        vb += begin * vs;
+    }
     if (keys > 0) fetch(0, s_k0, s_v0);
-    const int wkeys = wfirst < w.rows ? limit_of(wfirst + 31) : 0, wall = limit_of(wfirst);
+    const int wkeys = (wfirst < w.rows ? limit_of(wfirst + 31) : 0) - begin, wall = limit_of(wfirst) - begin;
 
     // this lane's query: row r of the sequence's packed rows
     const int r = wfirst + (lane & 31), rc = r < w.rows ? r : w.rows - 1, pos = (int)((uint32_t)rc / (uint32_t)w.g);
-    const int limit = key_limit(w, pos, p.d.causal);
+    const int limit = key_limit(w, pos, p.d.causal) - begin;
     const char* qp = static_cast<const char*>(p.q) +
                      ES * ((w.q0 + pos) * p.d.q_token + (w.head * w.g + (rc - pos * w.g)) * p.d.q_head) + 16 * half;
     // A negative scale becomes a positive one of the negated query: the maximum of the raw scores
@@ -568,9 +596,26 @@ __global__ void __launch_bounds__(64 * S::WAVES, S::PER_SIMD) prefill_kernel(Att
 #pragma unroll
             for (int i = 0; i < 16; ++i) o[db][i] = a0 * o[db][i] + a1 * so[(16 * db + i) * 64 + lane];
     }
+    if constexpr (S::RANGES) {
+        if (!whole) {  // this range's sums, for the join
+            const float l = other_half_sum(st.l), e = ES == 2 && LSE ? other_half_sum(st.exact) : l;
+            const int64_t at = ((int64_t)unit * p.ranges + rg) * M + 32 * rw + (lane & 31);
+            if (r < w.rows) {
+                float* to = p.part_o + at * D + 4 * half;
+#pragma unroll
+                for (int db = 0; db < ND; ++db)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        *reinterpret_cast<f32x4_t*>(to + 32 * db + 8 * i) =
+                            f32x4_t{o[db][4 * i], o[db][4 * i + 1], o[db][4 * i + 2], o[db][4 * i + 3]};
+                if (half == 0) p.part_ml[at] = make_float4(st.m * c, l, e, 0.f);
+            }
+            return;
+        }
+    }
     // All waves have met since the last use of K and V: each has a part of the buffers to itself (with
     // SPLIT 2 in the one where it read the other half's O).
-    constexpr int PART = 32 * ((C::ROWB < 256 ? C::ROWB : 256) + 16), PER_BUFFER = M / 32 / 4;
+    constexpr int PART = 32 * ((C::ROWB < 256 ? C::ROWB : 256) + 16), PER_BUFFER = (M / 32 + 3) / 4;
     static_assert(PER_BUFFER * PART <= S::STEPS * C::GROUPS * C::KG, "the waves' parts fit the buffers");
     const int buffer = rw / PER_BUFFER;
     char* part = buffer == 0 ? s_k0 : buffer == 1 ? s_k1 : buffer == 2 ? s_v0 : s_v1;
@@ -578,21 +623,126 @@ __global__ void __launch_bounds__(64 * S::WAVES, S::PER_SIMD) prefill_kernel(Att
     write_rows<T, D>(p, w, wfirst, lane, o, st, part + rw % PER_BUFFER * PART);
 }
 
-template <typename T, int D, bool LSE, typename S>
-hipError_t launch_kernel(const AttnCall& c)
+constexpr int kMaxRanges = 64;
+
+// Joins the ranges of a tile: D / 4 lanes hold a row, first one range each for the weights
+// exp2(m - max m), then four elements each of the weighted sum, in the order of the ranges.
+template <typename T, int D, typename S>
+__global__ void __launch_bounds__(256) join_kernel(AttnCall p)
 {
-    const int64_t tiles = c.d.total_q * (c.d.h_q / c.d.h_kv) / S::ROWS + c.d.n;
-    hipLaunchKernelGGL((prefill_kernel<T, D, LSE, S>), dim3((unsigned)(tiles * c.d.h_kv)), dim3(64 * S::WAVES), 0,
-                       c.stream, c);
-    return hipGetLastError();
+    constexpr int M = S::ROWS, LANES = D / 4, ROWS = 256 / LANES;
+    __shared__ float s_w[ROWS][kMaxRanges];
+    const int unit = blockIdx.x / (M / ROWS), mine = threadIdx.x / LANES, lane = threadIdx.x % LANES;
+    const int row = blockIdx.x % (M / ROWS) * ROWS + mine;
+    Work w;
+    if (!find_work<M>(p, unit / p.d.h_kv, unit % p.d.h_kv, threadIdx.x & 63, &w)) return;
+    const int last = w.row0 + M - 1, keys = key_limit(w, (last < w.rows ? last : w.rows - 1) / w.g, p.d.causal);
+    const int per = range_keys(keys, p.ranges, S::STEPS * Tile<T, D>::N), r = w.row0 + row;
+    if (keys <= per || r - mine >= w.rows) return;
+    const int used = (keys + per - 1) / per;
+    const int64_t at = (int64_t)unit * p.ranges * M + row;
+    float top = -INFINITY, l = 0.f, e = 0.f;
+    if (r < w.rows) {
+        constexpr int EACH = kMaxRanges / LANES;
+        float4 ml[EACH];
+#pragma unroll
+        for (int i = 0; i < EACH; ++i) {
+            const int x = i * LANES + lane;
+            ml[i] = x < used ? p.part_ml[at + x * M] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+            top = fmaxf(top, ml[i].x);
+        }
+#pragma unroll
+        for (int off = LANES / 2; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, 64));
+#pragma unroll
+        for (int i = 0; i < EACH; ++i) {
+            const float f = ml[i].x == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(ml[i].x - top);
+            s_w[mine][i * LANES + lane] = f;
+            l += ml[i].y * f;
+            e += ml[i].z * f;
+        }
+#pragma unroll
+        for (int off = LANES / 2; off >= 1; off >>= 1) {
+            l += __shfl_xor(l, off, 64);
+            e += __shfl_xor(e, off, 64);
+        }
+    }
+    __syncthreads();
+    if (r >= w.rows) return;
+    const float* from = p.part_o + at * D + lane * 4;
+    f32x4_t o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 16
+    for (int x = 0; x < used; ++x) o += *reinterpret_cast<const f32x4_t*>(from + (int64_t)x * M * D) * s_w[mine][x];
+    o *= l > 0.f ? 1.f / l : (l == l ? 0.f : l);
+    const int pos = r / w.g;
+    const int64_t to = (w.q0 + pos) * p.d.h_q + w.head * w.g + (r - pos * w.g);
+    T* out = static_cast<T*>(p.out) + to * D + lane * 4;
+    if constexpr (sizeof(T) == 2) *reinterpret_cast<u32x2_t*>(out) = u32x2_t{pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3])};
+    else *reinterpret_cast<f32x4_t*>(out) = o;
+    if (p.lse && lane == 0) p.lse[to] = e > 0.f ? (top + __builtin_amdgcn_logf(e)) * kLn2 : (e == e ? -INFINITY : e);
+}
+
+int64_t units_of(const gdn_attn_dims& d, int rows)
+{
+    return (d.total_q * (d.h_q / d.h_kv) / rows + d.n) * d.h_kv;
+}
+
+int range_rows(const gdn_attn_dims& d)  // of the shape with ranges
+{
+    return d.dtype == GDN_F32 && d.d == 256 ? Lone::ROWS : Few::ROWS;
+}
+
+// Ranges that every tile's keys are divided into: what makes the estimate of the call's time least.
+// 256 workgroups run at a time; each costs its keys and about 128 more, and a join about 256 (a key
+// takes some 20 ns, d = 256 bf16). Undivided, a workgroup takes 128 rows. Measured (us of a call,
+// undivided / divided): d = 256, 16/2 heads, 16 tokens after 32752 684 / 56, 128 after 32640 686 / 109,
+// 512 after 8192 195 / 114; d = 128, 32/8 heads, 8 sequences of 8 tokens after 8192 134 / 85.
+int ranges_of(const gdn_attn_dims& d)
+{
+    if (d.n == 0 || d.total_q == 0) return 1;
+    const int rows = range_rows(d);
+    const int64_t all = d.total_q * (d.h_q / d.h_kv), keys = d.total_k / d.n;
+    auto units = [&](int m) { return ((all + m - 1) / m > d.n ? (all + m - 1) / m : d.n) * d.h_kv; };
+    const int64_t u = units(rows), most = units_of(d, rows);
+    int best = 1;
+    int64_t least = (units(128) + 255) / 256 * (keys + 128);
+    for (int64_t r = 2; r <= kMaxRanges && most * r <= 1024 && keys >= 256 * r; ++r) {
+        const int64_t cost = (u * r + 255) / 256 * (keys / r + 128) + 256 + 4 * r;
+        if (cost < least) {
+            least = cost;
+            best = (int)r;
+        }
+    }
+    return best;
+}
+
+template <typename T, int D, bool LSE, typename S>
+hipError_t launch_kernel(const AttnCall& c, int ranges = 1)
+{
+    const int64_t units = units_of(c.d, S::ROWS);
+    AttnCall a = c;
+    a.ranges = ranges;
+    a.part_o = static_cast<float*>(c.ws);
+    a.part_ml = reinterpret_cast<float4*>(a.part_o + units * ranges * S::ROWS * D);
+    hipLaunchKernelGGL((prefill_kernel<T, D, LSE, S>), dim3((unsigned)(units * ranges)), dim3(64 * S::WAVES), 0,
+                       c.stream, a);
+    const hipError_t e = hipGetLastError();
+    if constexpr (S::RANGES)
+        if (e == hipSuccess && ranges > 1) {
+            hipLaunchKernelGGL((join_kernel<T, D, S>), dim3((unsigned)(units * (S::ROWS * D / 1024))), dim3(256), 0,
+                               c.stream, a);
+            return hipGetLastError();
+        }
+    return e;
 }
 
 template <typename T, int D, bool LSE>
 hipError_t launch_shape(const AttnCall& c)
 {
+    const int ranges = ranges_of(c.d);
     if constexpr (Tile<T, D>::ROWS == 1) {
-        return launch_kernel<T, D, LSE, Lone>(c);
+        return launch_kernel<T, D, LSE, Lone>(c, ranges);
     } else {
+        if (ranges > 1) return launch_kernel<T, D, LSE, Few>(c, ranges);
         // Measured (us, bf16, Wide / Split / Twin; tiles of 256 rows). Few tiles of many keys, where
         // one workgroup's time is the call's: d = 256, 16/2 heads, 4096-token prompt (256 tiles)
         // 190 / 144 / 169, 2048 (128) 98 / 62 / 74; d = 128, 16/16 heads, 4096 (256) 109 / 79 / 91.
@@ -600,6 +750,9 @@ hipError_t launch_shape(const AttnCall& c)
         // 205 / 270 / 193, 8192 (1024) 513 / 542 / 504. Long rows and many keys, where the traffic
         // of staging counts: d = 256, 8192 (512) 472 / 508 / 512, 16 of 1024 197 / 270 / 191.
         const int64_t tiles = c.d.total_q * c.d.h_q / 256, keys = c.d.total_k / c.d.n;
+        // fp32, Twin / Few: three prompts of up to 200, d = 64 22.3 / 17.9, 1024 tokens, 16/2 heads, d = 128
+        // (64) 131 / 79. bf16 gains 5% at 512 tokens and loses as much at eight of 64.
+        if (sizeof(T) == 4 && tiles <= 64) return launch_kernel<T, D, LSE, Few>(c);
         if (tiles <= 256 && keys >= 1024) return launch_kernel<T, D, LSE, Split>(c);
         if constexpr (Tile<T, D>::ROWS == 2 && sizeof(T) == 2)
             if (keys >= 8192) return launch_kernel<T, D, LSE, Wide>(c);
@@ -616,9 +769,15 @@ hipError_t launch_d(const AttnCall& c)
 
 }  // namespace
 
+size_t attn_prefill_workspace(const gdn_attn_dims& d)
+{
+    const int ranges = ranges_of(d), rows = range_rows(d);
+    return ranges == 1 ? 0 : (size_t)(units_of(d, rows) * ranges * rows) * (d.d * sizeof(float) + sizeof(float4));
+}
+
 int attn_prefill_rows(int32_t, int32_t)
 {
-    return 128;  // the smallest of the kernels' tiles
+    return 64;  // the smallest of the kernels' tiles
 }
 
 hipError_t launch_attn_prefill(const AttnCall& c)

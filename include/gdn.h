@@ -441,6 +441,9 @@ gdn_status gdn_kv_read(const gdn_kv_cache* cache, int64_t total, int32_t dtype, 
  * rounded to bf16 for the matrix product with V, with fp32 inputs nothing is rounded. A row is
  * divided by the sum of the weights that were multiplied, so that they add up to 1. A NaN
  * among what a row sees reaches its output.
+ * Where few rows meet many keys the keys are divided into ranges that a second kernel joins, in
+ * a fixed order: workspace then has gdn_attn_prefill_workspace_bytes(dims) bytes (0 when
+ * nothing is divided, and for invalid arguments).
  */
 typedef struct {
     int64_t n;       /* sequences                                                */
@@ -455,9 +458,10 @@ typedef struct {
     int64_t q_token, q_head, k_token, k_head, v_token, v_head; /* strides, in elements */
 } gdn_attn_dims;
 
+size_t gdn_attn_prefill_workspace_bytes(const gdn_attn_dims* dims);
 gdn_status gdn_attn_prefill(const gdn_attn_dims* dims, const void* q, const void* k,
                             const void* v, const int32_t* cu_q, const int32_t* cu_k, void* out,
-                            float* lse, void* stream);
+                            float* lse, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * Attention of one new token per sequence over the cache: query row s of q ([n][h_q][d], its

@@ -56,13 +56,13 @@ int main()
     expect("decode: workspace", gdn_attn_decode(&lng, 4, GDN_BF16, 0.1f, huge, at(4), 256, 64, i32(6), at(5), nullptr, at(8), need - 1, nullptr), GDN_ERR_WORKSPACE);
     expect("decode: scale", gdn_attn_decode(&c, 4, GDN_BF16, NAN, 64, at(4), 256, 64, i32(6), at(5), nullptr, nullptr, 0, nullptr), GDN_ERR_SHAPE);
     gdn_attn_dims d = {2, 10, 20, 4, 2, 64, GDN_BF16, 1, 0.125f, 256, 64, 128, 64, 128, 64};
-    expect("prefill: null", gdn_attn_prefill(&d, at(1), nullptr, at(3), i32(5), i32(6), at(4), nullptr, nullptr), GDN_ERR_NULL);
+    expect("prefill: null", gdn_attn_prefill(&d, at(1), nullptr, at(3), i32(5), i32(6), at(4), nullptr, nullptr, 0, nullptr), GDN_ERR_NULL);
     d.total_q = huge;
-    expect("prefill: total", gdn_attn_prefill(&d, at(1), at(2), at(3), i32(5), i32(6), at(4), nullptr, nullptr), GDN_ERR_SHAPE);
+    expect("prefill: total", gdn_attn_prefill(&d, at(1), at(2), at(3), i32(5), i32(6), at(4), nullptr, nullptr, 0, nullptr), GDN_ERR_SHAPE);
     d.total_q = 10;
     d.h_q = 0x7ffffffe;
     d.h_kv = 2;
-    expect("prefill: heads", gdn_attn_prefill(&d, at(1), at(2), at(3), i32(5), i32(6), at(4), nullptr, nullptr), GDN_ERR_SHAPE);
+    expect("prefill: heads", gdn_attn_prefill(&d, at(1), at(2), at(3), i32(5), i32(6), at(4), nullptr, nullptr, 0, nullptr), GDN_ERR_SHAPE);
     std::printf("attention driver ok\n");
     return 0;
 }

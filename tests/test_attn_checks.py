@@ -99,12 +99,12 @@ def test_calls_without_work(lib):
     assert read(lib, cache(n=0), total=0, k=None, v=None, start=None, cu=None) == OK
 
 
-def prefill(lib, lse=None, out=addr(4), q=addr(1), k=addr(2), v=addr(3), cu_q=addr(5), cu_k=addr(6), **over):
+def prefill(lib, lse=None, ws=None, ws_bytes=0, out=addr(4), q=addr(1), k=addr(2), v=addr(3), cu_q=addr(5), cu_k=addr(6), **over):
     a = dict(n=2, total_q=10, total_k=20, h_q=4, h_kv=2, d=64, dtype=gdn.GDN_BF16, causal=1, scale=0.125, q_token=256,
              q_head=64, k_token=128, k_head=64, v_token=128, v_head=64)
     a.update(over)
     d = gdn.AttnDims(*[a[f] for f, _ in gdn.AttnDims._fields_])
-    return lib.gdn_attn_prefill(ctypes.byref(d), q, k, v, cu_q, cu_k, out, lse, None)
+    return lib.gdn_attn_prefill(ctypes.byref(d), q, k, v, cu_q, cu_k, out, lse, ws, ws_bytes, None)
 
 
 @pytest.mark.parametrize("over,status", [
@@ -116,7 +116,9 @@ def prefill(lib, lse=None, out=addr(4), q=addr(1), k=addr(2), v=addr(3), cu_q=ad
     (dict(q=None), NULL), (dict(k=None), NULL), (dict(out=None), NULL), (dict(cu_q=None), NULL),
     (dict(q=addr(1) + 8), ALIGN), (dict(lse=addr(7) + 2), ALIGN), (dict(cu_k=addr(6) + 1), ALIGN),
     (dict(out=addr(1)), ALIAS), (dict(out=addr(3) + 256), ALIAS), (dict(lse=addr(2)), ALIAS), (dict(lse=addr(4)), ALIAS),
-    (dict(out=addr(5)), ALIAS),
+    (dict(out=addr(5)), ALIAS), (dict(ws=addr(8) + 4), ALIGN), (dict(total_k=9000), WS),
+    (dict(total_k=9000, ws=addr(8), ws_bytes=1000), WS),
+    (dict(total_k=9000, ws=addr(1), ws_bytes=1 << 30), ALIAS), (dict(total_k=9000, ws=addr(5), ws_bytes=1 << 30), ALIAS),
 ])
 def test_prefill_refusals(lib, over, status):
     assert prefill(lib, **over) == status
@@ -125,7 +127,7 @@ def test_prefill_refusals(lib, over, status):
 def test_prefill_without_work(lib):
     assert prefill(lib, n=0, q=None, k=None, v=None, out=None, cu_q=None, cu_k=None, total_k=10) == OK
     assert prefill(lib, total_q=0, q=None, out=None) == OK
-    assert lib.gdn_attn_prefill(None, None, None, None, None, None, None, None, None) == NULL
+    assert lib.gdn_attn_prefill(None, None, None, None, None, None, None, None, None, 0, None) == NULL
 
 
 def decode(lib, c=None, ws=None, ws_bytes=0, lse=None, **over):

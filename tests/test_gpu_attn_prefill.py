@@ -69,6 +69,72 @@ def test_against_64_bits(lq, lk, hq, hk, d, dtype, causal):
     compare(q, k, v, lq, lk, causal, d ** -0.5, out, lse)
 
 
+# Few rows over many keys: the keys are divided over workgroups. Ragged, so that some sequences have
+# fewer ranges than others, one or none; rows whose last keys lie in the middle of a range.
+FEW = [([8], [5000], 8, 2, 64), ([1, 3, 0, 40], [3000, 700, 900, 41], 4, 2, 128), ([70], [2500], 16, 2, 256),
+       ([2, 5, 30], [4100, 0, 20], 3, 1, 256), ([200, 1], [1700, 1900], 2, 2, 64), ([16, 16], [2049, 255], 6, 1, 128)]
+
+
+@pytest.mark.parametrize("lq,lk,hq,hk,d", FEW)
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("causal", [True, False])
+def test_few_rows_over_many_keys(lq, lk, hq, hk, d, dtype, causal):
+    q, k, v = make(lq, lk, hq, hk, d, dtype, seed=d + len(lk))
+    dims = gdn.AttnDims(len(lq), sum(lq), sum(lk), hq, hk, d, gdn.GDN_BF16 if dtype == BF else gdn.GDN_F32, int(causal),
+                        d ** -0.5, hq * d, d, hk * d, d, hk * d, d)
+    need = gdn._load().gdn_attn_prefill_workspace_bytes(dims)
+    assert need > 0
+    out, lse = run(q, k, v, lq, lk, causal)
+    compare(q, k, v, lq, lk, causal, d ** -0.5, out, lse)
+    # the same from run to run, also with a workspace that held something else, and without lse
+    ws = torch.full((need,), 0xff, dtype=torch.uint8, device=DEV)
+    again = gdn.gdn_attn_prefill(q.to(DEV), k.to(DEV), v.to(DEV), ints(offsets(lq)), ints(offsets(lk)), causal=causal,
+                                 workspace=ws)
+    assert torch.equal(out, again)
+    with pytest.raises(gdn.GdnError, match="WORKSPACE"):
+        gdn.gdn_attn_prefill(q.to(DEV), k.to(DEV), v.to(DEV), ints(offsets(lq)), ints(offsets(lk)), causal=causal,
+                             workspace=ws[:need - 1])
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_few_rows_masked_values_and_large_scores(dtype):
+    """NaN and infinities that a row may not see, in the range of its last keys, change nothing; the
+    largest score in any of the ranges."""
+    lq, lk, d = [6], [3000], 128
+    for at in (0, 700, 2990):
+        q, k, v = make(lq, lk, 2, 1, d, dtype, seed=at)
+        k[at] *= 30.0
+        out, lse = run(q, k, v, lq, lk)
+        compare(q, k, v, lq, lk, True, d ** -0.5, out, lse, f"large at {at}")
+        bad_k, bad_v = k.clone(), v.clone()
+        bad_k[2998:], bad_v[2997:] = math.nan, math.inf
+        bad, bad_lse = run(q, bad_k, bad_v, lq, lk)
+        assert torch.equal(bad[:3], out[:3]) and torch.equal(bad_lse[:3], lse[:3])
+
+
+def test_few_rows_in_a_graph():
+    lq, lk, d = [9, 2], [4000, 1000], 128
+    q, k, v = (x.to(DEV) for x in make(lq, lk, 4, 2, d, BF, seed=21))
+    cq, ck = ints(offsets(lq)), ints(offsets(lk))
+    out = torch.empty_like(q)
+    call = lambda o: gdn.gdn_attn_prefill(q, k, v, cq, ck, out=o)
+    call(out)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        call(out)
+    for step in range(4):
+        q.mul_(1.0 + 0.1 * step)
+        want = torch.empty_like(q)
+        call(want)
+        torch.cuda.synchronize()
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want), step
+
+
 @pytest.mark.parametrize("dtype,d,n", [(BF, 128, 1500), (BF, 256, 700), (BF, 64, 1100), (F32, 128, 300)])
 def test_longer(dtype, d, n):
     lq = lk = [n]
