@@ -26,7 +26,7 @@ __all__ = [
     "gdn_prefill_segmented", "gdn_prefill_segmented_workspace_bytes", "gdn_prefill_scan_blockwise",
     "calib_mfma_bf16", "calib_stream_copy", "gdn_prefill_segmented_noalloc", "gdn_noalloc_scratch_bytes",
     "debug_fill_lds", "gdn_kv_write", "gdn_kv_read", "gdn_attn_prefill", "gdn_attn_decode",
-    "gdn_attn_decode_workspace_bytes", "KvCache", "AttnDims",
+    "gdn_attn_prefill_workspace_bytes", "gdn_attn_decode_workspace_bytes", "KvCache", "AttnDims",
 ]
 
 GDN_F32, GDN_BF16, GDN_FP8 = 0, 1, 2
@@ -621,6 +621,13 @@ def gdn_kv_read(k_cache, v_cache, page_table, start, cu_seqlens, total, *, dtype
     return k_out, v_out
 
 
+def gdn_attn_prefill_workspace_bytes(n, total_q, total_k, h_q, h_kv, d, dtype=torch.bfloat16) -> int:
+    """Workspace bytes of gdn_attn_prefill for these sizes."""
+    t = _DTYPES.get(dtype, -1)
+    dims = AttnDims(n, total_q, total_k, h_q, h_kv, d, t, 1, 1.0, h_q * d, d, h_kv * d, d, h_kv * d, d)
+    return int(_load().gdn_attn_prefill_workspace_bytes(ctypes.byref(dims)))
+
+
 def gdn_attn_prefill(q, k, v, cu_q, cu_k=None, *, causal=True, scale=None, out=None, lse=None,
                      workspace=None, stream=None):
     """Attention over packed prompts, with grouped heads.
@@ -630,7 +637,8 @@ def gdn_attn_prefill(q, k, v, cu_q, cu_k=None, *, causal=True, scale=None, out=N
     key rows cu_k[s] to cu_k[s + 1] - 1 (cu_k None: the same). With causal, a sequence's last
     query sees its last key, so a segment of new tokens may follow a context. scale defaults to
     1 / sqrt(d). Rows that see no key give 0. Pass lse (float32 [total_q, h_q]) to have the
-    logarithm of each row's sum written to it. Returns out [total_q, h_q, d] of q's dtype."""
+    logarithm of each row's sum written to it; workspace: uint8, used where few rows meet many
+    keys (allocated if not given). Returns out [total_q, h_q, d] of q's dtype."""
     t = _dtype_id(q)
     gpu = _gpu(q)
     qp, qt, qh = _rows("q", q, q.dtype, gpu)
@@ -675,7 +683,8 @@ def gdn_attn_decode_workspace_bytes(n, max_pages, page_size, h_q, h_kv, d, max_l
 
 def gdn_attn_decode(q, k_cache, v_cache, page_table, lens, *, max_len=None, k_scale=None,
                     v_scale=None, scale=None, out=None, lse=None, workspace=None, stream=None):
-    """Attention of one new token per sequence over a paged cache.
+    """Attention of one new token per sequence over a paged cache (a long one is split, which takes a
+    workspace: uint8, allocated if not given).
 
     q [n, h_q, d] (bfloat16 or float32; tokens and heads may be strided): row s attends to
     positions 0 to lens[s] - 1 of sequence s (lens int32 [n]; the new token's own position,

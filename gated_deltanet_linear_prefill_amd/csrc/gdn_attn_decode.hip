@@ -2,10 +2,17 @@
 //
 // Bound by the bytes of the cache: every K and V row is read once per KV head, for all of its
 // G = h_q / h_kv query heads (up to 16 at a time). One workgroup takes one (sequence, KV head)
-// and one range of positions; its waves take 32-position (16 for long rows) steps of the range in turn, each with
-// its own softmax state, and are joined in LDS. When the pairs alone would not fill the chip
-// the positions are split over more workgroups (ranges), whose sums go to the workspace and
-// are joined by a second kernel.
+// and one range of positions; its waves take 32-position (16 for long rows) steps of the range
+// in turn, each with its own softmax state, and are joined in LDS. When the pairs alone would
+// not fill the chip the positions are split over more workgroups (ranges), whose sums go to the
+// workspace and are joined by a second kernel. (Joining by the workgroup that ends last was
+// slower: 4096 positions 20.8 us against 14, since every workgroup then has to write its cache
+// lines back before it counts itself.)
+//
+// Measured: 64 sequences of 17 to 8192, 32/8 heads, d = 128, bf16 (897 MB) 167 us + 7.6 us of join,
+// 5.4 TB/s in the first kernel (a large copy: 5.2 to 5.7); one sequence of 131072 fp8 positions,
+// 16/2 heads, d = 256 (135 MB) 29 + 4.4 us, 4.6 TB/s; 333 bf16 positions 11.5 us, the latency of
+// three dependent steps of loads.
 //
 // Registers only (16x16 MFMA, one query head per column). S^T = K Q^T: lane l (c = l & 15,
 // g = l >> 4) loads row c of a 16-key block in 16-byte pieces, which are the A operand as they
@@ -427,7 +434,7 @@ decode_attn_kernel(AttnDecodeCall p, int64_t range, int ranges, int head_tiles, 
 // Joins the ranges of one (sequence, head), 64 elements of it: the ranges' sums weighted by
 // exp2(m - max m). 16 lanes hold the elements, the blockDim / 16 groups of them take the ranges
 // in turn (few ranges need few groups: see join_threads); the order of the additions depends on
-// the sizes only.
+// the sizes only. Latency-bound: 4.4 us for 16 heads of 128 ranges, 7.6 us for 2048 of up to 8.
 constexpr int kJoinGroups = 64;  // at most
 
 int join_threads(int64_t ranges)
