@@ -443,7 +443,8 @@ gdn_status gdn_kv_read(const gdn_kv_cache* cache, int64_t total, int32_t dtype, 
  * among what a row sees reaches its output.
  * Where few rows meet many keys the keys are divided into ranges that a second kernel joins, in
  * a fixed order: workspace then has gdn_attn_prefill_workspace_bytes(dims) bytes (0 when
- * nothing is divided, and for invalid arguments).
+ * nothing is divided, and for invalid arguments). That does not grow steadily with the sizes;
+ * 64 * 1024 * (4 * d + 16) bytes, twice as many for fp32 with d = 256, serve every call.
  */
 typedef struct {
     int64_t n;       /* sequences                                                */
@@ -472,7 +473,8 @@ gdn_status gdn_attn_prefill(const gdn_attn_dims* dims, const void* q, const void
  * A long cache is split into ranges that are attended to separately and joined by a second
  * kernel, in a fixed order, so results are the same from run to run. Rounding and NaN as for
  * gdn_attn_prefill. workspace: gdn_attn_decode_workspace_bytes(cache, h_q, max_len) bytes (0
- * when nothing is split, and for invalid arguments).
+ * when nothing is split, and for invalid arguments). That does not grow steadily with max_len;
+ * (4096 + u) * 16 * (4 * d + 16) bytes, u = n * h_kv * ceil(h_q / h_kv / 16), serve every one.
  */
 size_t gdn_attn_decode_workspace_bytes(const gdn_kv_cache* cache, int32_t h_q, int64_t max_len);
 gdn_status gdn_attn_decode(const gdn_kv_cache* cache, int32_t h_q, int32_t dtype, float scale,

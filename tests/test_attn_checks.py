@@ -1,6 +1,7 @@
 """CPU tests of the attention entry points: every refusal returns its status before any HIP call,
 and the binding rejects what the library must not see. Addresses are fake; nothing is launched."""
 import ctypes
+import random
 
 import pytest
 import torch
@@ -179,3 +180,23 @@ def test_binding_rejects_cpu_tensors():
             call()
     with pytest.raises(ValueError):
         gdn.gdn_attn_prefill(z.tolist(), z, z, i)
+
+
+def test_workspaces_stay_below_their_bounds(lib):
+    """What the header says is enough for any call, over random sizes."""
+    rng = random.Random(5)
+    size = lambda top: int(2 ** rng.uniform(0, top))
+    seen = 0
+    for _ in range(20000):
+        hk, g, n, d = rng.choice([1, 2, 3, 8]), rng.choice([1, 3, 8, 16, 20]), size(9), rng.choice([64, 128, 256])
+        f32 = rng.random() < 0.4
+        need = gdn.gdn_attn_prefill_workspace_bytes(n, size(16), size(22), hk * g, hk, d,
+                                                    torch.float32 if f32 else torch.bfloat16)
+        assert need <= 64 * 1024 * (4 * d + 16) * (2 if f32 and d == 256 else 1)
+        seen += need > 0
+        page = rng.choice([16, 64, 1024])
+        units = n * hk * -(-g // 16)
+        need = gdn.gdn_attn_decode_workspace_bytes(n, size(12), page, hk * g, hk, d, size(22))
+        assert need <= (4096 + units) * 16 * (4 * d + 16)
+        seen += need > 0
+    assert seen > 4000
