@@ -88,6 +88,42 @@ def test_bad_values_behind_what_a_row_sees(lq, lk, hq, hk, d, dtype, bad):
     assert not bool(torch.isfinite(out[first:].float()).any())
 
 
+# 256 tiles of 256 rows or fewer with many keys, and enough of them that keys are not divided
+BUSY = [(2000, 2000, 16, 2, 128, BF), (1500, 2100, 16, 4, 64, BF), (1030, 1100, 32, 1, 256, BF), (1500, 1500, 16, 2, 64, F32),
+        (1060, 1060, 20, 2, 128, F32), (1030, 1030, 16, 16, 256, F32)]
+
+
+@pytest.mark.parametrize("with_lse", [False, True])
+@pytest.mark.parametrize("lq,lk,hq,hk,d,dtype", BUSY)
+def test_tiles_for_most_of_the_chip(lq, lk, hq, hk, d, dtype, with_lse):
+    assert gdn.gdn_attn_prefill_workspace_bytes(1, lq, lk, hq, hk, d, dtype) == 0
+    test_large_prefills(lq, lk, hq, hk, d, dtype, with_lse)
+
+
+@pytest.mark.parametrize("lq,lk,hq,hk,d,dtype", BUSY)
+@pytest.mark.parametrize("bad", [math.nan, -math.inf])
+def test_bad_values_on_most_of_the_chip(lq, lk, hq, hk, d, dtype, bad):
+    test_bad_values_behind_what_a_row_sees(lq, lk, hq, hk, d, dtype, bad)
+
+
+@pytest.mark.parametrize("seed", range(16))
+def test_random_prefills_after_contexts(seed):
+    """A few new tokens after long contexts of several lengths, strided and with the heads outside."""
+    r = random.Random(3000 + seed)
+    dtype, d = r.choice([BF, BF, F32]), r.choice([64, 128, 256])
+    hk, g, n = r.choice([1, 2, 3]), r.choice([1, 2, 5, 8]), r.randint(1, 4)
+    lq = [r.choice([0, 1, r.randint(1, 90)]) for _ in range(n)] + [1]
+    lk = [r.choice([0, x, r.randint(1, 3000), 2048]) for x in lq[:-1]] + [2000 * n]
+    causal = r.random() < 0.8
+    q, k, v = make(lq, lk, hk * g, hk, d, dtype, seed=seed)
+    assert gdn.gdn_attn_prefill_workspace_bytes(n + 1, sum(lq), sum(lk), hk * g, hk, d, dtype) > 0
+    kv = torch.stack([k, v], 1).to(DEV)                          # tokens, k or v, heads
+    qt = q.transpose(0, 1).contiguous().to(DEV).transpose(0, 1)  # a head's tokens together
+    lse = torch.full(q.shape[:2], 5.0, device=DEV)
+    out = gdn.gdn_attn_prefill(qt, kv[:, 0], kv[:, 1], ints(offsets(lq)), ints(offsets(lk)), causal=causal, lse=lse)
+    compare(q, k, v, lq, lk, causal, d ** -0.5, out, lse, f"{lq} {lk}")
+
+
 def test_many_sequences():
     """More sequences than a wave looks up at a time, empty ones among them."""
     r = random.Random(5)
