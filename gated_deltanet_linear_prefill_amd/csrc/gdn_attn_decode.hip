@@ -11,8 +11,8 @@
 //
 // Measured: 64 sequences of 17 to 8192, 32/8 heads, d = 128, bf16 (897 MB) 167 us + 7.6 us of join,
 // 5.4 TB/s in the first kernel (a large copy: 5.2 to 5.7); one sequence of 131072 fp8 positions,
-// 16/2 heads, d = 256 (135 MB) 29 + 4.4 us, 4.6 TB/s; 333 bf16 positions 11.5 us, the latency of
-// three dependent steps of loads.
+// 16/2 heads, d = 256 (135 MB) 29 + 4.4 us, 4.6 TB/s; 333 bf16 positions 11.5 us, what one CU
+// takes to load a KV head's 341 KB (with eight waves a workgroup 11.1).
 //
 // Registers only (16x16 MFMA, one query head per column). S^T = K Q^T: lane l (c = l & 15,
 // g = l >> 4) loads row c of a 16-key block in 16-byte pieces, which are the A operand as they
