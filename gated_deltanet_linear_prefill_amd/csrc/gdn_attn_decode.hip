@@ -375,7 +375,8 @@ decode_attn_kernel(AttnDecodeCall p, int64_t range, int ranges, int head_tiles, 
         for (int b = 0; b < C::NB; ++b) there[b] = nthere[b];
     }
 
-    // join the waves: weights relative to the largest maximum
+    // join the waves: weights relative to the largest maximum. A wave that saw nothing but NaN
+    // scores has m = -inf as one that saw no key has; its sums are NaN, and 0 x NaN hands them on
     l += __shfl_xor(l, 16, 64);
     l += __shfl_xor(l, 32, 64);
     exact += __shfl_xor(exact, 16, 64);
@@ -396,7 +397,7 @@ decode_attn_kernel(AttnDecodeCall p, int64_t range, int ranges, int head_tiles, 
             for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int j = 0; j < C::EPL; ++j)
-                    s_o[wave][c][16 * C::EPL * u + C::EPL * (4 * g + i) + j] = m == -INFINITY ? 0.f : o[u * C::EPL + j][i] * f;
+                    s_o[wave][c][16 * C::EPL * u + C::EPL * (4 * g + i) + j] = o[u * C::EPL + j][i] * f;
     }
     __syncthreads();
     for (int x = threadIdx.x; x < heads * (D / 4); x += 64 * kWaves) {
@@ -409,12 +410,11 @@ decode_attn_kernel(AttnDecodeCall p, int64_t range, int ranges, int head_tiles, 
 #pragma unroll
         for (int y = 0; y < kWaves; ++y) sum += *reinterpret_cast<const f32x4_t*>(&s_o[y][hd][el]);
 #pragma unroll
-        for (int y = 0; y < kWaves; ++y)
-            if (s_m[y][hd] != -INFINITY) {
-                const float w = __builtin_amdgcn_exp2f(s_m[y][hd] - top);
-                ls += s_l[y][hd].x * w;
-                le += s_l[y][hd].y * w;
-            }
+        for (int y = 0; y < kWaves; ++y) {
+            const float w = s_m[y][hd] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(s_m[y][hd] - top);
+            ls += s_l[y][hd].x * w;
+            le += s_l[y][hd].y * w;
+        }
         if (whole) {
             const int64_t orow = seq * p.h_q + kvh * G + 16 * ht + hd;
             const float inv = ls > 0.f ? 1.f / ls : (ls == ls ? 0.f : ls);
