@@ -497,8 +497,8 @@ def _bad(name, x, what):
 
 def _rows(name, x, dtype, index):
     """(pointer, token stride, head stride) of a [tokens, heads, d] tensor with contiguous d on the
-    GPU of this index. The stride of a dimension of one entry means nothing to torch: a dense one
-    stands for it."""
+    GPU of this index. The stride of a dimension of one entry means nothing to torch: one that every
+    layout of the other dimension allows stands for it."""
     if not isinstance(x, _Tensor) or x.dtype != dtype or x.dim() != 3 or x.get_device() != index:
         _bad(name, x, f"{dtype} [tokens, heads, d] on GPU {index}")
     st, sh, sd = x.stride()
@@ -508,7 +508,7 @@ def _rows(name, x, dtype, index):
     if h == 1:
         sh = d
     if t <= 1:
-        st = sh * h
+        st = d
     return x.data_ptr(), st, sh
 
 
