@@ -244,7 +244,7 @@ gdn_status gdn_attn_prefill(const gdn_attn_dims* d, const void* q, const void* k
         if (any_overlap(r[i], r + i + 1, 7 - i)) return GDN_ERR_ALIAS;
     if (!work) return GDN_OK;
     const AttnCall call = {*d, q, k, v, cu_q, cu_k ? cu_k : cu_q, out, lse, ws,
-                           static_cast<hipStream_t>(stream), 1, nullptr, nullptr};
+                           static_cast<hipStream_t>(stream), 0, 1, nullptr, nullptr};
     (void)hipGetLastError();
     return finish(launch_attn_prefill(call));
 }

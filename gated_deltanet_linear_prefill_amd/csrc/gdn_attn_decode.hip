@@ -56,7 +56,7 @@ Plan make_plan(const gdn_kv_cache* c, int32_t h_q, int64_t max_len)
     int64_t ranges = units > 0 ? (want + units - 1) / units : 1;
     if (ranges > (steps + 1) / 2) ranges = (steps + 1) / 2;
     if (steps <= 4) ranges = 1;
-    if (units > 0 && ranges > 0x7fffffff / units) ranges = 0x7fffffff / units;  // one grid dimension
+    if (units > 0 && ranges > 0x7fffffff / units) ranges = 0x7fffffff / units;  // the grid
     if (ranges < 1) ranges = 1;
     const int64_t per = (steps + ranges - 1) / ranges;
     p.range = per * kRange;
@@ -128,9 +128,10 @@ decode_attn_kernel(AttnDecodeCall p, int64_t range, int ranges, int head_tiles, 
     // ranges of one index lie together in the grid: which XCD a workgroup runs on (its index
     // modulo 8) then does not depend on its range, and late ranges, which few sequences have,
     // spread over all XCDs
-    const int64_t units = gridDim.x / ranges;
-    const int rg = (int)(blockIdx.x / units);
-    const int64_t unit = blockIdx.x % units;
+    const int64_t units = p.c.n * p.c.h_kv * head_tiles;
+    const int rg = (int)(block_index() / units);
+    const int64_t unit = block_index() % units;
+    if (rg >= ranges) return;  // past the grid's end
     const int ht = (int)(unit % head_tiles);
     const int kvh = (int)(unit / head_tiles % p.c.h_kv);
     const int64_t seq = unit / head_tiles / p.c.h_kv;
@@ -513,8 +514,8 @@ hipError_t launch_t(const AttnDecodeCall& c)
     Partials part;
     part.o = static_cast<float*>(c.ws);
     part.ml = reinterpret_cast<float4*>(part.o + units * pl.ranges * 16 * D);
-    hipLaunchKernelGGL((decode_attn_kernel<T, FP8, D>), dim3((unsigned)(units * pl.ranges)), dim3(64 * kWaves), 0,
-                       c.stream, c, pl.range, (int)pl.ranges, pl.head_tiles, shift, part);
+    hipLaunchKernelGGL((decode_attn_kernel<T, FP8, D>), grid_of(units * pl.ranges), dim3(64 * kWaves), 0, c.stream, c,
+                       pl.range, (int)pl.ranges, pl.head_tiles, shift, part);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || pl.ranges == 1) return e;
     hipLaunchKernelGGL((decode_join_kernel<T, D>), dim3((unsigned)(c.c.n * c.h_q * (D / 64))), dim3(join_threads(pl.ranges)), 0, c.stream, c,

@@ -26,9 +26,9 @@ struct AttnCall {
     float* lse;
     void* ws;
     hipStream_t stream;
-    // Set by the launcher: ranges of a tile's keys, and where their sums go, [unit][range][row]: o
-    // [d] and (m, l, exact l, -).
-    int ranges;
+    // Set by the launcher: tiles of all KV heads, ranges of a tile's keys, and where their sums go,
+    // [unit][range][row]: o [d] and (m, l, exact l, -).
+    int units, ranges;
     float* part_o;
     float4* part_ml;
 };
@@ -59,7 +59,24 @@ size_t attn_prefill_workspace(const gdn_attn_dims& d);
 // Workspace of a decode call (0: not split), from the sizes the host knows.
 size_t attn_decode_workspace(const gdn_kv_cache* c, int32_t h_q, int64_t max_len);
 
+// A grid of at least `blocks` workgroups. A launch holds fewer than 2^32 threads in one dimension (more
+// are not refused: workgroups are missing), so long ones go on in the second; workgroups have
+// at most 1024 threads. Those whose block_index() is past the call's own leave.
+constexpr int64_t kGridLine = INT64_C(1) << 21;
+
+inline dim3 grid_of(int64_t blocks)
+{
+    return blocks <= kGridLine ? dim3((unsigned)blocks)
+                               : dim3((unsigned)kGridLine, (unsigned)((blocks + kGridLine - 1) / kGridLine));
+}
+
 // ---------------------------------------------------------------- device helpers
+// The workgroup's number in a grid of grid_of: below 2^31 + kGridLine.
+__device__ __forceinline__ uint32_t block_index()
+{
+    return blockIdx.y * (uint32_t)kGridLine + blockIdx.x;
+}
+
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x4_t __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));

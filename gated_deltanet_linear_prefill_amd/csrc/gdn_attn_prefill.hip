@@ -455,7 +455,9 @@ __global__ void __launch_bounds__(64 * S::WAVES, S::PER_SIMD) prefill_kernel(Att
     const int half = lane >> 5;
     const int rw = wave % (S::WAVES / SPLIT), turn = wave / (S::WAVES / SPLIT);  // 32 rows, steps
     Work w;
-    const int units = S::RANGES ? gridDim.x / p.ranges : gridDim.x, unit = blockIdx.x % units, rg = blockIdx.x / units;
+    const uint32_t block = block_index();
+    if (block >= (uint32_t)p.units * (uint32_t)(S::RANGES ? p.ranges : 1)) return;  // past the grid's end
+    const int unit = S::RANGES ? block % (uint32_t)p.units : block, rg = S::RANGES ? block / (uint32_t)p.units : 0;
     if (!find_work<M>(p, unit / p.d.h_kv, unit % p.d.h_kv, lane, &w)) return;
 
     const int64_t ks = ES * p.d.k_token, vs = ES * p.d.v_token;
@@ -733,11 +735,11 @@ hipError_t launch_kernel(const AttnCall& c, int ranges = 1)
 {
     const int64_t units = units_of(c.d, S::ROWS);
     AttnCall a = c;
+    a.units = (int)units;
     a.ranges = ranges;
     a.part_o = static_cast<float*>(c.ws);
     a.part_ml = reinterpret_cast<float4*>(a.part_o + units * ranges * S::ROWS * D);
-    hipLaunchKernelGGL((prefill_kernel<T, D, LSE, S>), dim3((unsigned)(units * ranges)), dim3(64 * S::WAVES), 0,
-                       c.stream, a);
+    hipLaunchKernelGGL((prefill_kernel<T, D, LSE, S>), grid_of(units * ranges), dim3(64 * S::WAVES), 0, c.stream, a);
     const hipError_t e = hipGetLastError();
     if constexpr (S::RANGES)
         if (e == hipSuccess && ranges > 1) {

@@ -144,8 +144,8 @@ struct Piece {
     __device__ __forceinline__ Piece(const KvCall& p, int page_shift)
     {
         el = (int)(threadIdx.x % LPR) * E;
-        r = (int64_t)blockIdx.x * RPB + threadIdx.x / LPR;
-        token = (uint32_t)r / (uint32_t)p.c.h_kv;  // rows stay below 2^31
+        r = (int64_t)block_index() * RPB + threadIdx.x / LPR;
+        token = (uint32_t)r / (uint32_t)p.c.h_kv;  // rows stay below 2^31, and r below 2^32
         head = (int)((uint32_t)r % (uint32_t)p.c.h_kv);
         mine = false;
         const int first = __builtin_amdgcn_readfirstlane((int)token);
@@ -231,7 +231,7 @@ hipError_t launch_t(const KvCall& c, bool write)
 {
     const int64_t rows = c.total * c.c.h_kv;
     const int per = write ? Piece<D, write_elems<T, FP8>>::RPB : Piece<D, Some<T>::E>::RPB;
-    const dim3 grid((unsigned)((rows + per - 1) / per)), block(256);
+    const dim3 grid = grid_of((rows + per - 1) / per), block(256);
     const int shift = __builtin_ctz((unsigned)c.c.page_size);
     if (write)
         hipLaunchKernelGGL((kv_write_kernel<T, D, FP8>), grid, block, 0, c.stream, c, shift);
