@@ -507,10 +507,10 @@ __global__ void __launch_bounds__(64 * S::WAVES, S::PER_SIMD) prefill_kernel(Att
     const char* qp = static_cast<const char*>(p.q) +
                      ES * ((w.q0 + pos) * p.d.q_token + (w.head * w.g + (rc - pos * w.g)) * p.d.q_head) + 16 * half;
     // A negative scale becomes a positive one of the negated query: the maximum of the raw scores
-    // is then that of the scaled ones. Zero becomes so small a one that every weight is 1, and
-    // a masked score, -infinity, stays so.
+    // is then that of the scaled ones. Zero becomes the smallest positive number, which takes any
+    // finite score to less than 2^-20 and leaves a masked score, -infinity, as it is.
     const uint32_t flip = p.d.scale < 0.f ? (ES == 2 ? 0x80008000u : 0x80000000u) : 0u;
-    const float c = fmaxf(fabsf(p.d.scale) * kLog2e, 1e-37f);
+    const float c = fmaxf(fabsf(p.d.scale) * kLog2e, 0x1p-149f);
     u32x4_t q[D / (2 * C::PER)];  // piece kk: elements 2 PER kk + PER half ..
 #pragma unroll
     for (int kk = 0; kk < D / (2 * C::PER); ++kk) q[kk] = *reinterpret_cast<const u32x4_t*>(qp + 32 * kk) ^ flip;
