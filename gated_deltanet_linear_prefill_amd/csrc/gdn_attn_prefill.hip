@@ -299,6 +299,13 @@ __device__ __forceinline__ void write_rows(const AttnCall& p, const Work& w, int
 // `odd` is set if V holds a NaN or an infinity there. kOdd: for tiles where that was found.
 enum { kPlain, kMasks, kOdd };
 
+// The factor of weights relative to maximum `from` when they become relative to `to`. Raw scores may be
+// up to the largest float, and their difference twice that: it is halved, which is exact.
+__device__ __forceinline__ float rescaled(float from, float to, float c)
+{
+    return __builtin_amdgcn_exp2f((0.5f * from - 0.5f * to) * (2.f * c));
+}
+
 // One step of a wave's 32 rows over N staged keys at sk, sv (klane, vlane: this lane's offsets).
 // This lane's row sees the keys below lim (which may be negative, or above N).
 template <typename T, int D, bool LSE, int MODE>
@@ -359,7 +366,7 @@ __device__ __forceinline__ void attn_step(const char* sk, const char* sv, int kl
     // the reference maximum moves only when weights would pass 2^8: O is then rescaled
     const bool rise = mx > st.m && (st.m == -INFINITY || (mx - st.m) * c > 8.f);
     if (__any(rise)) {
-        const float a = !rise ? 1.f : st.m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((st.m - mx) * c);
+        const float a = !rise ? 1.f : st.m == -INFINITY ? 0.f : rescaled(st.m, mx, c);
         st.m = rise ? mx : st.m;
         st.l *= a;
         if (BF && LSE) st.exact *= a;
@@ -601,8 +608,8 @@ __global__ void __launch_bounds__(64 * S::WAVES, S::PER_SIMD) prefill_kernel(Att
         __syncthreads();
         if (turn == 1) return;
         const float m1 = s_st[rw][0][lane], mm = fmaxf(st.m, m1);
-        const float a0 = st.m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((st.m - mm) * c);
-        const float a1 = m1 == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((m1 - mm) * c);
+        const float a0 = st.m == -INFINITY ? 0.f : rescaled(st.m, mm, c);
+        const float a1 = m1 == -INFINITY ? 0.f : rescaled(m1, mm, c);
         st.m = mm;
         st.l = a0 * st.l + a1 * s_st[rw][1][lane];
         st.exact = a0 * st.exact + a1 * s_st[rw][2][lane];

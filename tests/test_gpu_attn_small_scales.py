@@ -26,6 +26,21 @@ def test_prefill(dtype, scale, lq, lk):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("scale", [0.0, 1e-39, -1e-39])
+@pytest.mark.parametrize("lq,lk", [([300], [300]), ([1200], [1200]), ([4], [3000])])
+def test_prefill_scores_of_both_ends(dtype, scale, lq, lk):
+    """Scores before the scale near the largest float, negative ones first: their difference is past it."""
+    q, k, v = make(lq, lk, 2, 1, 64, dtype)
+    q.zero_()
+    k.zero_()
+    q[..., 5] = 2.0 ** 63
+    k[:, :, 5] = 1.25 * 2.0 ** 64
+    k[:lk[0] // 2] *= -1
+    out, lse = run(q, k, v, lq, lk, True, scale)
+    compare(q, k, v, lq, lk, True, scale, out, lse, f"scale {scale}")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("scale", [0.0, 2e-38, -2e-38, 1e-40])
 def test_decode(dtype, scale):
     lens = [150, 3000]
