@@ -106,9 +106,10 @@ __device__ __forceinline__ float scale_of(uint32_t b)
 
 // The sequence a packed row belongs to: the last s in [0, n) with cu[s] <= row (0 if none), for a
 // wave whose lanes' rows start at `first` and lie close together: 64 sequences are compared with
-// the first row at a time, one a lane, and each lane goes on from there. Whatever cu holds, the
-// answer is a valid sequence index.
-__device__ __forceinline__ int find_seq(const int32_t* cu, int n, int first, int row)
+// the first row at a time, one a lane, and each lane goes on from there, in doubling steps over
+// what may be many empty sequences and back by halves. Whatever cu holds, the answer is a valid
+// sequence index. *end: cu of the next one.
+__device__ __forceinline__ int find_seq(const int32_t* cu, int n, int first, int row, int* end)
 {
     const int lane = threadIdx.x & 63;
     int s = 0;
@@ -119,7 +120,17 @@ __device__ __forceinline__ int find_seq(const int32_t* cu, int n, int first, int
         s += x * step;
         span = span - x * step < step ? span - x * step : step;
     }
-    while (s + 1 < n && cu[s + 1] <= row) ++s;
+    *end = cu[s + 1];
+    if (*end <= row && s + 1 < n) {
+        int step = 1;
+        for (; step < n - s && cu[s + step] <= row; step *= 2) s += step;
+        for (int stop = step < n - s ? s + step : n; stop - s > 1;) {  // the sequence is in [s, stop)
+            const int mid = s + (stop - s) / 2;
+            if (cu[mid] <= row) s = mid;
+            else stop = mid;
+        }
+        *end = cu[s + 1];
+    }
     return s;
 }
 

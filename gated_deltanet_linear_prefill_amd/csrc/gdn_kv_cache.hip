@@ -29,9 +29,10 @@ __device__ __forceinline__ int64_t pool_row(const KvCall& p, int64_t token, int 
     int64_t seq = token, i = 0;
     *mine = true;
     if (p.cu) {
-        seq = find_seq(p.cu, (int)c.n, first, (int)token);
+        int end;
+        seq = find_seq(p.cu, (int)c.n, first, (int)token, &end);
         i = token - p.cu[seq];
-        *mine = i >= 0 && token < p.cu[seq + 1];
+        *mine = i >= 0 && token < end;
         if (!*mine) return -1;
     }
     const int64_t pos = (int64_t)p.start[seq] + i;
