@@ -32,7 +32,8 @@ bool supported_chunk(int32_t c)
 }
 
 // Element counts of every tensor, or false on overflow. Sizes are bounded so that every
-// byte offset fits in int64 and every grid dimension in 31 bits.
+// byte offset fits in int64 and every grid dimension in 31 bits (whether a launch's threads fit
+// one is the launchers' check, which know their workgroups: fits_grid).
 struct Sizes {
     int64_t qk, v, gb, state, out;  // elements
     size_t esize;                   // bytes per q/k/v element

@@ -37,6 +37,7 @@ inline bool aligned(const void* p, uintptr_t a)
 
 inline gdn_status finish(hipError_t e)
 {
+    if (e == hipErrorInvalidConfiguration) return GDN_ERR_SHAPE;  // more workgroups than a launch holds
     return e == hipSuccess ? GDN_OK : GDN_ERR_HIP;
 }
 

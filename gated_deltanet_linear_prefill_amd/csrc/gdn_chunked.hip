@@ -2761,7 +2761,12 @@ hipError_t launch_chunked_t(const Call& cl, int parts)
     const TIn* q = static_cast<const TIn*>(cl.q);
     const TIn* k = static_cast<const TIn*>(cl.k);
     const TIn* v = static_cast<const TIn*>(cl.v);
-    const int64_t prep_blocks = cl.n * L.nch * cl.h_qk;
+    const int64_t prep_blocks = cl.n * L.nch * cl.h_qk, scan_blocks = cl.n * cl.h_v * (D / 16);
+    constexpr int SCAN_THREADS = [] {
+        if constexpr (C <= 32) return (int)ScanGeo<D, C, TIn>::THREADS;
+        else return C == 64 && D == 128 && !F32IN ? 512 : 256;
+    }();
+    if (!fits_grid(prep_blocks, 256) || !fits_grid(scan_blocks, SCAN_THREADS)) return kTooLong;
     if (parts & kChunkPrep) {
         // The staggered start of chunk_prep_kernel, measured for 64-token chunks of bf16 rows
         // of 128 features (four workgroups resident per CU): 1,024 workgroups at 4K tokens,
@@ -2800,17 +2805,16 @@ hipError_t launch_chunked_t(const Call& cl, int parts)
         if (e != hipSuccess) return e;
     }
     if (!(parts & kChunkScan)) return hipSuccess;
-    const int64_t scan_blocks = cl.n * cl.h_v * (D / 16);
     if constexpr (C <= 32) {
         hipLaunchKernelGGL((chunk_scan_kernel<D, C, TIn>), dim3((unsigned)scan_blocks),
-                           dim3(ScanGeo<D, C, TIn>::THREADS), 0, cl.stream, q, k, v, ws, L,
+                           dim3(SCAN_THREADS), 0, cl.stream, q, k, v, ws, L,
                            cl.state_in, cl.out, cl.state_out, cl.t, cl.h_qk, cl.h_v, scan_blocks);
     } else if constexpr (C == 64 && D == 128 && !F32IN) {
-        hipLaunchKernelGGL(chunk64_scan_kernel, dim3((unsigned)scan_blocks), dim3(512), 0, cl.stream,
+        hipLaunchKernelGGL(chunk64_scan_kernel, dim3((unsigned)scan_blocks), dim3(SCAN_THREADS), 0, cl.stream,
                            q, k, v, ws, L, cl.state_in, cl.out, cl.state_out, cl.t, cl.h_qk,
                            cl.h_v, scan_blocks);
     } else {
-        hipLaunchKernelGGL((chunk_scan_wide_kernel<D, C, TIn>), dim3((unsigned)scan_blocks), dim3(256), 0,
+        hipLaunchKernelGGL((chunk_scan_wide_kernel<D, C, TIn>), dim3((unsigned)scan_blocks), dim3(SCAN_THREADS), 0,
                            cl.stream, q, k, v, ws, L, cl.state_in, cl.out, cl.state_out, cl.t,
                            cl.h_qk, cl.h_v, scan_blocks);
     }

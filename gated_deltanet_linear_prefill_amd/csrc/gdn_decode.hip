@@ -280,6 +280,7 @@ template <int D, int SPLIT, typename TIn>
 hipError_t launch_decode_split(const Call& c)
 {
     const int64_t blocks = c.n * c.h_v * SPLIT;
+    if (!fits_grid(blocks, DecodeCfg<D, SPLIT>::NT)) return kTooLong;
     hipLaunchKernelGGL((decode_kernel<D, SPLIT, TIn>), dim3((unsigned)blocks),
                        dim3(DecodeCfg<D, SPLIT>::NT), 0, c.stream, static_cast<const TIn*>(c.q),
                        static_cast<const TIn*>(c.k), static_cast<const TIn*>(c.v), c.g, c.beta,

@@ -38,6 +38,14 @@ hipError_t launch_lds_fill(uint32_t pattern, int32_t blocks, uint32_t* sink, hip
 hipError_t launch_stream_copy(const void* src, void* dst, int64_t n16, int32_t blocks,
                               hipStream_t stream);
 
+// Whether a launch fits one grid dimension, which holds fewer than 2^32 threads: a longer one is not
+// refused, its workgroups past that are missing. Launchers return kTooLong instead.
+inline bool fits_grid(int64_t blocks, int64_t threads)
+{
+    return blocks < (INT64_C(1) << 32) / threads;
+}
+constexpr hipError_t kTooLong = hipErrorInvalidConfiguration;
+
 size_t scan_workspace_bytes(int64_t n, int64_t t, int32_t h_qk, int32_t h_v, int32_t d);
 size_t chunked_workspace_bytes(int64_t n, int64_t t, int32_t h_qk, int32_t h_v, int32_t d,
                                int chunk, int32_t dtype);

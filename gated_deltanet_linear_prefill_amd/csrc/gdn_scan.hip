@@ -250,6 +250,7 @@ template <int D, typename TIn>
 hipError_t launch_scan_t(const Call& c)
 {
     const int64_t blocks = c.n * c.h_v * (D / 16);
+    if (!fits_grid(blocks, 256)) return kTooLong;
     hipLaunchKernelGGL((scan_kernel<D, TIn>), dim3((unsigned)blocks), dim3(256), 0, c.stream,
                        static_cast<const TIn*>(c.q), static_cast<const TIn*>(c.k),
                        static_cast<const TIn*>(c.v), c.g, c.beta, c.state_in, c.out, c.state_out,
@@ -267,6 +268,7 @@ hipError_t launch_scan_blockwise_t(const Call& c, int64_t block_t)
     const TIn* k = static_cast<const TIn*>(c.k);
     const TIn* v = static_cast<const TIn*>(c.v);
     const int64_t state_elems = (int64_t)c.h_v * D * D;
+    if (!fits_grid((int64_t)c.h_v * (D / 16), 256)) return kTooLong;
     hipError_t e = hipSuccess;
     for (int64_t s = 0; s < c.n && e == hipSuccess; ++s) {
         for (int64_t t0 = 0; t0 < c.t && e == hipSuccess; t0 += block_t) {

@@ -89,7 +89,8 @@ extern "C" {
 typedef enum {
     GDN_OK = 0,
     GDN_ERR_NULL = 1,        /* a required pointer is NULL                               */
-    GDN_ERR_SHAPE = 2,       /* negative or inconsistent sizes, size overflow            */
+    GDN_ERR_SHAPE = 2,       /* negative or inconsistent sizes, size overflow, more      */
+                             /* workgroups than one launch holds                         */
     GDN_ERR_UNSUPPORTED = 3, /* valid but not built: head dim, chunk size, dtype          */
     GDN_ERR_ALIGN = 4,       /* pointer misaligned                                       */
     GDN_ERR_ALIAS = 5,       /* an output overlaps another buffer (see Aliasing)          */
