@@ -251,9 +251,10 @@ gdn_status gdn_attn_prefill(const gdn_attn_dims* d, const void* q, const void* k
 
 size_t gdn_attn_decode_workspace_bytes(const gdn_kv_cache* c, int32_t h_q, int64_t max_len)
 {
-    int64_t pool;
+    int64_t pool, rows;
     if (!c || h_q <= 0 || max_len < 0 || c->h_kv <= 0 || h_q % c->h_kv != 0) return 0;
     if (check_cache(c, c->store == GDN_FP8 ? GDN_BF16 : c->store, &pool) != GDN_OK) return 0;
+    if (!mul_ok(c->n, h_q, &rows) || rows >= (INT64_C(1) << 31)) return 0;
     return attn_decode_workspace(c, h_q, max_len);
 }
 

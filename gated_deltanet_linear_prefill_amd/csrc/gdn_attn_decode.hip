@@ -42,7 +42,7 @@ Plan make_plan(const gdn_kv_cache* c, int32_t h_q, int64_t max_len)
     const int64_t cap = c->max_pages * c->page_size;
     const int64_t len = max_len < cap ? max_len : cap;
     Plan p;
-    p.head_tiles = (h_q / c->h_kv + 15) / 16;
+    p.head_tiles = (h_q / c->h_kv - 1) / 16 + 1;
     const int64_t units = c->n * c->h_kv * p.head_tiles;
     const int64_t steps = len > 0 ? (len + kRange - 1) / kRange : 1;
     // Measured (us of a call, d = 256, 2 KV heads): 333 positions 13 in one range, 17.5 in three;
