@@ -19,6 +19,12 @@ bool attn_dtype(int32_t t)
     return t == GDN_F32 || t == GDN_BF16;
 }
 
+// Finite also in the units of exp2, which the kernels use.
+bool attn_scale(float scale)
+{
+    return isfinite(scale * 1.4426950408889634f);
+}
+
 size_t elem(int32_t t)
 {
     return t == GDN_F32 ? 4 : t == GDN_BF16 ? 2 : 1;
@@ -127,7 +133,7 @@ gdn_status check_prefill(const gdn_attn_dims* d, int64_t* rows, int64_t* qe, int
     if (!d) return GDN_ERR_NULL;
     if (d->n < 0 || d->total_q < 0 || d->total_k < 0 || d->h_q <= 0 || d->h_kv <= 0 || d->d <= 0)
         return GDN_ERR_SHAPE;
-    if (d->h_q % d->h_kv != 0 || (d->causal != 0 && d->causal != 1) || !isfinite(d->scale))
+    if (d->h_q % d->h_kv != 0 || (d->causal != 0 && d->causal != 1) || !attn_scale(d->scale))
         return GDN_ERR_SHAPE;
     if (!attn_dtype(d->dtype) || !attn_d(d->d)) return GDN_ERR_UNSUPPORTED;
     const int64_t lim = INT64_C(1) << 31;
@@ -266,7 +272,7 @@ gdn_status gdn_attn_decode(const gdn_kv_cache* c, int32_t h_q, int32_t dtype, fl
     int64_t pool, qe, rows;
     gdn_status st = check_cache(c, dtype, &pool);
     if (st != GDN_OK) return st;
-    if (h_q <= 0 || h_q % c->h_kv != 0 || max_len < 0 || !isfinite(scale)) return GDN_ERR_SHAPE;
+    if (h_q <= 0 || h_q % c->h_kv != 0 || max_len < 0 || !attn_scale(scale)) return GDN_ERR_SHAPE;
     if (!mul_ok(c->n, h_q, &rows) || rows >= (INT64_C(1) << 31)) return GDN_ERR_SHAPE;
     if (!strided(c->n, h_q, c->d, q_token, q_head, dtype, &qe)) return GDN_ERR_SHAPE;
     st = cache_pointers(c);

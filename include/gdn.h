@@ -456,7 +456,7 @@ typedef struct {
     int32_t d;       /* head dimension                                           */
     int32_t dtype;   /* gdn_dtype of q, k, v and out                             */
     int32_t causal;  /* 0 or 1                                                   */
-    float scale;     /* finite; 1 / sqrt(d) is usual                             */
+    float scale;     /* finite, also times log2 e; 1 / sqrt(d) is usual          */
     int64_t q_token, q_head, k_token, k_head, v_token, v_head; /* strides, in elements */
 } gdn_attn_dims;
 
