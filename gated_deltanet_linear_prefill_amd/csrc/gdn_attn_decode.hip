@@ -10,9 +10,12 @@
 // lines back before it counts itself.)
 //
 // Measured: 64 sequences of 17 to 8192, 32/8 heads, d = 128, bf16 (897 MB) 167 us + 7.6 us of join,
-// 5.4 TB/s in the first kernel (a large copy: 5.2 to 5.7); one sequence of 131072 fp8 positions,
-// 16/2 heads, d = 256 (135 MB) 29 + 4.4 us, 4.6 TB/s; 333 bf16 positions 11.5 us, what one CU
-// takes to load a KV head's 341 KB (with eight waves a workgroup 11.1).
+// 5.4 TB/s in the first kernel (a large copy: 5.2 to 5.7); 32 sequences of 4096, fp32, 5.6 TB/s
+// in all; one sequence of 131072 fp8 positions, 16/2 heads, d = 256 (135 MB) 29 + 4.3 us, 4.6 TB/s
+// (fp32 queries over an fp8 cache, 64 sequences of 8192, 32/8 heads, d = 128: 3.3 TB/s; four
+// heads fill a quarter of the fp32 matrix instructions' columns, which run at 70% of their rate);
+// 333 bf16 positions 11.4 us, what one CU takes to load a KV head's 341 KB (with eight waves a
+// workgroup 11.1).
 //
 // Registers only (16x16 MFMA, one query head per column). S^T = K Q^T: lane l (c = l & 15,
 // g = l >> 4) loads row c of a 16-key block in 16-byte pieces, which are the A operand as they
@@ -45,9 +48,14 @@ Plan make_plan(const gdn_kv_cache* c, int32_t h_q, int64_t max_len)
     p.head_tiles = (h_q / c->h_kv - 1) / 16 + 1;
     const int64_t units = c->n * c->h_kv * p.head_tiles;
     const int64_t steps = len > 0 ? (len + kRange - 1) / kRange : 1;
-    // Measured (us of a call, d = 256, 2 KV heads): 333 positions 13 in one range, 17.5 in three;
-    // 1024 positions 24 in one, 17.5 in four; so up to four steps stay together. A single
-    // sequence of 131072 fp8 positions 33 in 256 ranges (one workgroup a CU), 39 in 1024. A
+    // Measured (us of a C call, one sequence, d = 256, 16/2 heads, bf16, in 1 / 2 / 4 ranges): 256
+    // positions 9.2 / 10.3, 512 14.2 / 12.9 / 10.4, 1024 23.4 / 18.0 / 13.0; fp8 512 10.1 / 10.9 / 9.6,
+    // 1024 15.1 / 13.7 / 11.0; d = 128, 32/8 heads 512 8.4 / 9.7 / 8.5, 1024 12.7 / 11.9 / 9.7. Up to
+    // four steps stay together, which spares the workspace and the second launch (333 positions
+    // 11.4, 8.7 and 7.2; in ranges of one step 10.3, 9.5 and 8.4); longer ones are cut into ranges
+    // of two steps or more. Ranges of one step would be faster for long rows: bf16 d = 256 from
+    // 384 positions on (512: 10.4 us; 1024 in 8: 10.8), fp32 d = 256 from 256 on (512 29.5 / 15.4). A
+    // single sequence of 131072 fp8 positions 33 in 256 ranges (one workgroup a CU), 39 in 1024. A
     // batch's lengths differ: 64 sequences of up to 8192, 8 KV heads, 198 in one range each,
     // 187 in ranges of 2048, 176 of 1024, where late workgroups fill the CUs that are done.
     const int64_t most = units * steps;
@@ -318,6 +326,7 @@ decode_attn_kernel(AttnDecodeCall p, int64_t range, int ranges, int head_tiles, 
             exact += s[i];
             if constexpr (BF) s[i] = round_bf16(s[i]);
             l += s[i];
+            // exact, but for rows of V so small that the product is below the normal range
             if constexpr (FP8) s[i] *= scale_of((sv[i / 4] >> (8 * (i % 4))) & 0xff);
         }
 

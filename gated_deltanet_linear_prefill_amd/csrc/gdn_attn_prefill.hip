@@ -22,12 +22,14 @@
 // reference maximum of a row moves only when a score passes it by 2^8 (weights then stay below
 // 2^8 and sums far from overflow), so O is rarely rescaled.
 //
-// Bound by the matrix rate together with the softmax's vector instructions: about 3.9 of them a
-// score and lane, which the matrix instructions of the other wave of a SIMD hide only in part.
-// Measured, bf16: 4096 tokens after 28672, 16/2 heads, d = 256 1743 us, 1.18 PFLOP/s (the
-// library's large product 1.2 to 1.4; matrix units 66% busy); a 4096-token prompt 143 us,
-// 0.96 PFLOP/s; 16 packed prompts of up to 2500, 32/8 heads, d = 128 281 us, 0.78 PFLOP/s (44%
-// busy; each tile's start and end, and masked steps, weigh more). 8192 tokens without a mask,
+// Bound by the matrix rate together with the softmax's vector instructions, which the matrix
+// instructions of the other wave of a SIMD hide only in part: by the counters 4.6 of them a score
+// and lane for a long d = 256 segment, 6.1 for packed d = 128 prompts (masked steps, each tile's
+// start and end). Measured, bf16: 4096 tokens after 28672, 16/2 heads, d = 256 1765 us (1705 to
+// 1960 by machine), 1.17 PFLOP/s (the library's large product 1.2 to 1.4; matrix units 66% busy); a
+// 4096-token prompt 144 us, 0.95 PFLOP/s; 16 packed prompts of up to 2500, 32/8 heads, d = 128
+// 275 us, 0.80 PFLOP/s (44% busy). fp32: 4096 tokens, 16/2 heads, d = 256 1140 us, d = 128 530 us,
+// 79 and 85% of the fp32 library product's 153 TFLOP/s. 8192 tokens without a mask, bf16,
 // d = 256, 128 and 64: without the softmax 7, 12 and 20% less time, with each operand read once
 // 10, 9 and 5%, without loads 7, 6 and 4%: no single part is in the way. Few rows: see ranges_of.
 //
@@ -716,8 +718,8 @@ int range_rows(const gdn_attn_dims& d)  // of the shape with ranges
 // Ranges that every tile's keys are divided into: what makes the estimate of the call's time least.
 // 256 workgroups run at a time; each costs its keys and about 128 more, and a join about 256 (a key
 // takes some 20 ns, d = 256 bf16). Undivided, a workgroup takes 128 rows. Measured (us of a call,
-// undivided / divided): d = 256, 16/2 heads, 16 tokens after 32752 684 / 56, 128 after 32640 686 / 109,
-// 512 after 8192 195 / 114; d = 128, 32/8 heads, 8 sequences of 8 tokens after 8192 134 / 85.
+// undivided / divided): d = 256, 16/2 heads, 16 tokens after 32752 684 / 56, 128 after 32640 686 / 104,
+// 512 after 8192 195 / 108; d = 128, 32/8 heads, 8 sequences of 8 tokens after 8192 134 / 85.
 int ranges_of(const gdn_attn_dims& d)
 {
     if (d.n == 0 || d.total_q == 0) return 1;
@@ -766,8 +768,12 @@ hipError_t launch_shape(const AttnCall& c)
     } else {
         if (ranges > 1) return launch_kernel<T, D, LSE, Few>(c, ranges);
         // Measured (us, bf16, Wide / Split / Twin; tiles of 256 rows). Few tiles of many keys, where
-        // one workgroup's time is the call's: d = 256, 16/2 heads, 4096-token prompt (256 tiles)
-        // 190 / 144 / 169, 2048 (128) 98 / 62 / 74; d = 128, 16/16 heads, 4096 (256) 109 / 79 / 91.
+        // one workgroup's time is the call's: d = 256, 16/2 heads, 2048-token prompt (128 tiles)
+        // 98 / 63 / 68, 4096 (256) 190 / 150 / 163, 4112 (257) 193 / 161 / 163, 4352 206 / 180 / 177,
+        // 5120 253 / 241 / 224, 6144 (384) 321 / 323 / 300, 7168 (448) 390 / 414 / 413; Split / Twin,
+        // d = 128, 16/16 heads, 4096 (256) 82 / 94, 4112 93 / 95, 5120 133 / 126; d = 64, 32/8 heads,
+        // 2048 (256) 35 / 32, 2064 42 / 34. A 257th tile makes the busiest CU's list longer in every
+        // shape. (Wide would also save 6% from 448 tiles of fewer keys.)
         // Few keys: 32 prompts of 64, 32/8 heads (256) 21 / 30 / 18; many tiles: 16 of 1024 (2048)
         // 205 / 270 / 193, 8192 (1024) 513 / 542 / 504. Long rows and many keys, where the traffic
         // of staging counts: d = 256, 8192 (512) 472 / 508 / 512, 16 of 1024 197 / 270 / 191.

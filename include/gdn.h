@@ -441,7 +441,7 @@ gdn_status gdn_kv_read(const gdn_kv_cache* cache, int64_t total, int32_t dtype, 
  * Scores, softmax statistics and sums are fp32; with bf16 inputs the softmax weights are
  * rounded to bf16 for the matrix product with V, with fp32 inputs nothing is rounded. A row is
  * divided by the sum of the weights that were multiplied, so that they add up to 1. A NaN
- * among what a row sees reaches its output.
+ * among what a row sees reaches its output: one in q or k all of it and lse, one in v its element.
  * Where few rows meet many keys the keys are divided into ranges that a second kernel joins, in
  * a fixed order: workspace then has gdn_attn_prefill_workspace_bytes(dims) bytes (0 when
  * nothing is divided, and for invalid arguments). That does not grow steadily with the sizes;
@@ -473,7 +473,8 @@ gdn_status gdn_attn_prefill(const gdn_attn_dims* dims, const void* q, const void
  * the host cannot see: positions from max_len on are not read; the work is split over it.
  * A long cache is split into ranges that are attended to separately and joined by a second
  * kernel, in a fixed order, so results are the same from run to run. Rounding and NaN as for
- * gdn_attn_prefill. workspace: gdn_attn_decode_workspace_bytes(cache, h_q, max_len) bytes (0
+ * gdn_attn_prefill; with a GDN_FP8 store and bf16 q a weight times its V row's scale, which is what
+ * is multiplied, loses bits where it is below 2^-126. workspace: gdn_attn_decode_workspace_bytes(cache, h_q, max_len) bytes (0
  * when nothing is split, and for invalid arguments). That does not grow steadily with max_len;
  * (4096 + u) * 16 * (4 * d + 16) bytes, u = n * h_kv * ceil(h_q / h_kv / 16), serve every one.
  */
