@@ -474,9 +474,10 @@ gdn_status gdn_attn_prefill(const gdn_attn_dims* dims, const void* q, const void
  * A long cache is split into ranges that are attended to separately and joined by a second
  * kernel, in a fixed order, so results are the same from run to run. Rounding and NaN as for
  * gdn_attn_prefill; with a GDN_FP8 store and bf16 q a weight times its V row's scale, which is what
- * is multiplied, loses bits where it is below 2^-126. workspace: gdn_attn_decode_workspace_bytes(cache, h_q, max_len) bytes (0
- * when nothing is split, and for invalid arguments). That does not grow steadily with max_len;
- * (4096 + u) * 16 * (4 * d + 16) bytes, u = n * h_kv * ceil(h_q / h_kv / 16), serve every one.
+ * is multiplied, loses bits where it is below 2^-126. workspace:
+ * gdn_attn_decode_workspace_bytes(cache, h_q, max_len) bytes (0 when nothing is split, and for
+ * invalid arguments). That does not grow steadily with max_len; (4096 + u) * 16 * (4 * d + 16)
+ * bytes, u = n * h_kv * ceil(h_q / h_kv / 16), serve every one.
  */
 size_t gdn_attn_decode_workspace_bytes(const gdn_kv_cache* cache, int32_t h_q, int64_t max_len);
 gdn_status gdn_attn_decode(const gdn_kv_cache* cache, int32_t h_q, int32_t dtype, float scale,
