@@ -8,7 +8,10 @@ HIP kernels; there is no Python or CPU fallback, and a missing libgdn.so is an e
 
 For a hybrid stack's softmax-attention layers there are a paged key-value cache
 (gdn_kv_write, gdn_kv_read), attention over packed prompts (gdn_attn_prefill) and of one new
-token over the cache (gdn_attn_decode); their tensors are described at each function.
+token over the cache (gdn_attn_decode); around them the norms and rotary positions of queries and
+keys (gdn_qk_norm_rope), the cache written with them on the way (gdn_kv_append), and attention of
+several new tokens over the cache, with a sliding window (gdn_attn_extend). Their tensors are
+described at each function.
 
 Layouts of the recurrence (see include/gdn.h): q, k [n, t, h_qk, d]; v [n, t, h_v, d]; g, beta [n, t, h_v]
 fp32; state [n, h_v, d, d] fp32 with element [i][j] = S[j][i]; out [n, t, h_v, d] fp32.
@@ -27,6 +30,8 @@ __all__ = [
     "calib_mfma_bf16", "calib_stream_copy", "gdn_prefill_segmented_noalloc", "gdn_noalloc_scratch_bytes",
     "debug_fill_lds", "gdn_kv_write", "gdn_kv_read", "gdn_attn_prefill", "gdn_attn_decode",
     "gdn_attn_prefill_workspace_bytes", "gdn_attn_decode_workspace_bytes", "KvCache", "AttnDims",
+    "gdn_qk_norm_rope", "gdn_kv_append", "gdn_attn_extend", "gdn_attn_extend_workspace_bytes", "NormRope",
+    "ExtendDims",
 ]
 
 GDN_F32, GDN_BF16, GDN_FP8 = 0, 1, 2
@@ -59,6 +64,22 @@ class AttnDims(ctypes.Structure):
                 ("q_token", ctypes.c_int64), ("q_head", ctypes.c_int64),
                 ("k_token", ctypes.c_int64), ("k_head", ctypes.c_int64),
                 ("v_token", ctypes.c_int64), ("v_head", ctypes.c_int64)]
+
+
+class NormRope(ctypes.Structure):
+    """gdn_norm_rope from include/gdn.h."""
+    _fields_ = [("eps", ctypes.c_float), ("weight_bias", ctypes.c_float), ("q_weight", ctypes.c_void_p),
+                ("k_weight", ctypes.c_void_p), ("rot", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("axes", ctypes.c_int32), ("rope_scale", ctypes.c_float), ("freq", ctypes.c_void_p),
+                ("axis", ctypes.c_void_p), ("pos", ctypes.c_void_p)]
+
+
+class ExtendDims(ctypes.Structure):
+    """gdn_extend_dims from include/gdn.h."""
+    _fields_ = [("total_q", ctypes.c_int64), ("max_q", ctypes.c_int64), ("max_len", ctypes.c_int64),
+                ("window", ctypes.c_int64), ("sinks", ctypes.c_int64), ("h_q", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("scale", ctypes.c_float), ("q_token", ctypes.c_int64),
+                ("q_head", ctypes.c_int64)]
 
 
 class GdnError(RuntimeError):
@@ -111,6 +132,12 @@ def _load():
         "gdn_attn_decode_workspace_bytes": (sz, [K, i32, i64]),
         "gdn_attn_decode": (ctypes.c_int, [K, i32, i32, ctypes.c_float, i64, P, i64, i64, P, P, P,
                                            P, sz, P]),
+        "gdn_qk_norm_rope": (ctypes.c_int, [ctypes.POINTER(NormRope), i64, i32, i32, i32, i32, P, i64, i64, P, i64,
+                                            i64, P, P, P]),
+        "gdn_kv_append": (ctypes.c_int, [K, ctypes.POINTER(NormRope), i64, i32, P, i64, i64, P, i64, i64, P, P, i32,
+                                         P, i64, i64, P, P]),
+        "gdn_attn_extend_workspace_bytes": (sz, [K, ctypes.POINTER(ExtendDims)]),
+        "gdn_attn_extend": (ctypes.c_int, [K, ctypes.POINTER(ExtendDims)] + [P] * 6 + [sz, P]),
         "gdn_debug_fill_lds": (ctypes.c_int, [ctypes.c_uint32, ctypes.c_int32, P, P]),
     }
     for name, (res, args) in sig.items():
@@ -719,4 +746,168 @@ def gdn_attn_decode(q, k_cache, v_cache, page_table, lens, *, max_len=None, k_sc
         wbytes, _queue(gpu, stream))
     if st:
         raise GdnError(st, "gdn_attn_decode")
+    return out
+
+
+# ---------------------------------------------------------------- around the attention layers
+
+def _norm_rope(total, d, dtype, index, positions, freq, axis, interleaved, rope_scale, q_weight, k_weight,
+               weight_bias, eps, placed):
+    """gdn_norm_rope of these tensors; placed: without positions a token turns by its place."""
+    rot, axes, fp, ap, pp = 0, 1, None, None, None
+    if freq is not None:
+        if not isinstance(freq, _Tensor) or freq.dim() != 1:
+            raise ValueError("freq must be a float32 tensor [rot / 2]")
+        rot = 2 * freq.shape[0]
+        fp = _dense("freq", freq, (rot // 2,), torch.float32, index)
+        if axis is not None:
+            ap = _dense("axis", axis, (rot // 2,), _u8, index)
+        if positions is not None:
+            if not isinstance(positions, _Tensor) or positions.dim() not in (1, 2):
+                raise ValueError("positions must be an int32 tensor [tokens] or [axes, tokens]")
+            if positions.dim() == 2:
+                axes = positions.shape[0]
+            pp = _dense("positions", positions, (total,) if positions.dim() == 1 else (axes, total), _i32, index)
+        elif not placed:
+            raise ValueError("positions are needed with freq")
+    elif positions is not None or axis is not None:
+        raise ValueError("positions and axis need freq")
+    qw = None if q_weight is None else _dense("q_weight", q_weight, (d,), dtype, index)
+    kw = None if k_weight is None else _dense("k_weight", k_weight, (d,), dtype, index)
+    return NormRope(eps, weight_bias, qw, kw, rot, 1 if interleaved else 0, axes, rope_scale, fp, ap, pp)
+
+
+def gdn_qk_norm_rope(q, k=None, positions=None, *, freq=None, axis=None, interleaved=False, rope_scale=1.0,
+                     q_weight=None, k_weight=None, weight_bias=0.0, eps=1e-6, q_out=None, k_out=None, stream=None):
+    """Norms of queries and keys for each head, and their rotary positions, in one pass.
+
+    q [total, h_q, d] and k [total, h_kv, d] (bfloat16 or float32; tokens and heads may be strided; k
+    may be None). With q_weight (k_weight) [d], of q's dtype, each row is divided by the root of its
+    mean square plus eps and multiplied by weight_bias + weight. With freq (float32 [rot / 2], rot a
+    multiple of 16) the first rot elements are then turned, pair p by the angle freq[p] * position and
+    times rope_scale: elements p and p + rot / 2, or with interleaved 2 p and 2 p + 1. positions: int32
+    [total], or [axes, total] with axis (uint8 [rot / 2]) the axis of each pair. Computed in fp32,
+    angles in 64 bits, rounded once. Returns (q_out, k_out), dense, of q's dtype (k_out None
+    without k)."""
+    t = _dtype_id(q)
+    gpu = _gpu(q)
+    qp, qt, qh = _rows("q", q, q.dtype, gpu)
+    total, hq, d = q.shape
+    kp, kt, kh, hk, kop = None, 0, 0, 0, None
+    if k is not None:
+        kp, kt, kh = _rows("k", k, q.dtype, gpu)
+        hk = k.shape[1]
+        if k.shape[0] != total or k.shape[2] != d:
+            raise ValueError(f"k must have shape [{total}, h_kv, {d}]")
+    elif k_weight is not None or k_out is not None:
+        raise ValueError("k_weight and k_out need k")
+    f = _norm_rope(total, d, q.dtype, gpu, positions, freq, axis, interleaved, rope_scale, q_weight, k_weight,
+                   weight_bias, eps, False)
+    if q_out is None:
+        q_out = _empty(q.shape, q.dtype, gpu, stream)
+    if k is not None:
+        if k_out is None:
+            k_out = _empty(k.shape, q.dtype, gpu, stream)
+        kop = _dense("k_out", k_out, k.shape, q.dtype, gpu)
+    st = _load().gdn_qk_norm_rope(ctypes.byref(f), total, hq, hk, d, t, qp, qt, qh, kp, kt, kh,
+                                  _dense("q_out", q_out, q.shape, q.dtype, gpu), kop, _queue(gpu, stream))
+    if st:
+        raise GdnError(st, "gdn_qk_norm_rope")
+    return q_out, k_out
+
+
+def gdn_kv_append(k, v, k_cache, v_cache, page_table, start, cu_seqlens=None, *, positions=None, freq=None, axis=None,
+                  interleaved=False, rope_scale=1.0, k_weight=None, q=None, q_weight=None, weight_bias=0.0, eps=1e-6,
+                  q_out=None, k_scale=None, v_scale=None, stream=None):
+    """Write new tokens into a paged cache, their keys normed and rotated on the way, and their queries
+    too: what an attention layer does between its projections and its attention, in one launch.
+
+    k, v, the cache, start and cu_seqlens as for gdn_kv_write; weights, freq, positions and the rest as
+    for gdn_qk_norm_rope, but that without positions a token turns by its place in its sequence,
+    start[s] + i. q [total, h_q, d] (may be strided, and None) is normed and rotated into q_out
+    (dense), which is returned (None without q); rows of no sequence are left as they are there."""
+    t = _dtype_id(k)
+    c, gpu = _cache_of(k_cache, v_cache, page_table, k_scale, v_scale)
+    kp, kt, kh = _rows("k", k, k.dtype, gpu)
+    vp, vt, vh = _rows("v", v, k.dtype, gpu)
+    total = k.shape[0]
+    if k.shape[1:] != (c.h_kv, c.d) or v.shape != k.shape:
+        raise ValueError(f"k and v must have shape {(total, c.h_kv, c.d)}")
+    sp = _index("start", start, (c.n,), gpu)
+    cp = _index("cu_seqlens", cu_seqlens, (c.n + 1,), gpu)
+    f = _norm_rope(total, c.d, k.dtype, gpu, positions, freq, axis, interleaved, rope_scale, q_weight, k_weight,
+                   weight_bias, eps, True)
+    qp, qt, qh, hq, qop = None, 0, 0, 0, None
+    if q is not None:
+        qp, qt, qh = _rows("q", q, k.dtype, gpu)
+        hq = q.shape[1]
+        if q.shape[0] != total or q.shape[2] != c.d:
+            raise ValueError(f"q must have shape [{total}, h_q, {c.d}]")
+        if q_out is None:
+            q_out = _empty(q.shape, k.dtype, gpu, stream)
+        qop = _dense("q_out", q_out, q.shape, k.dtype, gpu)
+    elif q_weight is not None or q_out is not None:
+        raise ValueError("q_weight and q_out need q")
+    st = _load().gdn_kv_append(ctypes.byref(c), ctypes.byref(f), total, t, kp, kt, kh, vp, vt, vh, sp, cp, hq, qp, qt, qh,
+                               qop, _queue(gpu, stream))
+    if st:
+        raise GdnError(st, "gdn_kv_append")
+    return q_out
+
+
+def gdn_attn_extend_workspace_bytes(n, max_pages, page_size, total_q, h_q, h_kv, d, *, max_q=None, max_len=None, window=0,
+                                    sinks=0, dtype=torch.bfloat16, store=None) -> int:
+    """Workspace bytes of gdn_attn_extend for these sizes (max_q, max_len as there; store: the cache's
+    dtype if not dtype)."""
+    store = dtype if store is None else store
+    c = KvCache(n, 1, max_pages, page_size, h_kv, d, _POOLS.get(store, -1))
+    dims = ExtendDims(total_q, total_q if max_q is None else max_q, max_pages * page_size if max_len is None else max_len,
+                      window, sinks, h_q, _DTYPES.get(dtype, -1), 1.0, h_q * d, d)
+    return int(_load().gdn_attn_extend_workspace_bytes(ctypes.byref(c), ctypes.byref(dims)))
+
+
+def gdn_attn_extend(q, k_cache, v_cache, page_table, lens, cu_q=None, *, window=0, sinks=0, max_q=None, max_len=None,
+                    k_scale=None, v_scale=None, scale=None, out=None, lse=None, workspace=None, stream=None):
+    """Attention of new tokens over a paged cache that holds them already: the next piece of a prompt,
+    a few drafted tokens, or one token per sequence (cu_q None).
+
+    q [total, h_q, d] (bfloat16 or float32; tokens and heads may be strided): sequence s has rows
+    cu_q[s] to cu_q[s + 1] - 1 (int32 [n + 1]), the last of which is the token at position
+    lens[s] - 1 (int32 [n]; the new tokens, written before, are counted). A row sees the positions up
+    to its own; with window > 0 only the last `window` of them, and the first `sinks` of the sequence.
+    max_q and max_len are bounds on a sequence's rows and length that the host knows (default: total
+    and what the page table can hold; tight ones divide the work better): rows from max_q on are not
+    computed, positions from max_len on not read. The cache as for gdn_kv_write, lse and workspace
+    as for gdn_attn_prefill, scale defaults to 1 / sqrt(d). Returns out [total, h_q, d] of q's dtype."""
+    t = _dtype_id(q)
+    c, gpu = _cache_of(k_cache, v_cache, page_table, k_scale, v_scale)
+    qp, qt, qh = _rows("q", q, q.dtype, gpu)
+    total, hq, d = q.shape
+    if d != c.d:
+        raise ValueError(f"q must have shape [total, h_q, {c.d}]")
+    if cu_q is None and total != c.n:
+        raise ValueError(f"without cu_q, q must have one row per sequence, {c.n}")
+    if max_q is None:
+        max_q = total if cu_q is not None else 1
+    if max_len is None:
+        max_len = c.max_pages * c.page_size
+    if out is None:
+        out = _empty(q.shape, q.dtype, gpu, stream)
+        op = out.data_ptr()
+    else:
+        op = _dense("out", out, q.shape, q.dtype, gpu)
+    lp = None if lse is None else _dense("lse", lse, (total, hq), torch.float32, gpu)
+    dims = ExtendDims(total, max_q if cu_q is not None else min(max_q, 1), max_len, window, sinks, hq, t,
+                      d ** -0.5 if scale is None else scale, qt, qh)
+    lib = _load()
+    if workspace is None:
+        need = lib.gdn_attn_extend_workspace_bytes(ctypes.byref(c), ctypes.byref(dims))
+        if need:
+            workspace = _empty(need, _u8, gpu, stream)
+    wbytes = 0 if workspace is None else _check_workspace(workspace, q.device)
+    st = lib.gdn_attn_extend(ctypes.byref(c), ctypes.byref(dims), qp, _index("cu_q", cu_q, (c.n + 1,), gpu),
+                             _index("lens", lens, (c.n,), gpu), op, lp, None if workspace is None else workspace.data_ptr(),
+                             wbytes, _queue(gpu, stream))
+    if st:
+        raise GdnError(st, "gdn_attn_extend")
     return out

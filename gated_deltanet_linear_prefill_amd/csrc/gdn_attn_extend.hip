@@ -1,0 +1,766 @@
+// gdn_attn_extend.hip -- attention of new tokens over the paged cache: a few rows per sequence.
+//
+// Rows. The G = h_q / h_kv heads of a KV head read the same keys, so the rows of one (sequence, KV
+// head) are numbered position-major, row r being position r / G, head r % G, and a workgroup takes
+// M = 16 CT of them. Sequence s has the tiles [floor(cu[s] G / M) + s, floor(cu[s + 1] G / M) + s + 1),
+// which are disjoint and enough; a workgroup without a tile leaves.
+//
+// Positions. What a tile's rows see together is [0, sinks) and the stretch from the first row's window
+// to the last row. Both are taken in whole 16-position blocks, which never cross a page, and numbered
+// through ("virtual" positions); ranges and steps are of these, so that a window costs its own
+// length and no page outside it is looked at.
+//
+// Bound by the bytes of the cache. A wave takes 32 positions (16 for long rows) of K and V into
+// registers, for all M rows, with its own softmax state; waves are joined in LDS, ranges by a second
+// kernel through the workspace. 16x16 MFMA, one row per column: S^T = K Q^T takes 16-byte pieces of K
+// rows as its A operand as they were loaded, and its result is the B operand of O^T = V^T P^T, if
+// lane (c, g) brings pieces of the V rows of keys 4 g + i. No K, V or weight passes between lanes;
+// Q is read from LDS. The next step's K is loaded when this step's scores are done, its V when this
+// step's product is.
+//
+// A key that only some rows see may hold a NaN or an infinity, and 0 x NaN is NaN: in steps with
+// masked keys such elements of V are left out of the product and added to the rows that see them.
+#include "gdn_attn_internal.hpp"
+
+namespace gdn {
+namespace {
+
+constexpr int kWaves = 4;
+constexpr int kRange = 32 * kWaves;  // ranges are multiples of this: a step of every wave
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+struct Plan {
+    int ct;              // tiles of 16 rows a workgroup takes
+    int64_t slots;       // tiles of one KV head that the grid has room for
+    int64_t units;       // ... of all KV heads
+    int64_t range;       // virtual positions of a range
+    int64_t ranges;
+};
+
+// Virtual positions that a tile may have.
+int64_t longest(const gdn_kv_cache& c, const gdn_extend_dims& d, int m)
+{
+    if (d.window == 0) return d.max_len;
+    const int64_t g = d.h_q / c.h_kv;
+    const int64_t w = d.window + (m - 1) / g + 1 + 15 + (d.sinks + 15) / 16 * 16;
+    return w < d.max_len ? w : d.max_len;
+}
+
+Plan make_plan(const gdn_kv_cache& c, const gdn_extend_dims& d)
+{
+    Plan p;
+    const int64_t g = d.h_q / c.h_kv, rows = d.max_q * g;
+    p.ct = rows <= 16 ? 1 : rows <= 32 || c.d == 256 ? 2 : 4;
+    const int m = 16 * p.ct;
+    p.slots = d.max_q == 1 ? c.n * ((g + m - 1) / m) : d.total_q * g / m + c.n;
+    p.units = p.slots * c.h_kv;
+    const int64_t tiles = (d.total_q * g + m - 1) / m;
+    const int64_t real = (tiles > c.n ? tiles : c.n) * c.h_kv;
+    const int64_t len = longest(c, d, m), steps = len > 0 ? (len + kRange - 1) / kRange : 1;
+    const int64_t most = real * steps;
+    int64_t want = most / 8 < 4096 ? most / 8 : 4096;
+    if (want < 256 || c.n == 1) want = 256;
+    int64_t ranges = (want + real - 1) / real;
+    if (ranges > (steps + 1) / 2) ranges = (steps + 1) / 2;
+    if (steps <= 4) ranges = 1;
+    if (ranges > 0x7fffffff / p.units) ranges = 0x7fffffff / p.units;  // the grid
+    if (ranges < 1) ranges = 1;
+    const int64_t per = (steps + ranges - 1) / ranges;
+    p.range = per * kRange;
+    p.ranges = (steps + per - 1) / per;
+    return p;
+}
+
+// Workspace of one call: O sums [unit][range][M][D] fp32, then (m, l, exact l, -) of each row.
+struct Partials {
+    float* o;
+    float4* ml;
+};
+
+struct Args {
+    ExtendCall c;
+    int64_t range;
+    int ranges, slots, page_shift;
+    Partials part;
+};
+
+// A tile: rows row0 .. of the `rows` that its sequence has, and the positions that they see.
+struct Tile {
+    int seq, q0, rows, row0, g;
+    int first, last;       // positions of its first and last row
+    int shift;             // position of row 0 of the sequence
+    int sink, skip, len;   // virtual positions: [0, sink) as they are, then [sink, len) + skip
+    __device__ __forceinline__ int pos(int v) const { return v < sink ? v : v + skip; }
+};
+
+__device__ __forceinline__ int clamp_to(int x, int hi)
+{
+    return x < 0 ? 0 : (x > hi ? hi : x);
+}
+
+template <int M>
+__device__ __forceinline__ bool find_tile(const ExtendCall& p, int slot, Tile* t)
+{
+    const int g = p.d.h_q / p.c.h_kv, n = (int)p.c.n, total = (int)p.d.total_q;
+    int s = 0, qa, qb, local;
+    if (p.d.max_q == 1) {  // a sequence has the tiles of one token, or none
+        const int tiles = (g + M - 1) / M;
+        s = slot / tiles;
+        if (s >= n) return false;
+        qa = p.cu_q ? clamp_to(p.cu_q[s], total) : s;
+        qb = p.cu_q ? clamp_to(p.cu_q[s + 1], total) : s + 1;
+        local = tiles - 1 - (slot - s * tiles);
+    } else {
+        const int lane = threadIdx.x & 63;
+        auto base = [&](int x) { return (int)((int64_t)clamp_to(p.cu_q[x], total) * g / M) + x; };
+        for (int span = n; span > 1;) {  // the sequence is in [s, s + span)
+            const int step = (span + 63) / 64, at = s + lane * step;
+            const bool before = lane * step < span && (lane == 0 || base(at) <= slot);
+            const int x = 63 - __builtin_clzll(__ballot(before) | 1);  // the last lane not past the slot
+            s += x * step;
+            span = span - x * step < step ? span - x * step : step;
+        }
+        s = __builtin_amdgcn_readfirstlane(s);
+        qa = clamp_to(p.cu_q[s], total);
+        qb = clamp_to(p.cu_q[s + 1], total);
+        local = slot - ((int)((int64_t)qa * g / M) + s);
+    }
+    const int len_q = qb - qa;
+    if (len_q <= 0 || local < 0) return false;
+    t->seq = s;
+    t->q0 = qa;
+    t->g = g;
+    t->rows = (len_q < p.d.max_q ? len_q : (int)p.d.max_q) * g;
+    const int tiles = (t->rows + M - 1) / M;
+    if (local >= tiles) return false;
+    t->row0 = (tiles - 1 - local) * M;  // the last, which see most, first
+    int len = p.lens[s];
+    len = len < p.d.max_len ? len : (int)p.d.max_len;
+    len = len < 0 ? 0 : len;
+    t->shift = len - len_q;
+    t->first = t->shift + t->row0 / g;
+    t->last = t->shift + ((t->row0 + M < t->rows ? t->row0 + M : t->rows) - 1) / g;
+    const int w = (int)p.d.window, lo = w && t->first >= w ? (t->first - w + 1) & ~15 : 0;
+    const int sinks = (int)((p.d.sinks + 15) & ~15);
+    t->sink = sinks < lo ? sinks : lo;
+    t->skip = lo - t->sink;
+    t->len = t->last < 0 ? 0 : t->last + 1 - t->skip;
+    return true;
+}
+
+template <typename T, bool FP8, int D, int CT>
+struct Cfg {
+    // bytes of a K/V element, elements of a V row per lane and load, loads
+    static constexpr int ES = FP8 ? 1 : (int)sizeof(T);
+    static constexpr int VL = D / 16;                          // elements of a V row per lane
+    static constexpr int EPL = VL * ES > 16 ? 16 / ES : VL;    // ... per load
+    static constexpr int U = VL / EPL;
+    static constexpr int KL = D * ES / 64;                     // 16-byte loads of a K row per lane
+    static constexpr int EPK = 16 / ES;                        // elements of each
+    // 16-position blocks of a step: K and V rows of a step stay in registers
+    static constexpr int NB = D * ES > 512 ? 1 : 2, STEP = 16 * NB;
+    static constexpr int QSTRIDE = D * (int)sizeof(T) + 16;    // bytes of a row of Q in LDS
+    static constexpr int M = 16 * CT;
+    // registers of O, K and V; with 512 a wave there is one wave a SIMD
+    static constexpr int REGS = CT * VL * 4 + 2 * NB * KL * 4;
+    static constexpr int PER_SIMD = REGS > 192 ? 1 : 2;
+};
+
+template <int BYTES>
+struct Piece;
+template <> struct Piece<4> { typedef uint32_t type; };
+template <> struct Piece<8> { typedef u32x2_t type; };
+template <> struct Piece<16> { typedef u32x4_t type; };
+
+template <typename P>
+__device__ __forceinline__ uint32_t word(const P& p, int i)
+{
+    if constexpr (sizeof(P) == 4) return p;
+    else return p[i];
+}
+
+template <typename P>
+__device__ __forceinline__ void set_word(P& p, int i, uint32_t x)
+{
+    if constexpr (sizeof(P) == 4) p = x;
+    else p[i] = x;
+}
+
+__device__ __forceinline__ float round_bf16(float x)
+{
+    return (float)(__bf16)x;
+}
+
+__device__ __forceinline__ uint32_t cvt_bf16_fp8(uint32_t w, bool hi)
+{
+    return hi ? __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, true))
+              : __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, false));
+}
+
+// All ones in the places of a word's elements of ES bytes that are NaN or infinite.
+template <int ES>
+__device__ __forceinline__ uint32_t odd_mask(uint32_t w)
+{
+    if constexpr (ES == 4) return (w & 0x7f800000u) == 0x7f800000u ? 0xffffffffu : 0u;
+    else if constexpr (ES == 2) return ((((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u) >> 15) * 0xffffu;
+    else return ((((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7) * 0xffu;
+}
+
+// An element of a V row that is NaN or infinite, else 0.
+template <typename T, bool FP8>
+__device__ __forceinline__ float odd_element(const char* row, int e)
+{
+    if constexpr (FP8) {
+        return (static_cast<uint8_t>(row[e]) & 0x7f) == 0x7f ? __uint_as_float(0x7fc00000u) : 0.f;
+    } else {
+        const float x = load1_f32(reinterpret_cast<const T*>(row) + e);
+        return fabsf(x) <= 3.4028234e38f ? 0.f : x;
+    }
+}
+
+template <typename T, bool FP8, int D, int CT>
+__global__ void __launch_bounds__(64 * kWaves, (Cfg<T, FP8, D, CT>::PER_SIMD)) extend_kernel(Args a)
+{
+    using C = Cfg<T, FP8, D, CT>;
+    using VP = typename Piece<C::EPL * C::ES>::type;
+    constexpr bool BF = sizeof(T) == 2;
+    constexpr int M = C::M, NB = C::NB;
+    const ExtendCall& p = a.c;
+    constexpr int O_BYTES = kWaves * 16 * (D + 4) * 4, Q_BYTES = M * C::QSTRIDE;
+    __shared__ __align__(16) char s_buf[O_BYTES > Q_BYTES ? O_BYTES : Q_BYTES];
+    __shared__ float s_m[kWaves][M];
+    __shared__ float2 s_l[kWaves][M];
+    char* const s_q = s_buf;  // until the waves are joined
+    float(*const s_o)[16][D + 4] = reinterpret_cast<float(*)[16][D + 4]>(s_buf);
+
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int c = lane & 15, g = lane >> 4;
+    // ranges of one index lie together in the grid: late ones, which few tiles have, spread over all XCDs
+    const uint32_t units = (uint32_t)a.slots * (uint32_t)p.c.h_kv;
+    const uint32_t unit = block_index() % units;
+    const int rg = (int)(block_index() / units);
+    if (rg >= a.ranges) return;  // past the grid's end
+    const int kvh = (int)(unit % (uint32_t)p.c.h_kv);
+    Tile t;
+    if (!find_tile<M>(p, (int)(unit / (uint32_t)p.c.h_kv), &t)) return;
+    const int64_t begin64 = rg * a.range;
+    if (rg > 0 && begin64 >= t.len) return;  // the join does not read this range
+    const bool whole = t.len <= a.range;     // nothing to join
+    const int begin = (int)begin64;
+    const int end = t.len - begin < a.range ? t.len : (int)(begin64 + a.range);
+
+    // Q: row r of the tile, rows past the sequence's repeat its last
+    const int left = t.rows - t.row0, have = left < M ? left : M;
+    constexpr int CH = D * (int)sizeof(T) / 16;
+    for (int x = threadIdx.x; x < M * CH; x += 64 * kWaves) {
+        const int r = t.row0 + (x / CH < have ? x / CH : have - 1), i = r / t.g;
+        *reinterpret_cast<u32x4_t*>(s_q + x / CH * C::QSTRIDE + x % CH * 16) = *reinterpret_cast<const u32x4_t*>(
+            static_cast<const T*>(p.q) + (int64_t)(t.q0 + i) * p.d.q_token +
+            (int64_t)(kvh * t.g + r - i * t.g) * p.d.q_head + x % CH * (16 / (int)sizeof(T)));
+    }
+    int at[CT];  // this lane's rows' positions
+#pragma unroll
+    for (int x = 0; x < CT; ++x) at[x] = t.shift + (t.row0 + (16 * x + c < have ? 16 * x + c : have - 1)) / t.g;
+    int qoff = c * C::QSTRIDE + g * C::EPK * (int)sizeof(T);
+    auto q_at = [&](int ct, int i, int x) __attribute__((always_inline)) {
+        return *reinterpret_cast<const u32x4_t*>(s_q + qoff + ct * 16 * C::QSTRIDE + i * 4 * C::EPK * (int)sizeof(T) + x * 16);
+    };
+    __syncthreads();
+
+    const int window = (int)p.d.window, sinks = (int)p.d.sinks;
+    // every row sees the positions up to `first` that are in the last row's window or among the sinks
+    const int from = window && t.last >= window ? t.last - window + 1 : 0;
+    f32x4_t o[CT][C::VL];
+    float m[CT], l[CT], exact[CT];
+#pragma unroll
+    for (int x = 0; x < CT; ++x) {
+#pragma unroll
+        for (int j = 0; j < C::VL; ++j) o[x][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        m[x] = -INFINITY;
+        l[x] = exact[x] = 0.f;
+    }
+    const float cs = p.d.scale * kLog2e;
+    const int32_t* table = p.c.page_table + t.seq * p.c.max_pages;
+    const char* kpool = static_cast<const char*>(p.c.k);
+    const char* vpool = static_cast<const char*>(p.c.v);
+
+    u32x4_t kx[NB][C::KL];
+    VP vx[4 * NB][C::U];
+    uint32_t sk[NB], sv[NB];
+
+    // Row of the pools where block b of the step at virtual position j0 begins, and its position; absent
+    // pages read page 0 (and are masked), blocks past the range's end the last before it.
+    auto block_row = [&](int j0, int b, bool* there, int* pos) {
+        const int v = j0 + 16 * b;
+        *pos = t.pos(v);
+        const int from = v < end ? *pos : t.pos(end - 1);
+        const int64_t page = table[from >> a.page_shift];
+        *there = page >= 0 && page < p.c.num_pages;
+        return (((*there ? page : 0) * p.c.h_kv + kvh) << a.page_shift) + ((v < end ? *pos : from & ~15) & (p.c.page_size - 1));
+    };
+    auto load_k = [&](const int64_t* row) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            const char* kr = kpool + (row[b] + c) * (D * C::ES) + g * 16;
+#pragma unroll
+            for (int i = 0; i < C::KL; ++i) kx[b][i] = *reinterpret_cast<const u32x4_t*>(kr + i * 64);
+            if constexpr (FP8) sk[b] = *reinterpret_cast<const uint32_t*>(p.c.k_scale + row[b] + 4 * g);
+        }
+    };
+    auto load_v = [&](const int64_t* row) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const char* vr = vpool + (row[b] + 4 * g + i) * (D * C::ES) + c * (C::EPL * C::ES);
+#pragma unroll
+                for (int u = 0; u < C::U; ++u)
+                    vx[4 * b + i][u] = *reinterpret_cast<const VP*>(vr + u * (16 * C::EPL * C::ES));
+            }
+            if constexpr (FP8) sv[b] = *reinterpret_cast<const uint32_t*>(p.c.v_scale + row[b] + 4 * g);
+        }
+    };
+
+    int64_t row[NB];
+    bool there[NB];
+    int pos[NB];
+    const int first = begin + wave * C::STEP;
+    if (first < end) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b) row[b] = block_row(first, b, &there[b], &pos[b]);
+        load_k(row);
+        load_v(row);
+    }
+    // the host keeps lengths below 2^31 - 2^16, so that a step past the end is still an int
+    for (int j0 = first; j0 < end; j0 += kWaves * C::STEP) {
+        const int next = j0 + kWaves * C::STEP;
+        int64_t nrow[NB] = {};
+        bool nthere[NB] = {};
+        int npos[NB] = {};
+        if (next < end)
+#pragma unroll
+            for (int b = 0; b < NB; ++b) nrow[b] = block_row(next, b, &nthere[b], &npos[b]);
+
+        // scores
+        asm volatile("" : "+v"(qoff));  // read again in every step, not kept
+        float s[CT][4 * NB];
+        {
+            f32x4_t acc[CT][NB];
+#pragma unroll
+            for (int x = 0; x < CT; ++x)
+#pragma unroll
+                for (int b = 0; b < NB; ++b) acc[x][b] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < C::KL; ++i) {
+                constexpr int QP = C::EPK * (int)sizeof(T) / 16;  // 16-byte pieces of a load's elements
+#pragma unroll
+                for (int f = 0; f < QP; ++f) {
+                    u32x4_t k16[NB];
+                    if constexpr (BF)
+#pragma unroll
+                        for (int b = 0; b < NB; ++b) {
+                            if constexpr (FP8)
+                                k16[b] = u32x4_t{cvt_bf16_fp8(kx[b][i][2 * f], false), cvt_bf16_fp8(kx[b][i][2 * f], true),
+                                                 cvt_bf16_fp8(kx[b][i][2 * f + 1], false), cvt_bf16_fp8(kx[b][i][2 * f + 1], true)};
+                            else
+                                k16[b] = kx[b][i];
+                        }
+#pragma unroll
+                    for (int x = 0; x < CT; ++x) {
+                        const u32x4_t qq = q_at(x, i, f);
+#pragma unroll
+                        for (int b = 0; b < NB; ++b) {
+                            if constexpr (BF) {
+                                acc[x][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, k16[b]),
+                                                                                    __builtin_bit_cast(bf16x8_t, qq), acc[x][b], 0, 0, 0);
+                            } else {
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    float k1;
+                                    if constexpr (FP8)
+                                        k1 = e & 2 ? __builtin_amdgcn_cvt_pk_f32_fp8((int)kx[b][i][f], true)[e & 1]
+                                                   : __builtin_amdgcn_cvt_pk_f32_fp8((int)kx[b][i][f], false)[e & 1];
+                                    else
+                                        k1 = __uint_as_float(kx[b][i][e]);
+                                    acc[x][b] = __builtin_amdgcn_mfma_f32_16x16x4f32(k1, __uint_as_float(qq[e]), acc[x][b], 0, 0, 0);
+                                }
+                            }
+                        }
+                    }
+                }
+            }
+#pragma unroll
+            for (int x = 0; x < CT; ++x)
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        s[x][4 * b + i] = acc[x][b][i] * cs;
+                        if constexpr (FP8) s[x][4 * b + i] *= scale_of((sk[b] >> (8 * i)) & 0xff);
+                    }
+        }
+        if (next < end) load_k(nrow);
+
+        bool masked = false;
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+            masked |= !there[b] || j0 + 16 * b >= end || pos[b] + 15 > t.first || (pos[b] < from && pos[b] + 15 >= sinks);
+        bool odd = false;
+        uint32_t seen[CT];  // bits of this lane's keys
+        if (masked) {
+#pragma unroll
+            for (int x = 0; x < CT; ++x) seen[x] = 0;
+            uint32_t found = 0;
+#pragma unroll
+            for (int i = 0; i < 4 * NB; ++i) {
+                const int b = i / 4, j = pos[b] + 4 * g + i % 4;
+                const bool exists = there[b] && j0 + 16 * b < end && j <= t.last;
+                if (!exists) {  // what lies there is anything: not into the product
+#pragma unroll
+                    for (int u = 0; u < C::U; ++u) vx[i][u] = VP{};
+                    if constexpr (FP8) sv[b] &= ~(0xffu << (8 * (i % 4)));
+                }
+#pragma unroll
+                for (int x = 0; x < CT; ++x) {
+                    const bool sees = exists && j <= at[x] && (!window || j > at[x] - window || j < sinks);
+                    s[x][i] = sees ? s[x][i] : -INFINITY;
+                    seen[x] |= (uint32_t)sees << i;
+                }
+#pragma unroll
+                for (int u = 0; u < C::U; ++u)
+#pragma unroll
+                    for (int w = 0; w < (int)sizeof(VP) / 4; ++w) found |= odd_mask<C::ES>(word(vx[i][u], w));
+            }
+            odd = __any(found != 0);
+            if (odd)
+#pragma unroll
+                for (int i = 0; i < 4 * NB; ++i)
+#pragma unroll
+                    for (int u = 0; u < C::U; ++u)
+#pragma unroll
+                        for (int w = 0; w < (int)sizeof(VP) / 4; ++w)
+                            set_word(vx[i][u], w, word(vx[i][u], w) & ~odd_mask<C::ES>(word(vx[i][u], w)));
+        }
+
+        u32x4_t pw[CT];
+#pragma unroll
+        for (int x = 0; x < CT; ++x) {
+            // softmax; the reference maximum moves only when weights would pass 2^8
+            float mx = s[x][0];
+#pragma unroll
+            for (int i = 1; i < 4 * NB; ++i) mx = fmaxf(mx, s[x][i]);
+            if (__any(mx > m[x] && (m[x] == -INFINITY || mx > m[x] + 8.f))) {
+                const auto a16 = __builtin_amdgcn_permlane16_swap(__float_as_uint(mx), __float_as_uint(mx), false, false);
+                mx = fmaxf(__uint_as_float(a16[0]), __uint_as_float(a16[1]));
+                const auto a32 = __builtin_amdgcn_permlane32_swap(__float_as_uint(mx), __float_as_uint(mx), false, false);
+                mx = fmaxf(__uint_as_float(a32[0]), __uint_as_float(a32[1]));
+                const float mn = fmaxf(m[x], mx);  // the same in all lanes of a row
+                const float f = mn == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m[x] - mn);
+                m[x] = mn;
+                l[x] *= f;
+                exact[x] *= f;
+#pragma unroll
+                for (int j = 0; j < C::VL; ++j) o[x][j] *= f;
+            }
+            const float ref = m[x] == -INFINITY ? 0.f : m[x];
+            // Weights. For the product with bf16 V they are rounded to bf16; l is of what V is multiplied
+            // by, so that a rounding that all elements share cancels; lse is of the unrounded sum.
+#pragma unroll
+            for (int i = 0; i < 4 * NB; ++i) {
+                s[x][i] = __builtin_amdgcn_exp2f(s[x][i] - ref);
+                exact[x] += s[x][i];
+                if constexpr (BF) s[x][i] = round_bf16(s[x][i]);
+                l[x] += s[x][i];
+                // exact, but for rows of V so small that the product is below the normal range
+                if constexpr (FP8) {
+                    s[x][i] *= scale_of((sv[i / 4] >> (8 * (i % 4))) & 0xff);
+                    if (masked && !(seen[x] >> i & 1)) s[x][i] = 0.f;
+                }
+            }
+            if constexpr (BF)
+                pw[x] = u32x4_t{pack_bf16(s[x][0], s[x][1]), pack_bf16(s[x][2], s[x][3]), pack_bf16(s[x][4], s[x][5]),
+                                pack_bf16(s[x][6], s[x][7])};
+        }
+
+        // O^T += V^T P^T; o[.][u * EPL + j] rows are elements 16 EPL u + EPL (4 g + i) + j
+        if constexpr (BF) {
+            auto add = [&](int y, u32x4_t v) __attribute__((always_inline)) {
+#pragma unroll
+                for (int x = 0; x < CT; ++x)
+                    o[x][y] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, v),
+                                                                      __builtin_bit_cast(bf16x8_t, pw[x]), o[x][y], 0, 0, 0);
+            };
+#pragma unroll
+            for (int u = 0; u < C::U; ++u) {
+                if constexpr (!FP8) {
+#pragma unroll
+                    for (int j = 0; j < C::EPL; ++j) {
+                        u32x4_t v;
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            v[x] = __builtin_amdgcn_perm(word(vx[2 * x + 1][u], j / 2), word(vx[2 * x][u], j / 2),
+                                                         j & 1 ? 0x07060302u : 0x05040100u);
+                        add(u * C::EPL + j, v);
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < C::EPL; j += 2) {
+                        u32x4_t v0, v1;
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            // bytes j and j + 1 of two keys, interleaved
+                            const uint32_t y = __builtin_amdgcn_perm(word(vx[2 * x + 1][u], j / 4), word(vx[2 * x][u], j / 4),
+                                                                     j & 2 ? 0x07030602u : 0x05010400u);
+                            v0[x] = cvt_bf16_fp8(y, false);
+                            v1[x] = cvt_bf16_fp8(y, true);
+                        }
+                        add(u * C::EPL + j, v0);
+                        add(u * C::EPL + j + 1, v1);
+                    }
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4 * NB; ++i)
+#pragma unroll
+                for (int u = 0; u < C::U; ++u)
+#pragma unroll
+                    for (int j = 0; j < C::EPL; ++j) {
+                        float v;
+                        if constexpr (!FP8) v = __uint_as_float(word(vx[i][u], j));
+                        else v = j & 2 ? __builtin_amdgcn_cvt_pk_f32_fp8((int)word(vx[i][u], j / 4), true)[j & 1]
+                                       : __builtin_amdgcn_cvt_pk_f32_fp8((int)word(vx[i][u], j / 4), false)[j & 1];
+#pragma unroll
+                        for (int x = 0; x < CT; ++x)
+                            o[x][u * C::EPL + j] = __builtin_amdgcn_mfma_f32_16x16x4f32(v, s[x][i], o[x][u * C::EPL + j], 0, 0, 0);
+                    }
+        }
+        if (odd) {
+            // What was left out, key by key: in a row that sees the key any positive weight of an infinity
+            // is that infinity, and NaN is NaN.
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                if (!there[b] || j0 + 16 * b >= end) continue;
+#pragma unroll 1
+                for (int key = 0; key < 16 && pos[b] + key <= t.last; ++key) {
+                    const char* vr = vpool + (row[b] + key) * (D * C::ES);
+                    const int j = pos[b] + key;
+#pragma unroll
+                    for (int y = 0; y < C::VL; ++y)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float e = odd_element<T, FP8>(vr, 16 * C::EPL * (y / C::EPL) + C::EPL * (4 * g + i) + y % C::EPL);
+#pragma unroll
+                            for (int x = 0; x < CT; ++x)
+                                if (j <= at[x] && (!window || j > at[x] - window || j < sinks)) o[x][y][i] += e;
+                        }
+                }
+            }
+        }
+        if (next < end) load_v(nrow);
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            row[b] = nrow[b];
+            there[b] = nthere[b];
+            pos[b] = npos[b];
+        }
+    }
+
+    // Join the waves, 16 rows at a time: weights relative to the largest maximum. A wave that saw nothing
+    // but NaN scores has m = -inf as one that saw no key has; its sums are NaN, and 0 x NaN hands them on.
+#pragma unroll
+    for (int x = 0; x < CT; ++x) {
+        l[x] += __shfl_xor(l[x], 16, 64);
+        l[x] += __shfl_xor(l[x], 32, 64);
+        exact[x] += __shfl_xor(exact[x], 16, 64);
+        exact[x] += __shfl_xor(exact[x], 32, 64);
+        if (g == 0) {
+            s_m[wave][16 * x + c] = m[x];
+            s_l[wave][16 * x + c] = make_float2(l[x], exact[x]);
+        }
+    }
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct) {
+        __syncthreads();
+        if (16 * ct >= have) break;
+        float mm = s_m[0][16 * ct + c];
+#pragma unroll
+        for (int x = 1; x < kWaves; ++x) mm = fmaxf(mm, s_m[x][16 * ct + c]);
+        const float f = m[ct] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m[ct] - mm);
+#pragma unroll
+        for (int u = 0; u < C::U; ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < C::EPL; ++j)
+                    s_o[wave][c][16 * C::EPL * u + C::EPL * (4 * g + i) + j] = o[ct][u * C::EPL + j][i] * f;
+        __syncthreads();
+        const int rows = have - 16 * ct < 16 ? have - 16 * ct : 16;
+        for (int x = threadIdx.x; x < rows * (D / 4); x += 64 * kWaves) {
+            const int y = x / (D / 4), el = x % (D / 4) * 4, tr = 16 * ct + y;
+            float top = s_m[0][tr];
+#pragma unroll
+            for (int w = 1; w < kWaves; ++w) top = fmaxf(top, s_m[w][tr]);
+            f32x4_t sum = {0.f, 0.f, 0.f, 0.f};
+            float ls = 0.f, le = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) sum += *reinterpret_cast<const f32x4_t*>(&s_o[w][y][el]);
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) {
+                const float v = s_m[w][tr] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(s_m[w][tr] - top);
+                ls += s_l[w][tr].x * v;
+                le += s_l[w][tr].y * v;
+            }
+            if (whole) {
+                const int r = t.row0 + tr, i = r / t.g;
+                const int64_t to = (int64_t)(t.q0 + i) * p.d.h_q + kvh * t.g + r - i * t.g;
+                sum *= ls > 0.f ? 1.f / ls : (ls == ls ? 0.f : ls);
+                T* out = static_cast<T*>(p.out) + to * D + el;
+                if constexpr (BF) *reinterpret_cast<u32x2_t*>(out) = u32x2_t{pack_bf16(sum[0], sum[1]), pack_bf16(sum[2], sum[3])};
+                else *reinterpret_cast<f32x4_t*>(out) = sum;
+                if (p.lse && el == 0) p.lse[to] = le > 0.f ? (top + __builtin_amdgcn_logf(le)) * kLn2 : (le == le ? -INFINITY : le);
+            } else {
+                const int64_t to = ((int64_t)unit * a.ranges + rg) * M + tr;
+                *reinterpret_cast<f32x4_t*>(a.part.o + to * D + el) = sum;
+                if (el == 0) a.part.ml[to] = make_float4(top, ls, le, 0.f);
+            }
+        }
+    }
+}
+
+// Joins the ranges of one row of a tile, 64 elements of it: the ranges' sums weighted by
+// exp2(m - max m). 16 lanes hold the elements, the blockDim / 16 groups of them take the ranges in
+// turn; the order of the additions depends on the sizes only.
+constexpr int kJoinGroups = 64;  // at most
+
+int join_threads(int64_t ranges)
+{
+    const int64_t t = (ranges + 3) / 4 * 16;  // about four ranges a group
+    return t < 64 ? 64 : t > 16 * kJoinGroups ? 16 * kJoinGroups : (int)((t + 63) / 64 * 64);
+}
+
+template <typename T, int D, int M>
+__global__ void __launch_bounds__(16 * kJoinGroups) extend_join_kernel(Args a)
+{
+    __shared__ f32x4_t s_o[kJoinGroups][16];
+    __shared__ float2 s_l[kJoinGroups];
+    __shared__ float s_m[kJoinGroups / 4];
+    const ExtendCall& p = a.c;
+    const uint32_t units = (uint32_t)a.slots * (uint32_t)p.c.h_kv;
+    const int groups = blockDim.x / 16;
+    const int64_t tr64 = (int64_t)block_index() / (D / 64);
+    const int64_t unit = tr64 / M;
+    const int tr = (int)(tr64 - unit * M);
+    if (unit >= units) return;  // past the grid's end
+    const int kvh = (int)(unit % p.c.h_kv);
+    Tile t;
+    if (!find_tile<M>(p, (int)(unit / p.c.h_kv), &t)) return;
+    if (t.len <= a.range || t.row0 + tr >= t.rows) return;  // written by its only range
+    const int used = (int)((t.len + a.range - 1) / a.range);
+    const float4* ml = a.part.ml + (unit * a.ranges) * M + tr;
+    const int y = threadIdx.x / 16, el = (int)(block_index() % (D / 64)) * 64 + threadIdx.x % 16 * 4;
+    const float* po = a.part.o + ((unit * a.ranges) * M + tr) * D + el;
+
+    float top = -INFINITY;
+    for (int x = threadIdx.x; x < used; x += blockDim.x) top = fmaxf(top, ml[(int64_t)x * M].x);
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, 64));
+    if (threadIdx.x % 64 == 0) s_m[threadIdx.x / 64] = top;
+    __syncthreads();
+    for (int x = 0; x < (int)blockDim.x / 64; ++x) top = fmaxf(top, s_m[x]);
+
+    f32x4_t sum = {0.f, 0.f, 0.f, 0.f};
+    float ls = 0.f, le = 0.f;
+#pragma unroll 4
+    for (int x = y; x < used; x += groups) {
+        const float4 v = ml[(int64_t)x * M];
+        const f32x4_t part = *reinterpret_cast<const f32x4_t*>(po + (int64_t)x * M * D);
+        const float f = v.x == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(v.x - top);
+        ls += v.y * f;
+        le += v.z * f;
+        sum += part * f;
+    }
+    s_o[y][threadIdx.x % 16] = sum;
+    if (threadIdx.x % 16 == 0) s_l[y] = make_float2(ls, le);
+    __syncthreads();
+    if (y != 0) return;
+    float l = 0.f, e = 0.f;
+    f32x4_t o = {0.f, 0.f, 0.f, 0.f};
+    for (int x = 0; x < groups; ++x) {
+        o += s_o[x][threadIdx.x];
+        l += s_l[x].x;
+        e += s_l[x].y;
+    }
+    o *= l > 0.f ? 1.f / l : (l == l ? 0.f : l);
+    const int r = t.row0 + tr, i = r / t.g;
+    const int64_t to = (int64_t)(t.q0 + i) * p.d.h_q + kvh * t.g + r - i * t.g;
+    T* out = static_cast<T*>(p.out) + to * D + el;
+    if constexpr (sizeof(T) == 2) *reinterpret_cast<u32x2_t*>(out) = u32x2_t{pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3])};
+    else *reinterpret_cast<f32x4_t*>(out) = o;
+    if (p.lse && el == 0) p.lse[to] = e > 0.f ? (top + __builtin_amdgcn_logf(e)) * kLn2 : (e == e ? -INFINITY : e);
+}
+
+template <typename T, bool FP8, int D, int CT>
+hipError_t launch_ct(const ExtendCall& c, const Plan& pl)
+{
+    Args a;
+    a.c = c;
+    a.range = pl.range;
+    a.ranges = (int)pl.ranges;
+    a.slots = (int)pl.slots;
+    a.page_shift = __builtin_ctz((unsigned)c.c.page_size);
+    a.part.o = static_cast<float*>(c.ws);
+    a.part.ml = reinterpret_cast<float4*>(a.part.o + pl.units * pl.ranges * 16 * CT * D);
+    hipLaunchKernelGGL((extend_kernel<T, FP8, D, CT>), grid_of(pl.units * pl.ranges), dim3(64 * kWaves), 0, c.stream, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || pl.ranges == 1) return e;
+    hipLaunchKernelGGL((extend_join_kernel<T, D, 16 * CT>), grid_of(pl.units * 16 * CT * (D / 64)),
+                       dim3(join_threads(pl.ranges)), 0, c.stream, a);
+    return hipGetLastError();
+}
+
+template <typename T, bool FP8, int D>
+hipError_t launch_t(const ExtendCall& c)
+{
+    const Plan pl = make_plan(c.c, c.d);
+    switch (pl.ct) {
+        case 1: return launch_ct<T, FP8, D, 1>(c, pl);
+        case 2: return launch_ct<T, FP8, D, 2>(c, pl);
+        default:
+            if constexpr (D < 256) return launch_ct<T, FP8, D, 4>(c, pl);
+            else return hipErrorInvalidValue;
+    }
+}
+
+template <typename T, int D>
+hipError_t launch_store(const ExtendCall& c)
+{
+    return c.c.store == GDN_FP8 ? launch_t<T, true, D>(c) : launch_t<T, false, D>(c);
+}
+
+template <typename T>
+hipError_t launch_d(const ExtendCall& c)
+{
+    switch (c.c.d) {
+        case 64: return launch_store<T, 64>(c);
+        case 128: return launch_store<T, 128>(c);
+        case 256: return launch_store<T, 256>(c);
+        default: return hipErrorInvalidValue;
+    }
+}
+
+}  // namespace
+
+size_t attn_extend_workspace(const gdn_kv_cache& c, const gdn_extend_dims& d)
+{
+    const Plan p = make_plan(c, d);
+    return p.ranges == 1 ? 0 : (size_t)(p.units * p.ranges) * 16 * p.ct * (c.d * sizeof(float) + sizeof(float4));
+}
+
+hipError_t launch_attn_extend(const ExtendCall& c)
+{
+    return c.d.dtype == GDN_BF16 ? launch_d<uint16_t>(c) : launch_d<float>(c);
+}
+
+}  // namespace gdn

@@ -47,10 +47,37 @@ struct AttnDecodeCall {
     hipStream_t stream;
 };
 
+// gdn_qk_norm_rope (no cache: h_kv heads of k to k_out) and gdn_kv_append.
+struct RopeCall {
+    gdn_norm_rope f;
+    gdn_kv_cache c;
+    int64_t total;
+    int32_t h_q, h_kv, d, dtype;
+    const void *q, *k, *v;
+    int64_t q_token, q_head, k_token, k_head, v_token, v_head;
+    void *q_out, *k_out;
+    const int32_t *start, *cu;
+    hipStream_t stream;
+};
+
+// max_len is bounded by the page table, max_q by total_q; window 0 and sinks 0 where there is no window.
+struct ExtendCall {
+    gdn_kv_cache c;
+    gdn_extend_dims d;
+    const void* q;
+    const int32_t *cu_q, *lens;
+    void* out;
+    float* lse;
+    void* ws;
+    hipStream_t stream;
+};
+
 hipError_t launch_kv_write(const KvCall& c);
 hipError_t launch_kv_read(const KvCall& c);
 hipError_t launch_attn_prefill(const AttnCall& c);
 hipError_t launch_attn_decode(const AttnDecodeCall& c);
+hipError_t launch_rope(const RopeCall& c, bool cache);
+hipError_t launch_attn_extend(const ExtendCall& c);
 
 // Query rows (positions x heads of a KV head) a prefill workgroup handles, for the grid bound.
 int attn_prefill_rows(int32_t d, int32_t dtype);
@@ -58,6 +85,8 @@ int attn_prefill_rows(int32_t d, int32_t dtype);
 size_t attn_prefill_workspace(const gdn_attn_dims& d);
 // Workspace of a decode call (0: not split), from the sizes the host knows.
 size_t attn_decode_workspace(const gdn_kv_cache* c, int32_t h_q, int64_t max_len);
+// Workspace of a checked extend call with rows (0: not split).
+size_t attn_extend_workspace(const gdn_kv_cache& c, const gdn_extend_dims& d);
 
 // A grid of at least `blocks` workgroups. A launch holds fewer than 2^32 threads in one dimension (more
 // are not refused: workgroups are missing), so long ones go on in the second; workgroups have

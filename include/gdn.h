@@ -84,7 +84,7 @@
 extern "C" {
 #endif
 
-#define GDN_ABI_VERSION 3
+#define GDN_ABI_VERSION 4
 
 typedef enum {
     GDN_OK = 0,
@@ -484,6 +484,98 @@ gdn_status gdn_attn_decode(const gdn_kv_cache* cache, int32_t h_q, int32_t dtype
                            int64_t max_len, const void* q, int64_t q_token, int64_t q_head,
                            const int32_t* lens, void* out, float* lse, void* workspace,
                            size_t workspace_bytes, void* stream);
+
+/* ======================================================================================
+ * Around the attention layers: norms and rotary positions of queries and keys, the cache
+ * written with them on the way, and attention of new tokens over the cache. A serving step of an
+ * attention layer is gdn_kv_append and gdn_attn_extend; a packed prompt without a cache
+ * gdn_qk_norm_rope and gdn_attn_prefill. The rules, limits and layouts of the section above hold.
+ * ====================================================================================== */
+
+/*
+ * What happens to a row x of q or k (the d elements of one token and head): first, where there is a
+ * weight, a norm over the whole row,
+ *     y_i = x_i / sqrt(mean(x^2) + eps) * (weight_bias + weight_i),
+ * then the rotation of its first rot elements, in pairs (a, b) of the elements p and p + rot / 2, or
+ * with interleaved != 0 of 2 p and 2 p + 1, for p = 0 .. rot / 2 - 1:
+ *     a' = rope_scale * (a cos t - b sin t),  b' = rope_scale * (b cos t + a sin t),
+ *     t = freq[p] * pos[axis[p]][token].
+ * The other elements stay as they are. A model with one position per token has axes = 1 and axis
+ * NULL; images and video have several (time, height, width, say), and axis gives each pair's, in any
+ * arrangement (values from axes on count as axes - 1). Everything is computed in fp32, the angle in
+ * 64 bits and reduced there, so that far positions lose nothing, and rounded once at the end.
+ * A NaN in a row reaches all of it through its norm; without one, its pair.
+ */
+typedef struct {
+    float eps;            /* of the norms; finite, not negative                             */
+    float weight_bias;    /* finite: 0, or 1 where weights are kept as their distance from 1 */
+    const void* q_weight; /* [d] of the rows' dtype; NULL: q is not normed                  */
+    const void* k_weight; /* [d]; NULL: k is not normed                                     */
+    int32_t rot;          /* rotated elements: a multiple of 16, 0 to d                     */
+    int32_t interleaved;  /* 0 or 1: which elements make a pair                             */
+    int32_t axes;         /* positions per token, 1 to 4 (ignored with rot 0)               */
+    float rope_scale;     /* finite; 1 unless a context extension asks for another          */
+    const float* freq;    /* [rot / 2]: angle per position, in radians                      */
+    const uint8_t* axis;  /* [rot / 2], or NULL: all pairs turn by pos[0]                   */
+    const int32_t* pos;   /* [axes][total]                                                  */
+} gdn_norm_rope;
+
+/*
+ * Queries and keys of packed tokens, normed and rotated: q [total][h_q][d], k [total][h_kv][d]
+ * (strided, dtype bf16 or fp32) to q_out, k_out (dense, of dtype). One of h_q and h_kv may be 0;
+ * its pointers and strides are then ignored. One launch.
+ */
+gdn_status gdn_qk_norm_rope(const gdn_norm_rope* f, int64_t total, int32_t h_q, int32_t h_kv, int32_t d,
+                            int32_t dtype, const void* q, int64_t q_token, int64_t q_head, const void* k,
+                            int64_t k_token, int64_t k_head, void* q_out, void* k_out, void* stream);
+
+/*
+ * gdn_kv_write with keys normed and rotated on the way, and with h_q > 0 the queries of the same
+ * tokens too (q [total][h_q][d], strided, to q_out, dense): what an attention layer does between its
+ * projections and its attention, in one launch. With pos NULL (axes 1) a token turns by the place
+ * that it takes in its sequence, start[s] + i. An fp8 store quantises the rotated key, which is not
+ * rounded before. A token whose place is not in the cache drops its key and value and still has its
+ * query written; tokens of no sequence have none of them. total * (h_q + 2 h_kv) stays below 2^31.
+ */
+gdn_status gdn_kv_append(const gdn_kv_cache* cache, const gdn_norm_rope* f, int64_t total, int32_t dtype,
+                         const void* k, int64_t k_token, int64_t k_head, const void* v, int64_t v_token,
+                         int64_t v_head, const int32_t* start, const int32_t* cu_seqlens, int32_t h_q,
+                         const void* q, int64_t q_token, int64_t q_head, void* q_out, void* stream);
+
+/*
+ * Attention of new tokens over the cache, which holds them already: the next piece of a prompt, a few
+ * drafted tokens, or one token per sequence (cu_q NULL, total_q == n, max_q 1). Row i of the len_q rows that
+ * sequence s has (cu_q[s] .. cu_q[s + 1] - 1 of q) is the token at position
+ * p = min(lens[s], max_len, max_pages * page_size) - len_q + i, and sees the positions
+ *     j <= p  with  window == 0  or  p - j < window  or  j < sinks
+ * on pages that are there: with a window only the last positions, its own among them, and the first
+ * `sinks`, which stay visible. Pages that no row sees are not read and may be given away (-1). A row
+ * that sees nothing has o = 0, lse = -inf.
+ *   q [total_q][h_q][d] (strided); out [total_q][h_q][d] of dtype; lse [total_q][h_q] fp32, or NULL
+ * max_len and max_q are the caller's bounds on lens and len_q, which the host cannot see: the work is
+ * divided by them, positions from max_len on are not read, and a sequence's rows from max_q on are
+ * not computed (and left as they are in out and lse). Softmax, rounding and NaN as for
+ * gdn_attn_prefill and gdn_attn_decode; a key that a row may not see contributes nothing to it,
+ * whatever it holds. Keys may be divided into ranges that a second kernel joins, in a fixed order;
+ * workspace then has gdn_attn_extend_workspace_bytes(cache, dims) bytes (0 when nothing is divided,
+ * and for invalid arguments).
+ */
+typedef struct {
+    int64_t total_q; /* rows of q, out and lse; total_q * h_q / h_kv below 2^31 - 2^16   */
+    int64_t max_q;   /* no sequence has more rows                                       */
+    int64_t max_len; /* no sequence is longer; it or the table's positions below 2^31 - 2^16 */
+    int64_t window;  /* positions that a row sees up to its own; 0: all                 */
+    int64_t sinks;   /* first positions that stay visible beside a window               */
+    int32_t h_q;     /* query heads, a multiple of the cache's h_kv                     */
+    int32_t dtype;   /* gdn_dtype of q and out                                          */
+    float scale;     /* finite, also times log2 e; 1 / sqrt(d) is usual                 */
+    int64_t q_token, q_head; /* strides, in elements                                    */
+} gdn_extend_dims;
+
+size_t gdn_attn_extend_workspace_bytes(const gdn_kv_cache* cache, const gdn_extend_dims* dims);
+gdn_status gdn_attn_extend(const gdn_kv_cache* cache, const gdn_extend_dims* dims, const void* q,
+                           const int32_t* cu_q, const int32_t* lens, void* out, float* lse,
+                           void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }
