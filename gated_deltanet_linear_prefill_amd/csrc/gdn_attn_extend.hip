@@ -20,134 +20,13 @@
 //
 // A key that only some rows see may hold a NaN or an infinity, and 0 x NaN is NaN: in steps with
 // masked keys such elements of V are left out of the product and added to the rows that see them.
-#include "gdn_attn_internal.hpp"
+#include "gdn_extend.hpp"
 
 namespace gdn {
 namespace {
 
 constexpr int kWaves = 4;
 constexpr int kRange = 32 * kWaves;  // ranges are multiples of this: a step of every wave
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
-
-struct Plan {
-    int ct;              // tiles of 16 rows a workgroup takes
-    int64_t slots;       // tiles of one KV head that the grid has room for
-    int64_t units;       // ... of all KV heads
-    int64_t range;       // virtual positions of a range
-    int64_t ranges;
-};
-
-// Virtual positions that a tile may have.
-int64_t longest(const gdn_kv_cache& c, const gdn_extend_dims& d, int m)
-{
-    if (d.window == 0) return d.max_len;
-    const int64_t g = d.h_q / c.h_kv;
-    const int64_t w = d.window + (m - 1) / g + 1 + 15 + (d.sinks + 15) / 16 * 16;
-    return w < d.max_len ? w : d.max_len;
-}
-
-Plan make_plan(const gdn_kv_cache& c, const gdn_extend_dims& d)
-{
-    Plan p;
-    const int64_t g = d.h_q / c.h_kv, rows = d.max_q * g;
-    p.ct = rows <= 16 ? 1 : rows <= 32 || c.d == 256 ? 2 : 4;
-    const int m = 16 * p.ct;
-    p.slots = d.max_q == 1 ? c.n * ((g + m - 1) / m) : d.total_q * g / m + c.n;
-    p.units = p.slots * c.h_kv;
-    const int64_t tiles = (d.total_q * g + m - 1) / m;
-    const int64_t real = (tiles > c.n ? tiles : c.n) * c.h_kv;
-    const int64_t len = longest(c, d, m), steps = len > 0 ? (len + kRange - 1) / kRange : 1;
-    const int64_t most = real * steps;
-    int64_t want = most / 8 < 4096 ? most / 8 : 4096;
-    if (want < 256 || c.n == 1) want = 256;
-    int64_t ranges = (want + real - 1) / real;
-    if (ranges > (steps + 1) / 2) ranges = (steps + 1) / 2;
-    if (steps <= 4) ranges = 1;
-    if (ranges > 0x7fffffff / p.units) ranges = 0x7fffffff / p.units;  // the grid
-    if (ranges < 1) ranges = 1;
-    const int64_t per = (steps + ranges - 1) / ranges;
-    p.range = per * kRange;
-    p.ranges = (steps + per - 1) / per;
-    return p;
-}
-
-// Workspace of one call: O sums [unit][range][M][D] fp32, then (m, l, exact l, -) of each row.
-struct Partials {
-    float* o;
-    float4* ml;
-};
-
-struct Args {
-    ExtendCall c;
-    int64_t range;
-    int ranges, slots, page_shift;
-    Partials part;
-};
-
-// A tile: rows row0 .. of the `rows` that its sequence has, and the positions that they see.
-struct Tile {
-    int seq, q0, rows, row0, g;
-    int first, last;       // positions of its first and last row
-    int shift;             // position of row 0 of the sequence
-    int sink, skip, len;   // virtual positions: [0, sink) as they are, then [sink, len) + skip
-    __device__ __forceinline__ int pos(int v) const { return v < sink ? v : v + skip; }
-};
-
-__device__ __forceinline__ int clamp_to(int x, int hi)
-{
-    return x < 0 ? 0 : (x > hi ? hi : x);
-}
-
-template <int M>
-__device__ __forceinline__ bool find_tile(const ExtendCall& p, int slot, Tile* t)
-{
-    const int g = p.d.h_q / p.c.h_kv, n = (int)p.c.n, total = (int)p.d.total_q;
-    int s = 0, qa, qb, local;
-    if (p.d.max_q == 1) {  // a sequence has the tiles of one token, or none
-        const int tiles = (g + M - 1) / M;
-        s = slot / tiles;
-        if (s >= n) return false;
-        qa = p.cu_q ? clamp_to(p.cu_q[s], total) : s;
-        qb = p.cu_q ? clamp_to(p.cu_q[s + 1], total) : s + 1;
-        local = tiles - 1 - (slot - s * tiles);
-    } else {
-        const int lane = threadIdx.x & 63;
-        auto base = [&](int x) { return (int)((int64_t)clamp_to(p.cu_q[x], total) * g / M) + x; };
-        for (int span = n; span > 1;) {  // the sequence is in [s, s + span)
-            const int step = (span + 63) / 64, at = s + lane * step;
-            const bool before = lane * step < span && (lane == 0 || base(at) <= slot);
-            const int x = 63 - __builtin_clzll(__ballot(before) | 1);  // the last lane not past the slot
-            s += x * step;
-            span = span - x * step < step ? span - x * step : step;
-        }
-        s = __builtin_amdgcn_readfirstlane(s);
-        qa = clamp_to(p.cu_q[s], total);
-        qb = clamp_to(p.cu_q[s + 1], total);
-        local = slot - ((int)((int64_t)qa * g / M) + s);
-    }
-    const int len_q = qb - qa;
-    if (len_q <= 0 || local < 0) return false;
-    t->seq = s;
-    t->q0 = qa;
-    t->g = g;
-    t->rows = (len_q < p.d.max_q ? len_q : (int)p.d.max_q) * g;
-    const int tiles = (t->rows + M - 1) / M;
-    if (local >= tiles) return false;
-    t->row0 = (tiles - 1 - local) * M;  // the last, which see most, first
-    int len = p.lens[s];
-    len = len < p.d.max_len ? len : (int)p.d.max_len;
-    len = len < 0 ? 0 : len;
-    t->shift = len - len_q;
-    t->first = t->shift + t->row0 / g;
-    t->last = t->shift + ((t->row0 + M < t->rows ? t->row0 + M : t->rows) - 1) / g;
-    const int w = (int)p.d.window, lo = w && t->first >= w ? (t->first - w + 1) & ~15 : 0;
-    const int sinks = (int)((p.d.sinks + 15) & ~15);
-    t->sink = sinks < lo ? sinks : lo;
-    t->skip = lo - t->sink;
-    t->len = t->last < 0 ? 0 : t->last + 1 - t->skip;
-    return true;
-}
 
 template <typename T, bool FP8, int D, int CT>
 struct Cfg {
@@ -220,7 +99,7 @@ __device__ __forceinline__ float odd_element(const char* row, int e)
 }
 
 template <typename T, bool FP8, int D, int CT>
-__global__ void __launch_bounds__(64 * kWaves, (Cfg<T, FP8, D, CT>::PER_SIMD)) extend_kernel(Args a)
+__global__ void __launch_bounds__(64 * kWaves, (Cfg<T, FP8, D, CT>::PER_SIMD)) extend_kernel(ExtendArgs a)
 {
     using C = Cfg<T, FP8, D, CT>;
     using VP = typename Piece<C::EPL * C::ES>::type;
@@ -241,9 +120,9 @@ __global__ void __launch_bounds__(64 * kWaves, (Cfg<T, FP8, D, CT>::PER_SIMD)) e
     const uint32_t unit = block_index() % units;
     const int rg = (int)(block_index() / units);
     if (rg >= a.ranges) return;  // past the grid's end
-    const int kvh = (int)(unit % (uint32_t)p.c.h_kv);
-    Tile t;
-    if (!find_tile<M>(p, (int)(unit / (uint32_t)p.c.h_kv), &t)) return;
+    Span t;
+    if (!find_span<M>(a, unit, &t)) return;
+    const int kvh = t.head;
     const int64_t begin64 = rg * a.range;
     if (rg > 0 && begin64 >= t.len) return;  // the join does not read this range
     const bool whole = t.len <= a.range;     // nothing to join
@@ -259,18 +138,22 @@ __global__ void __launch_bounds__(64 * kWaves, (Cfg<T, FP8, D, CT>::PER_SIMD)) e
             static_cast<const T*>(p.q) + (int64_t)(t.q0 + i) * p.d.q_token +
             (int64_t)(kvh * t.g + r - i * t.g) * p.d.q_head + x % CH * (16 / (int)sizeof(T)));
     }
-    int at[CT];  // this lane's rows' positions
+    int upto[CT];  // virtual positions that this lane's rows see end here
 #pragma unroll
-    for (int x = 0; x < CT; ++x) at[x] = t.shift + (t.row0 + (16 * x + c < have ? 16 * x + c : have - 1)) / t.g;
+    for (int x = 0; x < CT; ++x)
+        upto[x] = max(t.shift + (t.row0 + (16 * x + c < have ? 16 * x + c : have - 1)) / t.g + 1 - t.skip, 0);
     int qoff = c * C::QSTRIDE + g * C::EPK * (int)sizeof(T);
     auto q_at = [&](int ct, int i, int x) __attribute__((always_inline)) {
         return *reinterpret_cast<const u32x4_t*>(s_q + qoff + ct * 16 * C::QSTRIDE + i * 4 * C::EPK * (int)sizeof(T) + x * 16);
     };
     __syncthreads();
 
-    const int window = (int)p.d.window, sinks = (int)p.d.sinks;
-    // every row sees the positions up to `first` that are in the last row's window or among the sinks
-    const int from = window && t.last >= window ? t.last - window + 1 : 0;
+    const int sinks = (int)p.d.sinks, window = (int)p.d.window;
+    auto sees = [&](int v, int x) __attribute__((always_inline)) {
+        return v < upto[x] && (!window || v >= upto[x] - window || v < sinks);
+    };
+    // every row sees the positions before `all` that are in the last row's window, from `from` on, or sinks
+    const int all = t.first + 1 - t.skip, from = window ? t.len - window : 0;
     f32x4_t o[CT][C::VL];
     float m[CT], l[CT], exact[CT];
 #pragma unroll
@@ -289,15 +172,13 @@ __global__ void __launch_bounds__(64 * kWaves, (Cfg<T, FP8, D, CT>::PER_SIMD)) e
     VP vx[4 * NB][C::U];
     uint32_t sk[NB], sv[NB];
 
-    // Row of the pools where block b of the step at virtual position j0 begins, and its position; absent
-    // pages read page 0 (and are masked), blocks past the range's end the last before it.
-    auto block_row = [&](int j0, int b, bool* there, int* pos) {
-        const int v = j0 + 16 * b;
-        *pos = t.pos(v);
-        const int from = v < end ? *pos : t.pos(end - 1);
-        const int64_t page = table[from >> a.page_shift];
+    // Row of the pools where block b of the step at virtual position j0 begins; absent pages read page 0
+    // (and are masked), blocks past the range's end the last before it.
+    auto block_row = [&](int j0, int b, bool* there) {
+        const int v = j0 + 16 * b, pos = t.pos(v < end ? v : (end - 1) & ~15);
+        const int64_t page = table[pos >> a.page_shift];
         *there = page >= 0 && page < p.c.num_pages;
-        return (((*there ? page : 0) * p.c.h_kv + kvh) << a.page_shift) + ((v < end ? *pos : from & ~15) & (p.c.page_size - 1));
+        return (((*there ? page : 0) * p.c.h_kv + kvh) << a.page_shift) + (pos & (p.c.page_size - 1));
     };
     auto load_k = [&](const int64_t* row) {
 #pragma unroll
@@ -324,11 +205,10 @@ __global__ void __launch_bounds__(64 * kWaves, (Cfg<T, FP8, D, CT>::PER_SIMD)) e
 
     int64_t row[NB];
     bool there[NB];
-    int pos[NB];
     const int first = begin + wave * C::STEP;
     if (first < end) {
 #pragma unroll
-        for (int b = 0; b < NB; ++b) row[b] = block_row(first, b, &there[b], &pos[b]);
+        for (int b = 0; b < NB; ++b) row[b] = block_row(first, b, &there[b]);
         load_k(row);
         load_v(row);
     }
@@ -337,10 +217,9 @@ __global__ void __launch_bounds__(64 * kWaves, (Cfg<T, FP8, D, CT>::PER_SIMD)) e
         const int next = j0 + kWaves * C::STEP;
         int64_t nrow[NB] = {};
         bool nthere[NB] = {};
-        int npos[NB] = {};
         if (next < end)
 #pragma unroll
-            for (int b = 0; b < NB; ++b) nrow[b] = block_row(next, b, &nthere[b], &npos[b]);
+            for (int b = 0; b < NB; ++b) nrow[b] = block_row(next, b, &nthere[b]);
 
         // scores
         asm volatile("" : "+v"(qoff));  // read again in every step, not kept
@@ -405,7 +284,7 @@ __global__ void __launch_bounds__(64 * kWaves, (Cfg<T, FP8, D, CT>::PER_SIMD)) e
         bool masked = false;
 #pragma unroll
         for (int b = 0; b < NB; ++b)
-            masked |= !there[b] || j0 + 16 * b >= end || pos[b] + 15 > t.first || (pos[b] < from && pos[b] + 15 >= sinks);
+            masked |= !there[b] || j0 + 16 * b + 16 > all || (j0 + 16 * b < from && j0 + 16 * b + 16 > sinks);
         bool odd = false;
         uint32_t seen[CT];  // bits of this lane's keys
         if (masked) {
@@ -414,8 +293,8 @@ __global__ void __launch_bounds__(64 * kWaves, (Cfg<T, FP8, D, CT>::PER_SIMD)) e
             uint32_t found = 0;
 #pragma unroll
             for (int i = 0; i < 4 * NB; ++i) {
-                const int b = i / 4, j = pos[b] + 4 * g + i % 4;
-                const bool exists = there[b] && j0 + 16 * b < end && j <= t.last;
+                const int b = i / 4, v = j0 + 16 * b + 4 * g + i % 4;
+                const bool exists = there[b] && v < end;
                 if (!exists) {  // what lies there is anything: not into the product
 #pragma unroll
                     for (int u = 0; u < C::U; ++u) vx[i][u] = VP{};
@@ -423,9 +302,9 @@ __global__ void __launch_bounds__(64 * kWaves, (Cfg<T, FP8, D, CT>::PER_SIMD)) e
                 }
 #pragma unroll
                 for (int x = 0; x < CT; ++x) {
-                    const bool sees = exists && j <= at[x] && (!window || j > at[x] - window || j < sinks);
-                    s[x][i] = sees ? s[x][i] : -INFINITY;
-                    seen[x] |= (uint32_t)sees << i;
+                    const bool in = exists && sees(v, x);
+                    s[x][i] = in ? s[x][i] : -INFINITY;
+                    seen[x] |= (uint32_t)in << i;
                 }
 #pragma unroll
                 for (int u = 0; u < C::U; ++u)
@@ -541,11 +420,11 @@ __global__ void __launch_bounds__(64 * kWaves, (Cfg<T, FP8, D, CT>::PER_SIMD)) e
             // is that infinity, and NaN is NaN.
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
-                if (!there[b] || j0 + 16 * b >= end) continue;
+                if (!there[b]) continue;
 #pragma unroll 1
-                for (int key = 0; key < 16 && pos[b] + key <= t.last; ++key) {
+                for (int key = 0; key < 16 && j0 + 16 * b + key < end; ++key) {
                     const char* vr = vpool + (row[b] + key) * (D * C::ES);
-                    const int j = pos[b] + key;
+                    const int v = j0 + 16 * b + key;
 #pragma unroll
                     for (int y = 0; y < C::VL; ++y)
 #pragma unroll
@@ -553,7 +432,7 @@ __global__ void __launch_bounds__(64 * kWaves, (Cfg<T, FP8, D, CT>::PER_SIMD)) e
                             const float e = odd_element<T, FP8>(vr, 16 * C::EPL * (y / C::EPL) + C::EPL * (4 * g + i) + y % C::EPL);
 #pragma unroll
                             for (int x = 0; x < CT; ++x)
-                                if (j <= at[x] && (!window || j > at[x] - window || j < sinks)) o[x][y][i] += e;
+                                if (sees(v, x)) o[x][y][i] += e;
                         }
                 }
             }
@@ -563,7 +442,6 @@ __global__ void __launch_bounds__(64 * kWaves, (Cfg<T, FP8, D, CT>::PER_SIMD)) e
         for (int b = 0; b < NB; ++b) {
             row[b] = nrow[b];
             there[b] = nthere[b];
-            pos[b] = npos[b];
         }
     }
 
@@ -622,8 +500,8 @@ __global__ void __launch_bounds__(64 * kWaves, (Cfg<T, FP8, D, CT>::PER_SIMD)) e
                 if (p.lse && el == 0) p.lse[to] = le > 0.f ? (top + __builtin_amdgcn_logf(le)) * kLn2 : (le == le ? -INFINITY : le);
             } else {
                 const int64_t to = ((int64_t)unit * a.ranges + rg) * M + tr;
-                *reinterpret_cast<f32x4_t*>(a.part.o + to * D + el) = sum;
-                if (el == 0) a.part.ml[to] = make_float4(top, ls, le, 0.f);
+                *reinterpret_cast<f32x4_t*>(a.part_o + to * D + el) = sum;
+                if (el == 0) a.part_ml[to] = make_float4(top, ls, le, 0.f);
             }
         }
     }
@@ -641,7 +519,7 @@ int join_threads(int64_t ranges)
 }
 
 template <typename T, int D, int M>
-__global__ void __launch_bounds__(16 * kJoinGroups) extend_join_kernel(Args a)
+__global__ void __launch_bounds__(16 * kJoinGroups) extend_join_kernel(ExtendArgs a)
 {
     __shared__ f32x4_t s_o[kJoinGroups][16];
     __shared__ float2 s_l[kJoinGroups];
@@ -653,14 +531,14 @@ __global__ void __launch_bounds__(16 * kJoinGroups) extend_join_kernel(Args a)
     const int64_t unit = tr64 / M;
     const int tr = (int)(tr64 - unit * M);
     if (unit >= units) return;  // past the grid's end
-    const int kvh = (int)(unit % p.c.h_kv);
-    Tile t;
-    if (!find_tile<M>(p, (int)(unit / p.c.h_kv), &t)) return;
+    Span t;
+    if (!find_span<M>(a, (uint32_t)unit, &t)) return;
+    const int kvh = t.head;
     if (t.len <= a.range || t.row0 + tr >= t.rows) return;  // written by its only range
     const int used = (int)((t.len + a.range - 1) / a.range);
-    const float4* ml = a.part.ml + (unit * a.ranges) * M + tr;
+    const float4* ml = a.part_ml + (unit * a.ranges) * M + tr;
     const int y = threadIdx.x / 16, el = (int)(block_index() % (D / 64)) * 64 + threadIdx.x % 16 * 4;
-    const float* po = a.part.o + ((unit * a.ranges) * M + tr) * D + el;
+    const float* po = a.part_o + ((unit * a.ranges) * M + tr) * D + el;
 
     float top = -INFINITY;
     for (int x = threadIdx.x; x < used; x += blockDim.x) top = fmaxf(top, ml[(int64_t)x * M].x);
@@ -701,66 +579,151 @@ __global__ void __launch_bounds__(16 * kJoinGroups) extend_join_kernel(Args a)
     if (p.lse && el == 0) p.lse[to] = e > 0.f ? (top + __builtin_amdgcn_logf(e)) * kLn2 : (e == e ? -INFINITY : e);
 }
 
-template <typename T, bool FP8, int D, int CT>
-hipError_t launch_ct(const ExtendCall& c, const Plan& pl)
+template <typename T, int D, int M>
+hipError_t launch_join(const ExtendArgs& a)
 {
-    Args a;
-    a.c = c;
-    a.range = pl.range;
-    a.ranges = (int)pl.ranges;
-    a.slots = (int)pl.slots;
-    a.page_shift = __builtin_ctz((unsigned)c.c.page_size);
-    a.part.o = static_cast<float*>(c.ws);
-    a.part.ml = reinterpret_cast<float4*>(a.part.o + pl.units * pl.ranges * 16 * CT * D);
-    hipLaunchKernelGGL((extend_kernel<T, FP8, D, CT>), grid_of(pl.units * pl.ranges), dim3(64 * kWaves), 0, c.stream, a);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess || pl.ranges == 1) return e;
-    hipLaunchKernelGGL((extend_join_kernel<T, D, 16 * CT>), grid_of(pl.units * 16 * CT * (D / 64)),
-                       dim3(join_threads(pl.ranges)), 0, c.stream, a);
+    const int64_t units = (int64_t)a.slots * a.c.c.h_kv;
+    hipLaunchKernelGGL((extend_join_kernel<T, D, M>), grid_of(units * M * (D / 64)), dim3(join_threads(a.ranges)), 0,
+                       a.c.stream, a);
     return hipGetLastError();
 }
 
-template <typename T, bool FP8, int D>
-hipError_t launch_t(const ExtendCall& c)
+template <typename T, int D>
+hipError_t launch_join_m(const ExtendArgs& a, int m)
 {
-    const Plan pl = make_plan(c.c, c.d);
-    switch (pl.ct) {
-        case 1: return launch_ct<T, FP8, D, 1>(c, pl);
-        case 2: return launch_ct<T, FP8, D, 2>(c, pl);
+    switch (m) {
+        case 16: return launch_join<T, D, 16>(a);
+        case 32: return launch_join<T, D, 32>(a);
+        case 64: return launch_join<T, D, 64>(a);
+        case 128: return launch_join<T, D, 128>(a);
+        case 256: return launch_join<T, D, 256>(a);
+        default: return hipErrorInvalidValue;
+    }
+}
+
+template <typename T>
+hipError_t launch_join_d(const ExtendArgs& a, int m)
+{
+    switch (a.c.c.d) {
+        case 64: return launch_join_m<T, 64>(a, m);
+        case 128: return launch_join_m<T, 128>(a, m);
+        case 256: return launch_join_m<T, 256>(a, m);
+        default: return hipErrorInvalidValue;
+    }
+}
+
+template <typename T, bool FP8, int D, int CT>
+hipError_t launch_ct(const ExtendCall& c, const ExtendPlan& pl, void* ws)
+{
+    const ExtendArgs a = extend_args(c, pl, ws);
+    hipLaunchKernelGGL((extend_kernel<T, FP8, D, CT>), grid_of(pl.units * pl.ranges), dim3(64 * kWaves), 0, c.stream, a);
+    const hipError_t e = hipGetLastError();
+    return e != hipSuccess || pl.ranges == 1 ? e : launch_extend_join(a, pl.m);
+}
+
+template <typename T, bool FP8, int D>
+hipError_t launch_t(const ExtendCall& c, const ExtendPlan& pl, void* ws)
+{
+    switch (pl.m) {
+        case 16: return launch_ct<T, FP8, D, 1>(c, pl, ws);
+        case 32: return launch_ct<T, FP8, D, 2>(c, pl, ws);
         default:
-            if constexpr (D < 256) return launch_ct<T, FP8, D, 4>(c, pl);
+            if constexpr (D < 256) return launch_ct<T, FP8, D, 4>(c, pl, ws);
             else return hipErrorInvalidValue;
     }
 }
 
 template <typename T, int D>
-hipError_t launch_store(const ExtendCall& c)
+hipError_t launch_store(const ExtendCall& c, const ExtendPlan& pl, void* ws)
 {
-    return c.c.store == GDN_FP8 ? launch_t<T, true, D>(c) : launch_t<T, false, D>(c);
+    return c.c.store == GDN_FP8 ? launch_t<T, true, D>(c, pl, ws) : launch_t<T, false, D>(c, pl, ws);
 }
 
 template <typename T>
-hipError_t launch_d(const ExtendCall& c)
+hipError_t launch_d(const ExtendCall& c, const ExtendPlan& pl, void* ws)
 {
     switch (c.c.d) {
-        case 64: return launch_store<T, 64>(c);
-        case 128: return launch_store<T, 128>(c);
-        case 256: return launch_store<T, 256>(c);
+        case 64: return launch_store<T, 64>(c, pl, ws);
+        case 128: return launch_store<T, 128>(c, pl, ws);
+        case 256: return launch_store<T, 256>(c, pl, ws);
         default: return hipErrorInvalidValue;
     }
 }
 
+// Rows of a KV head up to which a sequence is taken by the kernel of this file; longer ones by the tiles of
+// gdn_attn_extend_tile.hip.
+constexpr int kStreamRows = 64;
+
+// How the sequences of up to `to` rows are taken.
+ExtendPlan stream_plan(const gdn_kv_cache& c, const gdn_extend_dims& d, int64_t to)
+{
+    ExtendPlan p;
+    const int64_t g = d.h_q / c.h_kv, most = d.max_q * g, rows = most < to ? most : to;
+    p.m = rows <= 16 ? 16 : rows <= 32 || c.d == 256 ? 32 : 64;
+    const int64_t packed = d.total_q * g / p.m + c.n, each = (rows + p.m - 1) / p.m;
+    p.per_seq = each <= packed / c.n ? (int)each : 0;
+    p.slots = p.per_seq ? c.n * each : packed;
+    p.units = p.slots * c.h_kv;
+    p.rows_from = 0;
+    p.rows_to = (int)rows;
+    const int64_t tiles = (d.total_q * g + p.m - 1) / p.m;
+    const int64_t likely = tiles < p.slots ? tiles : p.slots, real = (likely > c.n ? likely : c.n) * c.h_kv;
+    const int64_t len = extend_longest(c, d, p.m), steps = len > 0 ? (len + kRange - 1) / kRange : 1;
+    const int64_t all = real * steps;
+    int64_t want = all / 8 < 4096 ? all / 8 : 4096;
+    if (want < 256 || c.n == 1) want = 256;
+    int64_t ranges = (want + real - 1) / real;
+    if (ranges > (steps + 1) / 2) ranges = (steps + 1) / 2;
+    if (steps <= 4) ranges = 1;
+    if (ranges > 0x7fffffff / p.units) ranges = 0x7fffffff / p.units;  // the grid
+    if (ranges < 1) ranges = 1;
+    const int64_t per = (steps + ranges - 1) / ranges;
+    p.range = per * kRange;
+    p.ranges = (steps + per - 1) / per;
+    return p;
+}
+
+struct Plans {
+    ExtendPlan stream, tiles;
+    size_t stream_bytes;  // the tiles' workspace follows
+};
+
+Plans make_plans(const gdn_kv_cache& c, const gdn_extend_dims& d)
+{
+    const int64_t most = d.max_q * (d.h_q / c.h_kv);
+    const bool only_stream = most <= kStreamRows || c.store == GDN_FP8;
+    Plans p;
+    p.stream.m = p.tiles.m = 0;
+    if (only_stream || c.n > 1) p.stream = stream_plan(c, d, only_stream ? most : kStreamRows);
+    if (!only_stream) {
+        p.tiles = extend_tile_plan(c, d);
+        p.tiles.rows_from = c.n > 1 ? kStreamRows + 1 : 0;
+        p.tiles.rows_to = 0x7fffffff;
+    }
+    p.stream_bytes = p.stream.workspace(c);
+    return p;
+}
+
 }  // namespace
+
+hipError_t launch_extend_join(const ExtendArgs& a, int m)
+{
+    return a.c.d.dtype == GDN_BF16 ? launch_join_d<uint16_t>(a, m) : launch_join_d<float>(a, m);
+}
 
 size_t attn_extend_workspace(const gdn_kv_cache& c, const gdn_extend_dims& d)
 {
-    const Plan p = make_plan(c, d);
-    return p.ranges == 1 ? 0 : (size_t)(p.units * p.ranges) * 16 * p.ct * (c.d * sizeof(float) + sizeof(float4));
+    const Plans p = make_plans(c, d);
+    return p.stream_bytes + p.tiles.workspace(c);
 }
 
 hipError_t launch_attn_extend(const ExtendCall& c)
 {
-    return c.d.dtype == GDN_BF16 ? launch_d<uint16_t>(c) : launch_d<float>(c);
+    const Plans p = make_plans(c.c, c.d);
+    hipError_t e = hipSuccess;
+    if (p.stream.m) e = c.d.dtype == GDN_BF16 ? launch_d<uint16_t>(c, p.stream, c.ws) : launch_d<float>(c, p.stream, c.ws);
+    if (e == hipSuccess && p.tiles.m) e = launch_extend_tiles(c, p.tiles, static_cast<char*>(c.ws) + p.stream_bytes);
+    return e;
 }
 
 }  // namespace gdn

@@ -1,0 +1,305 @@
+// gdn_attn_extend_tile.hip -- attention of new tokens over the paged cache: sequences with many rows.
+//
+// The matrix form, the padded LDS groups and the step are those of gdn_attn_prefill.hip
+// (gdn_attn_tile.hpp); what differs is where keys come from and which of them a row sees. A staged
+// group is 1 KiB of consecutive keys and never crosses a page (pages are 16 keys or more, virtual
+// positions skip whole blocks of 16): each wave holds a unit's page ids, one 16-position block a
+// lane, loaded a unit ahead, and takes a group's from there into the scalar unit, where its address
+// and how many of its bytes exist are formed; the rest of a group reads as zeros.
+//
+// Ranges. A tile's keys are divided into ranges of a fixed length where the tiles alone would not fill
+// the chip, and joined by the second kernel of gdn_attn_extend.hip.
+#include "gdn_extend.hpp"
+
+namespace gdn {
+namespace {
+
+// 128 rows, two workgroups a CU: one starts and ends while the other computes.
+using Twin = Shape<4, 1, 1, 2>;
+// 128 rows; half the waves take the first of two steps and half the second, and are joined at the end:
+// half the sums that ranges write.
+using Split = Shape<8, 2, 2, 2>;
+// 256 rows share every staged key: the least traffic.
+using Wide = Shape<8, 2, 1, 2>;
+// fp32 with d = 256, where a wave's O and Q take all of 256 registers.
+using Lone = Shape<4, 1, 1, 1>;
+
+template <typename T, int D, bool LSE, typename S>
+__global__ void __launch_bounds__(64 * S::WAVES, S::PER_SIMD) extend_tile_kernel(ExtendArgs a)
+{
+    using C = Tile<T, D>;
+    constexpr int N = C::N, UNIT = S::STEPS * N, M = S::ROWS, ND = D / 32, SPLIT = S::SPLIT, ES = C::ES;
+    constexpr int BLOCKS = UNIT / 16;  // 16-position blocks of a unit
+    static_assert(BLOCKS <= 64, "a lane each");
+    // separate arrays: the compiler then knows that reading one need not wait for the loads that
+    // are filling another
+    __shared__ __align__(16) char s_k0[S::STEPS * C::GROUPS * C::KG], s_k1[S::STEPS * C::GROUPS * C::KG];
+    __shared__ __align__(16) char s_v0[S::STEPS * C::GROUPS * C::VG], s_v1[S::STEPS * C::GROUPS * C::VG];
+    const ExtendCall& p = a.c;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int half = lane >> 5;
+    const int rw = wave % (S::WAVES / SPLIT), turn = wave / (S::WAVES / SPLIT);  // 32 rows, steps
+    const uint32_t units = (uint32_t)a.slots * (uint32_t)p.c.h_kv;
+    const uint32_t unit = block_index() % units;
+    const int rg = (int)(block_index() / units);
+    if (rg >= a.ranges) return;  // past the grid's end
+    Span w;
+    if (!find_span<M>(a, unit, &w)) return;
+    const int64_t begin64 = rg * a.range;
+    if (rg > 0 && begin64 >= w.len) return;  // the join does not read this range
+    const bool whole = w.len <= a.range;     // nothing to join
+    // from here on a key's number is its virtual position's distance from `begin`
+    const int begin = (int)begin64, valid = w.len - begin;
+    const int keys = valid < a.range ? valid : (int)a.range;
+
+    // K: row lane & 31 of a product is place (lane & 31) / GROUPS of group (lane & 31) % GROUPS. V,
+    // bf16: the reads of 16 lanes cover groups 4 half + 0..3, 16 elements of each, the next 16
+    // lanes the next 16; fp32: a half reads 32 elements of one group, 4 half on
+    const int klane = lane % C::GROUPS * C::KG + lane % 32 / C::GROUPS * C::ROWB + half * 16;
+    const int vlane = ES == 2 ? (4 * half + ((lane >> 2) & 3)) * C::VG + ((lane >> 4) & 1) * 32 + (lane & 3) * 8
+                              : 4 * half * C::VG + lane % 32 * 4;
+
+    // Page ids of the unit from key v0 on, a block a lane; -1: not there. Blocks past the end are as its last.
+    const int32_t* table = p.c.page_table + w.seq * p.c.max_pages;
+    auto pages_of = [&](int v0) __attribute__((always_inline)) {
+        const int v = begin + v0 + 16 * (lane < BLOCKS ? lane : BLOCKS - 1);
+        const int id = table[w.pos(v < w.len ? v : w.len - 1) >> a.page_shift];
+        return id >= 0 && id < p.c.num_pages ? id : -1;
+    };
+    // Stages the unit from key v0 on, whose pages are `ids`. Returns its blocks that are not there, a bit each.
+    const char* kpool = static_cast<const char*>(p.c.k);
+    const char* vpool = static_cast<const char*>(p.c.v);
+    auto fetch = [&](int v0, int ids, char* sk, char* sv) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < S::STEPS * C::GROUPS / S::WAVES; ++i) {
+            const int x = i * S::WAVES + wave, v = v0 + x * C::ROWS;
+            const int id = __builtin_amdgcn_readlane(ids, x * C::ROWS / 16);
+            const int left = id < 0 ? 0 : valid - v;
+            const int64_t row = (((int64_t)(id < 0 ? 0 : id) * p.c.h_kv + w.head) << a.page_shift) +
+                                (w.pos(begin + v) & (p.c.page_size - 1));
+            const int bytes = left >= C::ROWS ? 1024 : left <= 0 ? 0 : left * C::ROWB;
+            load_to_lds(make_rsrc(kpool + row * C::ROWB, bytes), sk + x * C::KG, lane * 16);
+            load_to_lds(make_rsrc(vpool + row * C::ROWB, bytes), sv + x * C::VG, lane * 16);
+        }
+        return (uint32_t)__ballot(lane < BLOCKS && ids < 0);
+    };
+    int ids = 0;
+    uint32_t gone0 = 0, gone1 = 0;
+    if (keys > 0) {
+        ids = pages_of(0);
+        gone0 = fetch(0, ids, s_k0, s_v0);
+        if (UNIT < keys) ids = pages_of(UNIT);
+    }
+
+    // What rows see: keys below upto that are at or past from, or sinks. Of the wave's first row, its last,
+    // and this lane's.
+    const int window = (int)p.d.window, sinks = (int)p.d.sinks - begin;
+    auto end_of = [&](int row) {
+        const int pos = w.shift + (int)((uint32_t)(row < w.rows ? row : w.rows - 1) / (uint32_t)w.g);
+        return pos < w.skip ? 0 : pos + 1 - w.skip;
+    };
+    auto from_of = [&](int end) { return (window && end > window ? end - window : 0) - begin; };
+    const int wfirst = w.row0 + 32 * rw, wlast = end_of(wfirst + 31);
+    const int wall = end_of(wfirst) - begin, wkeys = (wfirst < w.rows ? wlast : 0) - begin, wfrom = from_of(wlast);
+    const int r = wfirst + (lane & 31), rc = r < w.rows ? r : w.rows - 1, pos = (int)((uint32_t)rc / (uint32_t)w.g);
+    const int upto = end_of(r) - begin, from = from_of(end_of(r));
+
+    const char* qp = static_cast<const char*>(p.q) +
+                     ES * ((w.q0 + pos) * p.d.q_token + (w.head * w.g + (rc - pos * w.g)) * p.d.q_head) + 16 * half;
+    // A negative scale becomes a positive one of the negated query, zero the smallest positive number: see
+    // gdn_attn_prefill.hip.
+    const uint32_t flip = p.d.scale < 0.f ? (ES == 2 ? 0x80008000u : 0x80000000u) : 0u;
+    const float c = fmaxf(fabsf(p.d.scale) * kLog2e, 0x1p-149f);
+    u32x4_t q[D / (2 * C::PER)];  // piece kk: elements 2 PER kk + PER half ..
+#pragma unroll
+    for (int kk = 0; kk < D / (2 * C::PER); ++kk) q[kk] = *reinterpret_cast<const u32x4_t*>(qp + 32 * kk) ^ flip;
+
+    f32x16_t o[ND];
+    Stats st;
+    bool odd = false;
+    auto step = [&](auto rare, const char* sk, const char* sv, int j0, uint32_t gone) __attribute__((always_inline)) {
+        constexpr bool RARE = decltype(rare)::value;
+        if (j0 >= wkeys) return;  // nothing there for this wave's rows
+        gone &= (1u << (N / 16)) - 1;
+        const bool masked = j0 + N > wall || (j0 < wfrom && j0 + N > sinks) || gone != 0;
+        auto sees = [&, j0, gone](int key) __attribute__((always_inline)) {
+            const int v = j0 + key;
+            return v < upto && (v >= from || v < sinks) && !(gone >> (key / 16) & 1);
+        };
+        attn_step<T, D, LSE, RARE ? kOdd : kMasks>(sk, sv, klane, vlane, q, o, st, c, masked, sees, lane, odd);
+    };
+    auto use = [&](auto rare, const char* sk, const char* sv, int j0, uint32_t gone) __attribute__((always_inline)) {
+        if constexpr (SPLIT == 2) {
+            step(rare, sk + turn * C::GROUPS * C::KG, sv + turn * C::GROUPS * C::VG, j0 + turn * N, gone >> (turn * (N / 16)));
+        } else {
+#pragma unroll 1
+            for (int t = 0; t < S::STEPS; ++t)
+                step(rare, sk + t * C::GROUPS * C::KG, sv + t * C::GROUPS * C::VG, j0 + t * N, gone >> (t * (N / 16)));
+        }
+    };
+    // Two buffers: while the steps in one are used those in the other arrive. The barrier before
+    // a use has every wave's loads of it landed, and every wave past the buffer refilled next.
+    auto run = [&](auto rare) __attribute__((always_inline)) {
+        for (int j0 = 0; j0 < keys; j0 += 2 * UNIT) {
+            staged_barrier();
+            if (j0 + UNIT < keys) {
+                gone1 = fetch(j0 + UNIT, ids, s_k1, s_v1);
+                if (j0 + 2 * UNIT < keys) ids = pages_of(j0 + 2 * UNIT);
+            }
+            use(rare, s_k0, s_v0, j0, gone0);
+            if (j0 + UNIT >= keys) break;
+            staged_barrier();
+            if (j0 + 2 * UNIT < keys) {
+                gone0 = fetch(j0 + 2 * UNIT, ids, s_k0, s_v0);
+                if (j0 + 3 * UNIT < keys) ids = pages_of(j0 + 3 * UNIT);
+            }
+            use(rare, s_k1, s_v1, j0 + UNIT, gone1);
+        }
+    };
+    auto clear = [&]() __attribute__((always_inline)) {
+#pragma unroll
+        for (int db = 0; db < ND; ++db)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[db][i] = 0.f;
+        st = Stats{-INFINITY, 0.f, 0.f};
+    };
+    clear();
+    run(std::integral_constant<bool, false>{});
+    if (__syncthreads_or(odd)) {  // rare: the whole tile again
+        clear();
+        ids = pages_of(0);
+        gone0 = fetch(0, ids, s_k0, s_v0);
+        if (UNIT < keys) ids = pages_of(UNIT);
+        run(std::integral_constant<bool, true>{});
+        __syncthreads();  // the buffers are written to below
+    }
+
+    if constexpr (SPLIT == 2) {
+        // O of the second steps' waves through LDS: D / 2 registers of 64 lanes a wave, in the
+        // buffers of K and V, a row group in each
+        static_assert(D / 2 * 256 <= S::STEPS * C::GROUPS * C::KG, "a wave's O fits a buffer");
+        float* so = reinterpret_cast<float*>(rw == 0 ? s_k0 : rw == 1 ? s_k1 : rw == 2 ? s_v0 : s_v1);
+        __shared__ float s_st[4][3][64];
+        if (turn == 1) {
+#pragma unroll
+            for (int db = 0; db < ND; ++db)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) so[(16 * db + i) * 64 + lane] = o[db][i];
+            s_st[rw][0][lane] = st.m;
+            s_st[rw][1][lane] = st.l;
+            s_st[rw][2][lane] = st.exact;
+        }
+        __syncthreads();
+        if (turn == 1) return;
+        const float m1 = s_st[rw][0][lane], mm = fmaxf(st.m, m1);
+        const float a0 = st.m == -INFINITY ? 0.f : rescaled(st.m, mm, c);
+        const float a1 = m1 == -INFINITY ? 0.f : rescaled(m1, mm, c);
+        st.m = mm;
+        st.l = a0 * st.l + a1 * s_st[rw][1][lane];
+        st.exact = a0 * st.exact + a1 * s_st[rw][2][lane];
+#pragma unroll
+        for (int db = 0; db < ND; ++db)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[db][i] = a0 * o[db][i] + a1 * so[(16 * db + i) * 64 + lane];
+    }
+    if (!whole) {  // this range's sums, for the join
+        const float l = other_half_sum(st.l), e = ES == 2 && LSE ? other_half_sum(st.exact) : l;
+        const int64_t at = ((int64_t)unit * a.ranges + rg) * M + 32 * rw + (lane & 31);
+        if (r < w.rows) {
+            float* to = a.part_o + at * D + 4 * half;
+#pragma unroll
+            for (int db = 0; db < ND; ++db)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    *reinterpret_cast<f32x4_t*>(to + 32 * db + 8 * i) =
+                        f32x4_t{o[db][4 * i], o[db][4 * i + 1], o[db][4 * i + 2], o[db][4 * i + 3]};
+            if (half == 0) a.part_ml[at] = make_float4(st.m * c, l, e, 0.f);
+        }
+        return;
+    }
+    // All waves have met since the last use of K and V: each has a part of the buffers to itself (with
+    // SPLIT 2 in the one where it read the other half's O).
+    constexpr int PART = 32 * ((C::ROWB < 256 ? C::ROWB : 256) + 16), PER_BUFFER = (M / 32 + 3) / 4;
+    static_assert(PER_BUFFER * PART <= S::STEPS * C::GROUPS * C::KG, "the waves' parts fit the buffers");
+    const int buffer = rw / PER_BUFFER;
+    char* part = buffer == 0 ? s_k0 : buffer == 1 ? s_k1 : buffer == 2 ? s_v0 : s_v1;
+    st.m *= c;
+    write_rows<T, D>(p, w, wfirst, lane, o, st, part + rw % PER_BUFFER * PART);
+}
+
+enum { kTwin, kSplit, kWide, kLone };
+
+int shape_of(const gdn_kv_cache& c, const gdn_extend_dims& d)
+{
+    if (d.dtype == GDN_F32 && c.d == 256) return kLone;
+    const int64_t rows = d.total_q * (d.h_q / c.h_kv);
+    if (d.dtype == GDN_BF16 && c.d == 256 && rows / c.n >= 1024) return kWide;
+    return rows * c.h_kv / 128 < 512 ? kSplit : kTwin;
+}
+
+template <typename T, int D, bool LSE, typename S>
+hipError_t launch_kernel(const ExtendCall& c, const ExtendPlan& pl, void* ws)
+{
+    const ExtendArgs a = extend_args(c, pl, ws);
+    hipLaunchKernelGGL((extend_tile_kernel<T, D, LSE, S>), grid_of(pl.units * pl.ranges), dim3(64 * S::WAVES), 0, c.stream, a);
+    const hipError_t e = hipGetLastError();
+    return e != hipSuccess || pl.ranges == 1 ? e : launch_extend_join(a, pl.m);
+}
+
+template <typename T, int D, bool LSE>
+hipError_t launch_shape(const ExtendCall& c, const ExtendPlan& pl, void* ws)
+{
+    if constexpr (Tile<T, D>::ROWS == 1) {
+        return launch_kernel<T, D, LSE, Lone>(c, pl, ws);
+    } else {
+        switch (shape_of(c.c, c.d)) {
+            case kSplit: return launch_kernel<T, D, LSE, Split>(c, pl, ws);
+            case kWide:
+                if constexpr (D == 256) return launch_kernel<T, D, LSE, Wide>(c, pl, ws);
+                else return hipErrorInvalidValue;
+            default: return launch_kernel<T, D, LSE, Twin>(c, pl, ws);
+        }
+    }
+}
+
+template <int D>
+hipError_t launch_d(const ExtendCall& c, const ExtendPlan& pl, void* ws)
+{
+    if (c.d.dtype == GDN_F32) return launch_shape<float, D, false>(c, pl, ws);
+    return c.lse ? launch_shape<uint16_t, D, true>(c, pl, ws) : launch_shape<uint16_t, D, false>(c, pl, ws);
+}
+
+}  // namespace
+
+ExtendPlan extend_tile_plan(const gdn_kv_cache& c, const gdn_extend_dims& d)
+{
+    ExtendPlan p;
+    p.m = shape_of(c, d) == kWide ? 256 : 128;
+    const int64_t g = d.h_q / c.h_kv;
+    p.per_seq = 0;
+    p.slots = d.total_q * g / p.m + c.n;
+    p.units = p.slots * c.h_kv;
+    // 256 workgroups of eight waves, or 512 of four, fill the chip. Ranges of 512 positions or more.
+    const int64_t tiles = (d.total_q * g + p.m - 1) / p.m * c.h_kv, len = extend_longest(c, d, p.m);
+    const int64_t want = 256;
+    int64_t ranges = want / (tiles > 0 ? tiles : 1);
+    if (ranges > len / 512) ranges = len / 512;
+    if (ranges > 0x7fffffff / p.units) ranges = 0x7fffffff / p.units;  // the grid
+    if (ranges < 1) ranges = 1;
+    const int64_t per = ((len + ranges - 1) / ranges + 255) / 256 * 256;  // whole units of every shape
+    p.range = per > 0 ? per : 256;
+    p.ranges = len > 0 ? (len + p.range - 1) / p.range : 1;
+    return p;
+}
+
+hipError_t launch_extend_tiles(const ExtendCall& c, const ExtendPlan& p, void* ws)
+{
+    switch (c.c.d) {
+        case 64: return launch_d<64>(c, p, ws);
+        case 128: return launch_d<128>(c, p, ws);
+        case 256: return launch_d<256>(c, p, ws);
+        default: return hipErrorInvalidValue;
+    }
+}
+
+}  // namespace gdn

@@ -1,0 +1,134 @@
+// gdn_extend.hpp -- what the kernels of gdn_attn_extend share: which rows a workgroup takes, what they
+// see, and where divided sums go (not part of the C ABI).
+#pragma once
+
+#include "gdn_attn_tile.hpp"
+
+namespace gdn {
+
+// Where the keys of a call's tiles are divided into ranges, sums go to the workspace,
+// [unit][range][row]: o [D] fp32 and (m, l, exact l, -).
+struct ExtendPlan {
+    int m;          // rows of a tile (0: nothing is launched)
+    int per_seq;    // tiles of every sequence, or 0: as many as its rows need, packed
+    int64_t slots;  // tiles of one KV head that the grid has room for
+    int64_t units;  // ... of all KV heads
+    int64_t range;  // virtual positions of a range
+    int64_t ranges;
+    int rows_from, rows_to;  // the sequences that are taken: by their rows (of a KV head)
+    size_t workspace(const gdn_kv_cache& c) const
+    {
+        return m == 0 || ranges == 1 ? 0 : (size_t)(units * ranges * m) * (c.d * sizeof(float) + sizeof(float4));
+    }
+};
+
+struct ExtendArgs {
+    ExtendCall c;
+    int64_t range;
+    int ranges, slots, per_seq, rows_from, rows_to, page_shift;
+    float* part_o;
+    float4* part_ml;
+};
+
+inline ExtendArgs extend_args(const ExtendCall& c, const ExtendPlan& p, void* ws)
+{
+    ExtendArgs a;
+    a.c = c;
+    a.range = p.range;
+    a.ranges = (int)p.ranges;
+    a.slots = (int)p.slots;
+    a.per_seq = p.per_seq;
+    a.rows_from = p.rows_from;
+    a.rows_to = p.rows_to;
+    a.page_shift = __builtin_ctz((unsigned)c.c.page_size);
+    a.part_o = static_cast<float*>(ws);
+    a.part_ml = reinterpret_cast<float4*>(a.part_o + p.units * p.ranges * p.m * c.c.d);
+    return a;
+}
+
+// Virtual positions that a tile of m rows may have.
+inline int64_t extend_longest(const gdn_kv_cache& c, const gdn_extend_dims& d, int m)
+{
+    if (d.window == 0) return d.max_len;
+    const int64_t g = d.h_q / c.h_kv;
+    const int64_t w = d.window + (m - 1) / g + 1 + 15 + (d.sinks + 15) / 16 * 16;
+    return w < d.max_len ? w : d.max_len;
+}
+
+hipError_t launch_extend_join(const ExtendArgs& a, int m);
+ExtendPlan extend_tile_plan(const gdn_kv_cache& c, const gdn_extend_dims& d);
+hipError_t launch_extend_tiles(const ExtendCall& c, const ExtendPlan& p, void* ws);
+
+namespace {
+
+// A tile: rows row0 .. of the `rows` that its sequence has, and the positions that they see. These are
+// [0, sinks) and the stretch from the first row's window to the last row, in whole 16-position
+// blocks and numbered through: virtual position v is position v below `sink` and v + skip from there on.
+// Where something is skipped, all of the tile's rows lie behind it, so that a row at position p sees
+//     v < p + 1 - skip  with  v >= p + 1 - window - skip  or  v < sinks.
+struct Span {
+    int64_t q0;
+    int seq, head, rows, row0, g;
+    int first, last;      // positions of its first and last row
+    int shift;            // position of the sequence's row 0
+    int sink, skip, len;  // len: virtual positions
+    __device__ __forceinline__ int pos(int v) const { return v < sink ? v : v + skip; }
+};
+
+template <int M>
+__device__ __forceinline__ bool find_span(const ExtendArgs& a, uint32_t unit, Span* t)
+{
+    const ExtendCall& p = a.c;
+    const int g = p.d.h_q / p.c.h_kv, n = (int)p.c.n, total = (int)p.d.total_q;
+    const int slot = (int)(unit / (uint32_t)p.c.h_kv);
+    t->head = (int)(unit - (uint32_t)slot * (uint32_t)p.c.h_kv);
+    int s = 0, qa, qb, local;
+    if (a.per_seq) {
+        s = slot / a.per_seq;
+        if (s >= n) return false;
+        qa = p.cu_q ? clamp_to(p.cu_q[s], total) : s;
+        qb = p.cu_q ? clamp_to(p.cu_q[s + 1], total) : s + 1;
+        local = slot - s * a.per_seq;
+    } else {
+        // sequence s has the slots [floor(cu[s] g / M) + s, floor(cu[s + 1] g / M) + s + 1): disjoint, in order
+        // and enough; it is looked for 64 sequences at a time, one a lane
+        const int lane = threadIdx.x & 63;
+        auto base = [&](int x) { return (int)((int64_t)clamp_to(p.cu_q ? p.cu_q[x] : x, total) * g / M) + x; };
+        for (int span = n; span > 1;) {  // the sequence is in [s, s + span)
+            const int step = (span + 63) / 64, at = s + lane * step;
+            const bool before = lane * step < span && (lane == 0 || base(at) <= slot);
+            const int x = 63 - __builtin_clzll(__ballot(before) | 1);  // the last lane not past the slot
+            s += x * step;
+            span = span - x * step < step ? span - x * step : step;
+        }
+        s = __builtin_amdgcn_readfirstlane(s);
+        qa = p.cu_q ? clamp_to(p.cu_q[s], total) : s;
+        qb = p.cu_q ? clamp_to(p.cu_q[s + 1], total) : s + 1;
+        local = slot - ((int)((int64_t)qa * g / M) + s);
+    }
+    const int len_q = qb - qa;
+    if (len_q <= 0 || local < 0) return false;
+    t->seq = s;
+    t->q0 = qa;
+    t->g = g;
+    t->rows = (len_q < p.d.max_q ? len_q : (int)p.d.max_q) * g;
+    if (t->rows < a.rows_from || t->rows > a.rows_to) return false;
+    const int tiles = (t->rows + M - 1) / M;
+    if (local >= tiles) return false;
+    t->row0 = (tiles - 1 - local) * M;  // the last, which see most, first
+    int len = p.lens[s];
+    len = len < p.d.max_len ? len : (int)p.d.max_len;
+    len = len < 0 ? 0 : len;
+    t->shift = len - len_q;
+    t->first = t->shift + t->row0 / g;
+    t->last = t->shift + ((t->row0 + M < t->rows ? t->row0 + M : t->rows) - 1) / g;
+    const int w = (int)p.d.window, lo = w && t->first >= w ? (t->first - w + 1) & ~15 : 0;
+    const int sinks = (int)((p.d.sinks + 15) & ~15);
+    t->sink = sinks < lo ? sinks : lo;
+    t->skip = lo - t->sink;
+    t->len = t->last < 0 ? 0 : t->last + 1 - t->skip;
+    return true;
+}
+
+}  // namespace
+}  // namespace gdn
