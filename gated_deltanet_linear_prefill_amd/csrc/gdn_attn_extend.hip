@@ -579,10 +579,64 @@ __global__ void __launch_bounds__(16 * kJoinGroups) extend_join_kernel(ExtendArg
     if (p.lse && el == 0) p.lse[to] = e > 0.f ? (top + __builtin_amdgcn_logf(e)) * kLn2 : (e == e ? -INFINITY : e);
 }
 
+// The same for few ranges of many rows: D / 4 lanes hold a row, first a range each for the weights, then four
+// elements each of the weighted sum.
+constexpr int kFewRanges = 16;
+
+template <typename T, int D, int M>
+__global__ void __launch_bounds__(256) extend_join_rows_kernel(ExtendArgs a)
+{
+    constexpr int LANES = D / 4, ROWS = 256 / LANES;
+    static_assert(M % ROWS == 0 && LANES >= kFewRanges, "a tile is whole workgroups, a range has a lane");
+    __shared__ float s_w[ROWS][kFewRanges];
+    const ExtendCall& p = a.c;
+    const uint32_t unit = block_index() / (M / ROWS);
+    const int tr = (int)(block_index() % (M / ROWS)) * ROWS + threadIdx.x / LANES, lane = threadIdx.x % LANES;
+    if (unit >= (uint32_t)a.slots * (uint32_t)p.c.h_kv) return;  // past the grid's end
+    Span t;
+    if (!find_span<M>(a, unit, &t)) return;
+    const int r = t.row0 + tr;
+    if (t.len <= a.range) return;  // written by its only range
+    const int used = (int)((t.len + a.range - 1) / a.range);
+    const int64_t at = (int64_t)unit * a.ranges * M + tr;
+    const float4 ml = lane < used && r < t.rows ? a.part_ml[at + (int64_t)lane * M] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+    const float* from = a.part_o + at * D + lane * 4;
+    float top = ml.x;
+#pragma unroll
+    for (int off = kFewRanges / 2; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, LANES));
+    top = __shfl(top, 0, LANES);
+    const float w = ml.x == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(ml.x - top);
+    float l = ml.y * w, e = ml.z * w;
+#pragma unroll
+    for (int off = kFewRanges / 2; off >= 1; off >>= 1) {
+        l += __shfl_xor(l, off, LANES);
+        e += __shfl_xor(e, off, LANES);
+    }
+    l = __shfl(l, 0, LANES);
+    if (lane < kFewRanges) s_w[threadIdx.x / LANES][lane] = w;
+    __syncthreads();
+    if (r >= t.rows) return;
+    f32x4_t o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+    for (int x = 0; x < used; ++x)
+        o += *reinterpret_cast<const f32x4_t*>(from + (int64_t)x * M * D) * s_w[threadIdx.x / LANES][x];
+    o *= l > 0.f ? 1.f / l : (l == l ? 0.f : l);
+    const int i = (int)((uint32_t)r / (uint32_t)t.g);
+    const int64_t to = (t.q0 + i) * p.d.h_q + t.head * t.g + r - i * t.g;
+    T* out = static_cast<T*>(p.out) + to * D + lane * 4;
+    if constexpr (sizeof(T) == 2) *reinterpret_cast<u32x2_t*>(out) = u32x2_t{pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3])};
+    else *reinterpret_cast<f32x4_t*>(out) = o;
+    if (p.lse && lane == 0) p.lse[to] = e > 0.f ? (top + __builtin_amdgcn_logf(e)) * kLn2 : (e == e ? -INFINITY : e);
+}
+
 template <typename T, int D, int M>
 hipError_t launch_join(const ExtendArgs& a)
 {
     const int64_t units = (int64_t)a.slots * a.c.c.h_kv;
+    if (a.ranges <= kFewRanges) {
+        hipLaunchKernelGGL((extend_join_rows_kernel<T, D, M>), grid_of(units * (M * D / 1024)), dim3(256), 0, a.c.stream, a);
+        return hipGetLastError();
+    }
     hipLaunchKernelGGL((extend_join_kernel<T, D, M>), grid_of(units * M * (D / 64)), dim3(join_threads(a.ranges)), 0,
                        a.c.stream, a);
     return hipGetLastError();
@@ -691,7 +745,7 @@ struct Plans {
 Plans make_plans(const gdn_kv_cache& c, const gdn_extend_dims& d)
 {
     const int64_t most = d.max_q * (d.h_q / c.h_kv);
-    const bool only_stream = most <= kStreamRows || c.store == GDN_FP8;
+    const bool only_stream = most <= kStreamRows || (d.dtype == GDN_F32 && c.store == GDN_FP8);
     Plans p;
     p.stream.m = p.tiles.m = 0;
     if (only_stream || c.n > 1) p.stream = stream_plan(c, d, only_stream ? most : kStreamRows);

@@ -21,13 +21,34 @@ using Twin = Shape<4, 1, 1, 2>;
 using Split = Shape<8, 2, 2, 2>;
 // 256 rows share every staged key: the least traffic.
 using Wide = Shape<8, 2, 1, 2>;
+// The same for an fp8 store, whose codes take LDS of their own beside the bf16 keys.
+using Codes8 = Shape<8, 1, 1, 2>;
 // fp32 with d = 256, where a wave's O and Q take all of 256 registers.
 using Lone = Shape<4, 1, 1, 1>;
 
-template <typename T, int D, bool LSE, typename S>
+// Every wave's loads to LDS have landed, and every wave is past its reads of LDS. The wait is one that the
+// compiler sees (vmcnt 0, lgkmcnt 0): it would otherwise wait, before a buffer is read, for loads that
+// were issued to the other one since, where it cannot count them.
+__device__ __forceinline__ void landed_barrier()
+{
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0x0070);
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// What is the same in all lanes, in scalar registers.
+__device__ __forceinline__ int64_t uniform(int64_t x)
+{
+    return (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(x >> 32)) << 32 |
+                     (uint32_t)__builtin_amdgcn_readfirstlane((int)x));
+}
+
+template <typename T, bool FP8, int D, bool LSE, typename S>
 __global__ void __launch_bounds__(64 * S::WAVES, S::PER_SIMD) extend_tile_kernel(ExtendArgs a)
 {
     using C = Tile<T, D>;
+    static_assert(!FP8 || (sizeof(T) == 2 && S::WAVES == 8 && S::STEPS == 1 && S::SPLIT == 1), "what codes are staged for");
     constexpr int N = C::N, UNIT = S::STEPS * N, M = S::ROWS, ND = D / 32, SPLIT = S::SPLIT, ES = C::ES;
     constexpr int BLOCKS = UNIT / 16;  // 16-position blocks of a unit
     static_assert(BLOCKS <= 64, "a lane each");
@@ -35,6 +56,9 @@ __global__ void __launch_bounds__(64 * S::WAVES, S::PER_SIMD) extend_tile_kernel
     // are filling another
     __shared__ __align__(16) char s_k0[S::STEPS * C::GROUPS * C::KG], s_k1[S::STEPS * C::GROUPS * C::KG];
     __shared__ __align__(16) char s_v0[S::STEPS * C::GROUPS * C::VG], s_v1[S::STEPS * C::GROUPS * C::VG];
+    // fp8: the codes of a unit's K and V, 8 KiB each, and their scales
+    __shared__ __align__(16) char s_r0[FP8 ? 2 * UNIT * D : 16], s_r1[FP8 ? 2 * UNIT * D : 16];
+    __shared__ __align__(16) char s_c0[FP8 ? 2 * UNIT : 16], s_c1[FP8 ? 2 * UNIT : 16];
     const ExtendCall& p = a.c;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int half = lane >> 5;
@@ -59,37 +83,103 @@ __global__ void __launch_bounds__(64 * S::WAVES, S::PER_SIMD) extend_tile_kernel
     const int vlane = ES == 2 ? (4 * half + ((lane >> 2) & 3)) * C::VG + ((lane >> 4) & 1) * 32 + (lane & 3) * 8
                               : 4 * half * C::VG + lane % 32 * 4;
 
-    // Page ids of the unit from key v0 on, a block a lane; -1: not there. Blocks past the end are as its last.
+    // Page ids of the unit from key v0 on, a block a lane. Blocks past the end are as its last.
     const int32_t* table = p.c.page_table + w.seq * p.c.max_pages;
     auto pages_of = [&](int v0) __attribute__((always_inline)) {
         const int v = begin + v0 + 16 * (lane < BLOCKS ? lane : BLOCKS - 1);
-        const int id = table[w.pos(v < w.len ? v : w.len - 1) >> a.page_shift];
-        return id >= 0 && id < p.c.num_pages ? id : -1;
+        return table[w.pos(v < w.len ? v : w.len - 1) >> a.page_shift];
     };
-    // Stages the unit from key v0 on, whose pages are `ids`. Returns its blocks that are not there, a bit each.
+    auto absent = [&](int id) __attribute__((always_inline)) { return id < 0 || id >= p.c.num_pages; };
+    // Stages the unit from key v0 on, whose pages are `ids`, and loads those of the unit after it (before
+    // the keys: loads are waited for in their order, and these are not to wait for the keys'). Returns the
+    // unit's blocks that are not there, a bit each.
     const char* kpool = static_cast<const char*>(p.c.k);
     const char* vpool = static_cast<const char*>(p.c.v);
-    auto fetch = [&](int v0, int ids, char* sk, char* sv) __attribute__((always_inline)) {
-#pragma unroll
-        for (int i = 0; i < S::STEPS * C::GROUPS / S::WAVES; ++i) {
-            const int x = i * S::WAVES + wave, v = v0 + x * C::ROWS;
-            const int id = __builtin_amdgcn_readlane(ids, x * C::ROWS / 16);
-            const int left = id < 0 ? 0 : valid - v;
-            const int64_t row = (((int64_t)(id < 0 ? 0 : id) * p.c.h_kv + w.head) << a.page_shift) +
-                                (w.pos(begin + v) & (p.c.page_size - 1));
-            const int bytes = left >= C::ROWS ? 1024 : left <= 0 ? 0 : left * C::ROWB;
-            load_to_lds(make_rsrc(kpool + row * C::ROWB, bytes), sk + x * C::KG, lane * 16);
-            load_to_lds(make_rsrc(vpool + row * C::ROWB, bytes), sv + x * C::VG, lane * 16);
-        }
-        return (uint32_t)__ballot(lane < BLOCKS && ids < 0);
-    };
     int ids = 0;
+    auto fetch = [&](int v0, char* sk, char* sv) __attribute__((always_inline)) {
+        asm volatile("" : "+v"(ids));  // not looked at before the barrier that this follows
+        const int now = absent(ids) ? -1 : ids;
+        ids = pages_of(v0 + UNIT);
+        // A wave stages consecutive keys, at most 16 of which lie in one block and need one address. It starts
+        // at another group than its neighbours, whose runs are a multiple of the memory channels' stride away.
+        constexpr int MINE = UNIT / S::WAVES, RUN = MINE < 16 ? MINE : 16, GR = RUN / C::ROWS;
+#pragma unroll
+        for (int y = 0; y < MINE / RUN; ++y) {
+            const int first = wave * MINE + y * RUN, v = v0 + first;
+            const int id = __builtin_amdgcn_readlane(now, first / 16), left = id < 0 ? 0 : valid - v;
+            const int64_t row = uniform((((int64_t)(id < 0 ? 0 : id) * p.c.h_kv + w.head) << a.page_shift) +
+                                        (w.pos(begin + v) & (p.c.page_size - 1)));
+            const int bytes = __builtin_amdgcn_readfirstlane((left >= RUN ? RUN : left <= 0 ? 0 : left) * C::ROWB);
+            const __amdgpu_buffer_rsrc_t rk = make_rsrc(kpool + row * C::ROWB, bytes), rv = make_rsrc(vpool + row * C::ROWB, bytes);
+#pragma unroll
+            for (int i = 0; i < GR; ++i) {
+                const int gi = (i + wave) % GR, at = first / C::ROWS + gi;
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(rk, (__attribute__((address_space(3))) void*)(sk + at * C::KG), 16, lane * 16, gi * 1024, 0, 0);
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(rv, (__attribute__((address_space(3))) void*)(sv + at * C::VG), 16, lane * 16, gi * 1024, 0, 0);
+            }
+        }
+        return (uint32_t)__ballot(lane < BLOCKS && now < 0);
+    };
+    // The same for codes: 1 KiB of K and of V a wave, and the scales by the first two waves.
+    auto fetch_codes = [&](int v0, char* raw, char* scales) __attribute__((always_inline)) {
+        asm volatile("" : "+v"(ids));
+        const int now = absent(ids) ? -1 : ids;
+        ids = pages_of(v0 + UNIT);
+        constexpr int RUN = UNIT / 8;
+        const int first = wave * RUN, v = v0 + first;
+        const int id = __builtin_amdgcn_readlane(now, first / 16), left = id < 0 ? 0 : valid - v;
+        const int64_t row = uniform((((int64_t)(id < 0 ? 0 : id) * p.c.h_kv + w.head) << a.page_shift) +
+                                    (w.pos(begin + v) & (p.c.page_size - 1)));
+        const int bytes = __builtin_amdgcn_readfirstlane((left >= RUN ? RUN : left <= 0 ? 0 : left) * D);
+        load_to_lds(make_rsrc(kpool + row * D, bytes), raw + wave * 1024, lane * 16);
+        load_to_lds(make_rsrc(vpool + row * D, bytes), raw + UNIT * D + wave * 1024, lane * 16);
+        if (wave < 2 && lane < UNIT / 4) {  // four keys a lane; of absent pages and past the end any, not used
+            const int at = __shfl(now, lane / 4), vb = begin + v0 + lane / 4 * 16;
+            const int pos = w.pos(vb < w.len ? vb : (w.len - 1) & ~15);
+            const uint8_t* from = (wave == 0 ? p.c.k_scale : p.c.v_scale) +
+                                  ((((int64_t)(at < 0 ? 0 : at) * p.c.h_kv + w.head) << a.page_shift) + (pos & (p.c.page_size - 1)) + lane % 4 * 4);
+            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)from,
+                                             (__attribute__((address_space(3))) void*)(scales + wave * UNIT), 4, 0, 0);
+        }
+        return (uint32_t)__ballot(lane < BLOCKS && now < 0);
+    };
+    // Codes that have arrived to bf16 in the places where keys are staged: 16 of K and of V a thread. A value is
+    // its code times a power of two, which bf16 holds exactly (but below its normal range).
+    auto convert = [&](int v0, uint32_t gone, const char* raw, const char* scales, char* sk, char* sv) __attribute__((always_inline)) {
+        const int row = threadIdx.x / (D / 16), at = row / C::ROWS, to = row % C::ROWS * C::ROWB + threadIdx.x % (D / 16) * 32;
+        const bool there = v0 + row < valid && !(gone >> (row / 16) & 1);  // elsewhere codes are 0, scales anything
+        auto write = [&](const char* codes, int scale, char* dst) __attribute__((always_inline)) {
+            const u32x4_t x = *reinterpret_cast<const u32x4_t*>(codes + threadIdx.x * 16);
+            const float f = __uint_as_float((uint32_t)(there ? scale : 127) << 23);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                u32x4_t y;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    y[2 * i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[2 * h + i], f, false));
+                    y[2 * i + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[2 * h + i], f, true));
+                }
+                *reinterpret_cast<u32x4_t*>(dst + to + 16 * h) = y;
+            }
+        };
+        const uint8_t* sc = reinterpret_cast<const uint8_t*>(scales);
+        write(raw, sc[row], sk + at * C::KG);
+        write(raw + UNIT * D, sc[UNIT + row], sv + at * C::VG);
+    };
     uint32_t gone0 = 0, gone1 = 0;
-    if (keys > 0) {
+    auto start = [&]() __attribute__((always_inline)) {
+        if (keys <= 0) return;
         ids = pages_of(0);
-        gone0 = fetch(0, ids, s_k0, s_v0);
-        if (UNIT < keys) ids = pages_of(UNIT);
-    }
+        if constexpr (FP8) {
+            gone0 = fetch_codes(0, s_r0, s_c0);
+            if (UNIT < keys) gone1 = fetch_codes(UNIT, s_r1, s_c1);
+            landed_barrier();
+            convert(0, gone0, s_r0, s_c0, s_k0, s_v0);
+        } else {
+            gone0 = fetch(0, s_k0, s_v0);
+        }
+    };
+    start();
 
     // What rows see: keys below upto that are at or past from, or sinks. Of the wave's first row, its last,
     // and this lane's.
@@ -117,44 +207,58 @@ __global__ void __launch_bounds__(64 * S::WAVES, S::PER_SIMD) extend_tile_kernel
     f32x16_t o[ND];
     Stats st;
     bool odd = false;
-    auto step = [&](auto rare, const char* sk, const char* sv, int j0, uint32_t gone) __attribute__((always_inline)) {
-        constexpr bool RARE = decltype(rare)::value;
-        if (j0 >= wkeys) return;  // nothing there for this wave's rows
+    auto step = [&](auto mode, const char* sk, const char* sv, int j0, uint32_t gone) __attribute__((always_inline)) {
+        constexpr int MODE = decltype(mode)::value;
+        if (MODE != kPlain && j0 >= wkeys) return;  // nothing there for this wave's rows
         gone &= (1u << (N / 16)) - 1;
         const bool masked = j0 + N > wall || (j0 < wfrom && j0 + N > sinks) || gone != 0;
         auto sees = [&, j0, gone](int key) __attribute__((always_inline)) {
             const int v = j0 + key;
             return v < upto && (v >= from || v < sinks) && !(gone >> (key / 16) & 1);
         };
-        attn_step<T, D, LSE, RARE ? kOdd : kMasks>(sk, sv, klane, vlane, q, o, st, c, masked, sees, lane, odd);
+        attn_step<T, D, LSE, MODE>(sk, sv, klane, vlane, q, o, st, c, masked, sees, lane, odd);
     };
-    auto use = [&](auto rare, const char* sk, const char* sv, int j0, uint32_t gone) __attribute__((always_inline)) {
+    auto use = [&](auto mode, const char* sk, const char* sv, int j0, uint32_t gone) __attribute__((always_inline)) {
         if constexpr (SPLIT == 2) {
-            step(rare, sk + turn * C::GROUPS * C::KG, sv + turn * C::GROUPS * C::VG, j0 + turn * N, gone >> (turn * (N / 16)));
+            step(mode, sk + turn * C::GROUPS * C::KG, sv + turn * C::GROUPS * C::VG, j0 + turn * N, gone >> (turn * (N / 16)));
         } else {
 #pragma unroll 1
             for (int t = 0; t < S::STEPS; ++t)
-                step(rare, sk + t * C::GROUPS * C::KG, sv + t * C::GROUPS * C::VG, j0 + t * N, gone >> (t * (N / 16)));
+                step(mode, sk + t * C::GROUPS * C::KG, sv + t * C::GROUPS * C::VG, j0 + t * N, gone >> (t * (N / 16)));
         }
     };
     // Two buffers: while the steps in one are used those in the other arrive. The barrier before
-    // a use has every wave's loads of it landed, and every wave past the buffer refilled next.
-    auto run = [&](auto rare) __attribute__((always_inline)) {
-        for (int j0 = 0; j0 < keys; j0 += 2 * UNIT) {
-            staged_barrier();
-            if (j0 + UNIT < keys) {
-                gone1 = fetch(j0 + UNIT, ids, s_k1, s_v1);
-                if (j0 + 2 * UNIT < keys) ids = pages_of(j0 + 2 * UNIT);
-            }
-            use(rare, s_k0, s_v0, j0, gone0);
-            if (j0 + UNIT >= keys) break;
-            staged_barrier();
-            if (j0 + 2 * UNIT < keys) {
-                gone0 = fetch(j0 + 2 * UNIT, ids, s_k0, s_v0);
-                if (j0 + 3 * UNIT < keys) ids = pages_of(j0 + 3 * UNIT);
-            }
-            use(rare, s_k1, s_v1, j0 + UNIT, gone1);
+    // a use has every wave's loads of it landed, and every wave past the buffer refilled next. Codes arrive a
+    // unit earlier, in buffers of their own, and are converted while the unit before them is used.
+    auto pair = [&](auto mode, int j0) __attribute__((always_inline)) {
+        landed_barrier();
+        if constexpr (FP8) {
+            uint32_t gone = 0;
+            if (j0 + 2 * UNIT < keys) gone = fetch_codes(j0 + 2 * UNIT, s_r0, s_c0);
+            if (j0 + UNIT < keys) convert(j0 + UNIT, gone1, s_r1, s_c1, s_k1, s_v1);
+            use(mode, s_k0, s_v0, j0, gone0);
+            gone0 = gone;
+            if (j0 + UNIT >= keys) return;
+            landed_barrier();
+            gone = 0;
+            if (j0 + 3 * UNIT < keys) gone = fetch_codes(j0 + 3 * UNIT, s_r1, s_c1);
+            if (j0 + 2 * UNIT < keys) convert(j0 + 2 * UNIT, gone0, s_r0, s_c0, s_k0, s_v0);
+            use(mode, s_k1, s_v1, j0 + UNIT, gone1);
+            gone1 = gone;
+        } else {
+            if (j0 + UNIT < keys) gone1 = fetch(j0 + UNIT, s_k1, s_v1);
+            use(mode, s_k0, s_v0, j0, gone0);
+            if (j0 + UNIT >= keys) return;
+            landed_barrier();
+            if (j0 + 2 * UNIT < keys) gone0 = fetch(j0 + 2 * UNIT, s_k0, s_v0);
+            use(mode, s_k1, s_v1, j0 + UNIT, gone1);
         }
+    };
+    // Whether all rows see all of two units: the second's pages are in `ids` when it is asked, or in gone1.
+    const int tend = end_of(w.row0) - begin, tfrom = from_of(end_of(w.row0 + M - 1));
+    auto plain = [&](int j0) __attribute__((always_inline)) {
+        return j0 >= tfrom && j0 + 2 * UNIT <= tend && j0 + 2 * UNIT <= keys && gone0 == 0 &&
+               (FP8 ? gone1 == 0 : !__any(lane < BLOCKS && absent(ids)));
     };
     auto clear = [&]() __attribute__((always_inline)) {
 #pragma unroll
@@ -164,13 +268,15 @@ __global__ void __launch_bounds__(64 * S::WAVES, S::PER_SIMD) extend_tile_kernel
         st = Stats{-INFINITY, 0.f, 0.f};
     };
     clear();
-    run(std::integral_constant<bool, false>{});
+    // In order: the window's edge, what all rows see, the causal edge (or all from the first absent page on).
+    int j0 = 0;
+    for (; j0 < keys && !plain(j0); j0 += 2 * UNIT) pair(std::integral_constant<int, kMasks>{}, j0);
+    for (; j0 < keys && plain(j0); j0 += 2 * UNIT) pair(std::integral_constant<int, kPlain>{}, j0);
+    for (; j0 < keys; j0 += 2 * UNIT) pair(std::integral_constant<int, kMasks>{}, j0);
     if (__syncthreads_or(odd)) {  // rare: the whole tile again
         clear();
-        ids = pages_of(0);
-        gone0 = fetch(0, ids, s_k0, s_v0);
-        if (UNIT < keys) ids = pages_of(UNIT);
-        run(std::integral_constant<bool, true>{});
+        start();
+        for (j0 = 0; j0 < keys; j0 += 2 * UNIT) pair(std::integral_constant<int, kOdd>{}, j0);
         __syncthreads();  // the buffers are written to below
     }
 
@@ -220,28 +326,36 @@ __global__ void __launch_bounds__(64 * S::WAVES, S::PER_SIMD) extend_tile_kernel
     // All waves have met since the last use of K and V: each has a part of the buffers to itself (with
     // SPLIT 2 in the one where it read the other half's O).
     constexpr int PART = 32 * ((C::ROWB < 256 ? C::ROWB : 256) + 16), PER_BUFFER = (M / 32 + 3) / 4;
-    static_assert(PER_BUFFER * PART <= S::STEPS * C::GROUPS * C::KG, "the waves' parts fit the buffers");
-    const int buffer = rw / PER_BUFFER;
-    char* part = buffer == 0 ? s_k0 : buffer == 1 ? s_k1 : buffer == 2 ? s_v0 : s_v1;
+    char* part;
+    if constexpr (FP8) {
+        static_assert(PART <= (int)sizeof(s_k0) && 2 * PART <= (int)sizeof(s_v0) && PART <= (int)sizeof(s_r0), "eight parts");
+        part = rw == 0 ? s_k0 : rw == 1 ? s_k1 : rw < 4 ? s_v0 : rw < 6 ? s_v1 : rw == 6 ? s_r0 : s_r1;
+        if (rw == 3 || rw == 5) part += PART;
+    } else {
+        static_assert(PER_BUFFER * PART <= (int)sizeof(s_k0), "the waves' parts fit the buffers");
+        const int buffer = rw / PER_BUFFER;
+        part = (buffer == 0 ? s_k0 : buffer == 1 ? s_k1 : buffer == 2 ? s_v0 : s_v1) + rw % PER_BUFFER * PART;
+    }
     st.m *= c;
-    write_rows<T, D>(p, w, wfirst, lane, o, st, part + rw % PER_BUFFER * PART);
+    write_rows<T, D>(p, w, wfirst, lane, o, st, part);
 }
 
-enum { kTwin, kSplit, kWide, kLone };
+enum { kTwin, kSplit, kWide, kLone, kCodes };
 
 int shape_of(const gdn_kv_cache& c, const gdn_extend_dims& d)
 {
+    if (c.store == GDN_FP8) return kCodes;
     if (d.dtype == GDN_F32 && c.d == 256) return kLone;
     const int64_t rows = d.total_q * (d.h_q / c.h_kv);
     if (d.dtype == GDN_BF16 && c.d == 256 && rows / c.n >= 1024) return kWide;
     return rows * c.h_kv / 128 < 512 ? kSplit : kTwin;
 }
 
-template <typename T, int D, bool LSE, typename S>
+template <typename T, bool FP8, int D, bool LSE, typename S>
 hipError_t launch_kernel(const ExtendCall& c, const ExtendPlan& pl, void* ws)
 {
     const ExtendArgs a = extend_args(c, pl, ws);
-    hipLaunchKernelGGL((extend_tile_kernel<T, D, LSE, S>), grid_of(pl.units * pl.ranges), dim3(64 * S::WAVES), 0, c.stream, a);
+    hipLaunchKernelGGL((extend_tile_kernel<T, FP8, D, LSE, S>), grid_of(pl.units * pl.ranges), dim3(64 * S::WAVES), 0, c.stream, a);
     const hipError_t e = hipGetLastError();
     return e != hipSuccess || pl.ranges == 1 ? e : launch_extend_join(a, pl.m);
 }
@@ -250,14 +364,17 @@ template <typename T, int D, bool LSE>
 hipError_t launch_shape(const ExtendCall& c, const ExtendPlan& pl, void* ws)
 {
     if constexpr (Tile<T, D>::ROWS == 1) {
-        return launch_kernel<T, D, LSE, Lone>(c, pl, ws);
+        return launch_kernel<T, false, D, LSE, Lone>(c, pl, ws);
     } else {
         switch (shape_of(c.c, c.d)) {
-            case kSplit: return launch_kernel<T, D, LSE, Split>(c, pl, ws);
+            case kSplit: return launch_kernel<T, false, D, LSE, Split>(c, pl, ws);
             case kWide:
-                if constexpr (D == 256) return launch_kernel<T, D, LSE, Wide>(c, pl, ws);
+                if constexpr (D == 256) return launch_kernel<T, false, D, LSE, Wide>(c, pl, ws);
                 else return hipErrorInvalidValue;
-            default: return launch_kernel<T, D, LSE, Twin>(c, pl, ws);
+            case kCodes:
+                if constexpr (sizeof(T) == 2) return launch_kernel<T, true, D, LSE, Codes8>(c, pl, ws);
+                else return hipErrorInvalidValue;
+            default: return launch_kernel<T, false, D, LSE, Twin>(c, pl, ws);
         }
     }
 }
@@ -274,10 +391,11 @@ hipError_t launch_d(const ExtendCall& c, const ExtendPlan& pl, void* ws)
 ExtendPlan extend_tile_plan(const gdn_kv_cache& c, const gdn_extend_dims& d)
 {
     ExtendPlan p;
-    p.m = shape_of(c, d) == kWide ? 256 : 128;
+    const int shape = shape_of(c, d);
+    p.m = shape == kWide || shape == kCodes ? 256 : 128;
     const int64_t g = d.h_q / c.h_kv;
-    p.per_seq = 0;
-    p.slots = d.total_q * g / p.m + c.n;
+    p.per_seq = c.n == 1 ? (int)((d.max_q * g + p.m - 1) / p.m) : 0;
+    p.slots = c.n == 1 ? p.per_seq : d.total_q * g / p.m + c.n;
     p.units = p.slots * c.h_kv;
     // 256 workgroups of eight waves, or 512 of four, fill the chip. Ranges of 512 positions or more.
     const int64_t tiles = (d.total_q * g + p.m - 1) / p.m * c.h_kv, len = extend_longest(c, d, p.m);
