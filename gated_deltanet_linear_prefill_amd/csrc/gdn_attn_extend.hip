@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(64 * kWaves, (Cfg<T, FP8, D, CT>::PER_SIMD)) e
 
     const int sinks = (int)p.d.sinks, window = (int)p.d.window;
     auto sees = [&](int v, int x) __attribute__((always_inline)) {
-        return v < upto[x] && (!window || v >= upto[x] - window || v < sinks);
+        return (v < upto[x]) & (!window | (v >= upto[x] - window) | (v < sinks));
     };
     // every row sees the positions before `all` that are in the last row's window, from `from` on, or sinks
     const int all = t.first + 1 - t.skip, from = window ? t.len - window : 0;
@@ -302,7 +302,7 @@ __global__ void __launch_bounds__(64 * kWaves, (Cfg<T, FP8, D, CT>::PER_SIMD)) e
                 }
 #pragma unroll
                 for (int x = 0; x < CT; ++x) {
-                    const bool in = exists && sees(v, x);
+                    const bool in = exists & sees(v, x);
                     s[x][i] = in ? s[x][i] : -INFINITY;
                     seen[x] |= (uint32_t)in << i;
                 }
@@ -742,16 +742,21 @@ struct Plans {
     size_t stream_bytes;  // the tiles' workspace follows
 };
 
+// A tile of 128 rows with a few in use asks for bf16 pages at 7.8 TB/s (128 flops a byte at 1 PFLOP/s), more than
+// memory gives, so that short sequences beside long ones are best left to the tiles, one launch: 24
+// sequences of 1 to 700 tokens, of which few are short, 398 us and 72 + 5 less. fp8 and fp32 pages, a
+// quarter and a third of that, are taken by the kernel of this file.
 Plans make_plans(const gdn_kv_cache& c, const gdn_extend_dims& d)
 {
     const int64_t most = d.max_q * (d.h_q / c.h_kv);
     const bool only_stream = most <= kStreamRows || (d.dtype == GDN_F32 && c.store == GDN_FP8);
+    const bool both = !only_stream && c.n > 1 && c.store != GDN_BF16;
     Plans p;
     p.stream.m = p.tiles.m = 0;
-    if (only_stream || c.n > 1) p.stream = stream_plan(c, d, only_stream ? most : kStreamRows);
+    if (only_stream || both) p.stream = stream_plan(c, d, only_stream ? most : kStreamRows);
     if (!only_stream) {
         p.tiles = extend_tile_plan(c, d);
-        p.tiles.rows_from = c.n > 1 ? kStreamRows + 1 : 0;
+        p.tiles.rows_from = both ? kStreamRows + 1 : 0;
         p.tiles.rows_to = 0x7fffffff;
     }
     p.stream_bytes = p.stream.workspace(c);

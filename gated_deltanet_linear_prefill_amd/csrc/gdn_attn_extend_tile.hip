@@ -37,6 +37,23 @@ __device__ __forceinline__ void landed_barrier()
     asm volatile("" ::: "memory");
 }
 
+// What a row sees of a step: `span` keys from the window's first on; in steps with sinks or with absent pages
+// (blocks of 16, a bit each) more and less.
+struct SeesWindow {
+    static constexpr bool RARE = true;
+    int lo;
+    uint32_t span;
+    int sink;
+    uint32_t gone;
+    bool other;
+    __device__ __forceinline__ bool operator()(int key) const { return (uint32_t)(lo + key) < span; }
+    __device__ __forceinline__ bool rare() const { return other; }
+    __device__ __forceinline__ bool rarely(int key) const
+    {
+        return ((uint32_t)(lo + key) < span || key < sink) && !(gone >> ((uint32_t)key / 16) & 1);
+    }
+};
+
 // What is the same in all lanes, in scalar registers.
 __device__ __forceinline__ int64_t uniform(int64_t x)
 {
@@ -212,10 +229,7 @@ __global__ void __launch_bounds__(64 * S::WAVES, S::PER_SIMD) extend_tile_kernel
         if (MODE != kPlain && j0 >= wkeys) return;  // nothing there for this wave's rows
         gone &= (1u << (N / 16)) - 1;
         const bool masked = j0 + N > wall || (j0 < wfrom && j0 + N > sinks) || gone != 0;
-        auto sees = [&, j0, gone](int key) __attribute__((always_inline)) {
-            const int v = j0 + key;
-            return v < upto && (v >= from || v < sinks) && !(gone >> (key / 16) & 1);
-        };
+        const SeesWindow sees = {j0 - from, (uint32_t)max(upto - from, 0), min(sinks, upto) - j0, gone, gone != 0 || j0 < sinks};
         attn_step<T, D, LSE, MODE>(sk, sv, klane, vlane, q, o, st, c, masked, sees, lane, odd);
     };
     auto use = [&](auto mode, const char* sk, const char* sv, int j0, uint32_t gone) __attribute__((always_inline)) {
@@ -269,9 +283,17 @@ __global__ void __launch_bounds__(64 * S::WAVES, S::PER_SIMD) extend_tile_kernel
     };
     clear();
     // In order: the window's edge, what all rows see, the causal edge (or all from the first absent page on).
+    // O stays in place from loop to loop: without the pins d = 128 kept two copies of it, one in scratch memory
+    // (2.4 times the time).
+    auto pin = [&]() __attribute__((always_inline)) {
+#pragma unroll
+        for (int db = 0; db < ND; ++db) asm volatile("" : "+v"(o[db]));
+    };
     int j0 = 0;
     for (; j0 < keys && !plain(j0); j0 += 2 * UNIT) pair(std::integral_constant<int, kMasks>{}, j0);
+    pin();
     for (; j0 < keys && plain(j0); j0 += 2 * UNIT) pair(std::integral_constant<int, kPlain>{}, j0);
+    pin();
     for (; j0 < keys; j0 += 2 * UNIT) pair(std::integral_constant<int, kMasks>{}, j0);
     if (__syncthreads_or(odd)) {  // rare: the whole tile again
         clear();
@@ -342,13 +364,24 @@ __global__ void __launch_bounds__(64 * S::WAVES, S::PER_SIMD) extend_tile_kernel
 
 enum { kTwin, kSplit, kWide, kLone, kCodes };
 
+// Measured (us of a call, bf16, Twin / Split / Wide; tiles of 128 rows, all KV heads; Split's and Wide's keys in
+// ranges where tiles are few). Few tiles: d = 256, 16/2 heads, 128 new tokens after 8192 (16) 51 / 46 / 63, 512 (64)
+// 102 / 95 / 99, 1024 (128) 170 / 165 / 165, 2048 (256) 336 / 312 / 313; d = 128, 32/8 heads 512 (128)
+// 95 / 92, 1024 (256) 173 / 158; d = 64, 16/16 heads 1024 (128) 77 / 71. 512 tiles: d = 256 4096 from the start 187 /
+// 158 / 205, after 8192 650 / 645 / 660, after 30000 1960 / 1965 / 1890; d = 128 2048 after 8192 317 / 324. More: d = 256
+// 8192 from the start (1024) 539 / 546 / 500, 8 sequences of 100 to 2000 after 4000 376 / 380 / 397; d = 128 4096
+// after 8192 (1024) 671 / 695, 16 prompts of 1 to 2500 307 / 393; d = 64 8192 (1024) 209 / 227.
 int shape_of(const gdn_kv_cache& c, const gdn_extend_dims& d)
 {
     if (c.store == GDN_FP8) return kCodes;
     if (d.dtype == GDN_F32 && c.d == 256) return kLone;
-    const int64_t rows = d.total_q * (d.h_q / c.h_kv);
-    if (d.dtype == GDN_BF16 && c.d == 256 && rows / c.n >= 1024) return kWide;
-    return rows * c.h_kv / 128 < 512 ? kSplit : kTwin;
+    const int64_t tiles = d.total_q * d.h_q / 128;
+    if (tiles <= 256) return kSplit;
+    if (c.d == 256 && d.dtype == GDN_BF16) {
+        if (c.n == 1 && tiles >= 512 && (tiles > 512 || d.max_len >= 16384)) return kWide;
+        if (tiles <= 512) return kSplit;
+    }
+    return kTwin;
 }
 
 template <typename T, bool FP8, int D, bool LSE, typename S>
@@ -397,12 +430,21 @@ ExtendPlan extend_tile_plan(const gdn_kv_cache& c, const gdn_extend_dims& d)
     p.per_seq = c.n == 1 ? (int)((d.max_q * g + p.m - 1) / p.m) : 0;
     p.slots = c.n == 1 ? p.per_seq : d.total_q * g / p.m + c.n;
     p.units = p.slots * c.h_kv;
-    // 256 workgroups of eight waves, or 512 of four, fill the chip. Ranges of 512 positions or more.
+    // 256 workgroups of eight waves run at a time. Each costs its keys and what starting, masking, ending and
+    // joining take, 15 to 20 us: as long as 280 keys (d = 256; a key takes 75 ns with 128 rows), 700 (128)
+    // or 1200 (64). Ranges are those that make this estimate least.
     const int64_t tiles = (d.total_q * g + p.m - 1) / p.m * c.h_kv, len = extend_longest(c, d, p.m);
-    const int64_t want = 256;
-    int64_t ranges = want / (tiles > 0 ? tiles : 1);
-    if (ranges > len / 512) ranges = len / 512;
-    if (ranges > 0x7fffffff / p.units) ranges = 0x7fffffff / p.units;  // the grid
+    const int64_t over = c.d == 256 ? 280 : c.d == 128 ? 700 : 1200;
+    int64_t ranges = 1, least = (tiles + 255) / 256 * (len + over);
+    if (shape != kTwin)
+        for (int64_t r = 2; r <= 64 && len >= 512 * r && tiles * r <= 1024; ++r) {
+            const int64_t cost = (tiles * r + 255) / 256 * (len / r + over) + over / 2;
+            if (cost < least) {
+                least = cost;
+                ranges = r;
+            }
+        }
+    if (p.units > 0 && ranges > 0x7fffffff / p.units) ranges = 0x7fffffff / p.units;  // the grid
     if (ranges < 1) ranges = 1;
     const int64_t per = ((len + ranges - 1) / ranges + 255) / 256 * 256;  // whole units of every shape
     p.range = per > 0 ? per : 256;

@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(64 * S::WAVES, S::PER_SIMD) prefill_kernel(Att
         constexpr int MODE = decltype(mode)::value;
         if (MODE != kPlain && j0 >= wkeys) return;  // nothing there for this wave's rows
         attn_step<T, D, LSE, MODE>(sk, sv, klane, vlane, q, o, st, c, j0 + N > wall,
-                                    [lim = limit - j0](int key) __attribute__((always_inline)) { return key < lim; }, lane, odd);
+                                    SeesBelow{limit - j0}, lane, odd);
     };
     auto use = [&](auto mode, const char* sk, const char* sv, int j0) __attribute__((always_inline)) {
         if constexpr (SPLIT == 2) {

@@ -184,8 +184,16 @@ __device__ __forceinline__ float rescaled(float from, float to, float c)
     return __builtin_amdgcn_exp2f((0.5f * from - 0.5f * to) * (2.f * c));
 }
 
+// What a row sees of a packed sequence: the keys below lim (which may be negative, or above N).
+struct SeesBelow {
+    static constexpr bool RARE = false;
+    int lim;
+    __device__ __forceinline__ bool operator()(int key) const { return key < lim; }
+};
+
 // One step of a wave's 32 rows over N staged keys at sk, sv (klane, vlane: this lane's offsets).
-// This lane's row sees the keys of [0, N) for which sees(key) holds.
+// This lane's row sees the keys of [0, N) for which sees(key) holds; or, with RARE and where it is so that
+// rare(), those for which rarely(key) does.
 template <typename T, int D, bool LSE, int MODE, typename Sees>
 __device__ __forceinline__ void attn_step(const char* sk, const char* sv, int klane, int vlane,
                                           const u32x4_t (&q)[D / (32 / sizeof(T))], f32x16_t (&o)[D / 32],
@@ -225,11 +233,29 @@ __device__ __forceinline__ void attn_step(const char* sk, const char* sv, int kl
     }
 
     if (MODE != kPlain && masked) {
+        if constexpr (Sees::RARE) {
+            // made here and not before the branch, for every step
+            asm volatile("" : "+v"(sees.lo));
+            if (sees.rare()) {
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
+                for (int b = 0; b < NB; ++b)
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-                s[b][i] = sees(C::ROWS * (group_of(i) + 4 * half) + place_of(b, i)) ? s[b][i] : -INFINITY;
+                    for (int i = 0; i < 16; ++i)
+                        s[b][i] = sees.rarely(C::ROWS * (group_of(i) + 4 * half) + place_of(b, i)) ? s[b][i] : -INFINITY;
+            } else {
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        s[b][i] = sees(C::ROWS * (group_of(i) + 4 * half) + place_of(b, i)) ? s[b][i] : -INFINITY;
+            }
+        } else {
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    s[b][i] = sees(C::ROWS * (group_of(i) + 4 * half) + place_of(b, i)) ? s[b][i] : -INFINITY;
+        }
         if (MODE == kMasks)
 #pragma unroll 1
             for (int x = 0; x < C::GROUPS; ++x)
@@ -306,7 +332,9 @@ __device__ __forceinline__ void attn_step(const char* sk, const char* sv, int kl
 #pragma unroll 1
         for (int key = 0; key < N; ++key) {
             const char* at = sv + key / C::ROWS * C::VG + key % C::ROWS * C::ROWB + 4 * half * C::ES;
-            const bool seen = sees(key);
+            bool seen;
+            if constexpr (Sees::RARE) seen = sees.rare() ? sees.rarely(key) : sees(key);
+            else seen = sees(key);
 #pragma unroll
             for (int db = 0; db < ND; ++db)
 #pragma unroll

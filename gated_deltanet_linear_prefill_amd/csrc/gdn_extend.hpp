@@ -75,6 +75,19 @@ struct Span {
     __device__ __forceinline__ int pos(int v) const { return v < sink ? v : v + skip; }
 };
 
+// Sequences up to which a workgroup counts the tiles before its own (64 at a time); of more it looks its
+// sequence up in slots that are spread enough to need no counting.
+constexpr int kExactSeqs = 256;
+
+// Rows of a KV head that a sequence of len_q tokens has.
+__device__ __forceinline__ int rows_of(const ExtendCall& p, int len_q, int g)
+{
+    return len_q <= 0 ? 0 : (len_q < p.d.max_q ? len_q : (int)p.d.max_q) * g;
+}
+
+// A workgroup's tile, or false where there is none. Workgroups without one come last, where the tiles are
+// counted: in between they cost more than they seem to (one in nine of them made a call of 256
+// others, one a CU, take two rounds: 260 us instead of 155).
 template <int M>
 __device__ __forceinline__ bool find_span(const ExtendArgs& a, uint32_t unit, Span* t)
 {
@@ -89,6 +102,36 @@ __device__ __forceinline__ bool find_span(const ExtendArgs& a, uint32_t unit, Sp
         qa = p.cu_q ? clamp_to(p.cu_q[s], total) : s;
         qb = p.cu_q ? clamp_to(p.cu_q[s + 1], total) : s + 1;
         local = slot - s * a.per_seq;
+    } else if (n <= kExactSeqs) {
+        // the tiles of the sequences that are taken, one after another: a lane counts a sequence's
+        const int lane = threadIdx.x & 63;
+        int before = 0;
+        for (; s < n; s += 64) {
+            const int x = s + lane;
+            int tiles = 0;
+            if (x < n) {
+                const int rows = rows_of(p, clamp_to(p.cu_q ? p.cu_q[x + 1] : x + 1, total) - clamp_to(p.cu_q ? p.cu_q[x] : x, total), g);
+                tiles = rows < a.rows_from || rows > a.rows_to ? 0 : (rows + M - 1) / M;
+            }
+            int upto = tiles;
+#pragma unroll
+            for (int off = 1; off < 64; off <<= 1) {
+                const int y = __shfl_up(upto, off, 64);
+                upto += lane >= off ? y : 0;
+            }
+            const uint64_t past = __ballot(before + upto > slot);
+            if (past) {
+                const int l = __builtin_ctzll(past);
+                before += __builtin_amdgcn_readlane(upto, l) - __builtin_amdgcn_readlane(tiles, l);
+                s += l;
+                break;
+            }
+            before += __builtin_amdgcn_readlane(upto, 63);
+        }
+        if (s >= n) return false;
+        qa = clamp_to(p.cu_q ? p.cu_q[s] : s, total);
+        qb = clamp_to(p.cu_q ? p.cu_q[s + 1] : s + 1, total);
+        local = slot - before;
     } else {
         // sequence s has the slots [floor(cu[s] g / M) + s, floor(cu[s + 1] g / M) + s + 1): disjoint, in order
         // and enough; it is looked for 64 sequences at a time, one a lane
@@ -111,7 +154,7 @@ __device__ __forceinline__ bool find_span(const ExtendArgs& a, uint32_t unit, Sp
     t->seq = s;
     t->q0 = qa;
     t->g = g;
-    t->rows = (len_q < p.d.max_q ? len_q : (int)p.d.max_q) * g;
+    t->rows = rows_of(p, len_q, g);
     if (t->rows < a.rows_from || t->rows > a.rows_to) return false;
     const int tiles = (t->rows + M - 1) / M;
     if (local >= tiles) return false;
