@@ -43,7 +43,7 @@ struct Cfg {
     static constexpr int M = 16 * CT;
     // registers of O, K and V; with 512 a wave there is one wave a SIMD
     static constexpr int REGS = CT * VL * 4 + 2 * NB * KL * 4;
-    static constexpr int PER_SIMD = REGS > 192 ? 1 : 2;
+    static constexpr int PER_SIMD = REGS > (CT > 1 ? 159 : 192) ? 1 : 2;
 };
 
 template <int BYTES>
@@ -180,26 +180,33 @@ __global__ void __launch_bounds__(64 * kWaves, (Cfg<T, FP8, D, CT>::PER_SIMD)) e
         *there = page >= 0 && page < p.c.num_pages;
         return (((*there ? page : 0) * p.c.h_kv + kvh) << a.page_shift) + (pos & (p.c.page_size - 1));
     };
+    // A block's rows begin at a scalar address; what a lane adds to it is 32 bits, made from the lane's number
+    // in every step: the registers are full, and an offset reloaded from scratch memory would wait for
+    // the loads before it.
+    uint32_t own = lane;
     auto load_k = [&](const int64_t* row) {
+        asm volatile("" : "+v"(own));
+        const uint32_t koff = (own & 15) * (D * C::ES) + (own >> 4) * 16, soff = (own >> 4) * 4;
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-            const char* kr = kpool + (row[b] + c) * (D * C::ES) + g * 16;
+            const char* kr = kpool + row[b] * (D * C::ES);
 #pragma unroll
-            for (int i = 0; i < C::KL; ++i) kx[b][i] = *reinterpret_cast<const u32x4_t*>(kr + i * 64);
-            if constexpr (FP8) sk[b] = *reinterpret_cast<const uint32_t*>(p.c.k_scale + row[b] + 4 * g);
+            for (int i = 0; i < C::KL; ++i) kx[b][i] = *reinterpret_cast<const u32x4_t*>(kr + koff + i * 64);
+            if constexpr (FP8) sk[b] = *reinterpret_cast<const uint32_t*>(p.c.k_scale + row[b] + soff);
         }
     };
     auto load_v = [&](const int64_t* row) {
+        asm volatile("" : "+v"(own));
+        const uint32_t voff = (own >> 4) * (4 * D * C::ES) + (own & 15) * (C::EPL * C::ES), soff = (own >> 4) * 4;
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
+            const char* vr = vpool + row[b] * (D * C::ES);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const char* vr = vpool + (row[b] + 4 * g + i) * (D * C::ES) + c * (C::EPL * C::ES);
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int u = 0; u < C::U; ++u)
-                    vx[4 * b + i][u] = *reinterpret_cast<const VP*>(vr + u * (16 * C::EPL * C::ES));
-            }
-            if constexpr (FP8) sv[b] = *reinterpret_cast<const uint32_t*>(p.c.v_scale + row[b] + 4 * g);
+                    vx[4 * b + i][u] = *reinterpret_cast<const VP*>(vr + voff + i * (D * C::ES) + u * (16 * C::EPL * C::ES));
+            if constexpr (FP8) sv[b] = *reinterpret_cast<const uint32_t*>(p.c.v_scale + row[b] + soff);
         }
     };
 
@@ -291,9 +298,11 @@ __global__ void __launch_bounds__(64 * kWaves, (Cfg<T, FP8, D, CT>::PER_SIMD)) e
 #pragma unroll
             for (int x = 0; x < CT; ++x) seen[x] = 0;
             uint32_t found = 0;
+            asm volatile("" : "+v"(own));  // comparisons ahead of the branch would be made for every step
+            const int mine = (int)(own >> 4) * 4;
 #pragma unroll
             for (int i = 0; i < 4 * NB; ++i) {
-                const int b = i / 4, v = j0 + 16 * b + 4 * g + i % 4;
+                const int b = i / 4, v = j0 + 16 * b + mine + i % 4;
                 const bool exists = there[b] && v < end;
                 if (!exists) {  // what lies there is anything: not into the product
 #pragma unroll
@@ -723,10 +732,14 @@ ExtendPlan stream_plan(const gdn_kv_cache& c, const gdn_extend_dims& d, int64_t 
     const int64_t tiles = (d.total_q * g + p.m - 1) / p.m;
     const int64_t likely = tiles < p.slots ? tiles : p.slots, real = (likely > c.n ? likely : c.n) * c.h_kv;
     const int64_t len = extend_longest(c, d, p.m), steps = len > 0 ? (len + kRange - 1) / kRange : 1;
-    const int64_t all = real * steps;
-    int64_t want = all / 8 < 4096 ? all / 8 : 4096;
-    if (want < 256 || c.n == 1) want = 256;
-    int64_t ranges = (want + real - 1) / real;
+    // As many ranges as fill the chip once: `fill` workgroups run at a time, and late ones cost a round. Where the
+    // tiles alone do, ranges of about eight steps, so that late ones fill the CUs that are done. Measured
+    // (us, workgroups 128 / 256 / 512 / 1024): 32 sequences behind a window of 4096, d = 256, 16/2 heads 77 / 58 / 63 / 65; 16 of 4
+    // tokens after up to 8192, d = 128, 32/8 150 / 91 / 75 / 82; 8 of one token 80 / 49 / 42 / 43; 8 of 16 (64 rows) 104 / 64 / 75 / 94;
+    // one token after 32767, d = 256 23 / 21 / 23 / 23. Up to four steps stay together, which spares the
+    // second launch.
+    const int64_t fill = c.d == 256 || p.m == 64 ? 256 : 512;
+    int64_t ranges = real >= fill ? (real * steps / 8 < 4096 ? real * steps / 8 : 4096) / real : fill / real;
     if (ranges > (steps + 1) / 2) ranges = (steps + 1) / 2;
     if (steps <= 4) ranges = 1;
     if (ranges > 0x7fffffff / p.units) ranges = 0x7fffffff / p.units;  // the grid
