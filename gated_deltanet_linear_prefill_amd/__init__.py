@@ -751,6 +751,32 @@ def gdn_attn_decode(q, k_cache, v_cache, page_table, lens, *, max_len=None, k_sc
 
 # ---------------------------------------------------------------- around the attention layers
 
+def _new(x, index, stream):
+    """An output of x's shape and type, dense, for a call on `stream`."""
+    return torch.empty_like(x, memory_format=_dense_format) if stream is None else _empty(x.shape, x.dtype, index, stream)
+
+
+_dense_format, _f32 = torch.contiguous_format, torch.float32
+_this_gpu = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
+
+
+def _launch(name, call, index, stream):
+    """Enqueue call(stream handle) with the tensors' GPU as the current one, as the library expects it."""
+    if stream is None:
+        queue = _raw_stream(index)
+    elif stream.device_index == index:
+        queue = stream.cuda_stream
+    else:
+        raise ValueError(f"stream must be one of GPU {index}")
+    if _this_gpu() == index:
+        st = call(queue)
+    else:
+        with torch.cuda.device(index):
+            st = call(queue)
+    if st:
+        raise GdnError(st, name)
+
+
 def _norm_rope(total, d, dtype, index, positions, freq, axis, interleaved, rope_scale, q_weight, k_weight,
                weight_bias, eps, placed):
     """gdn_norm_rope of these tensors; placed: without positions a token turns by its place."""
@@ -758,16 +784,18 @@ def _norm_rope(total, d, dtype, index, positions, freq, axis, interleaved, rope_
     if freq is not None:
         if not isinstance(freq, _Tensor) or freq.dim() != 1:
             raise ValueError("freq must be a float32 tensor [rot / 2]")
-        rot = 2 * freq.shape[0]
-        fp = _dense("freq", freq, (rot // 2,), torch.float32, index)
+        half = freq.shape
+        rot = 2 * half[0]
+        fp = _dense("freq", freq, half, _f32, index)
         if axis is not None:
-            ap = _dense("axis", axis, (rot // 2,), _u8, index)
+            ap = _dense("axis", axis, half, _u8, index)
         if positions is not None:
-            if not isinstance(positions, _Tensor) or positions.dim() not in (1, 2):
-                raise ValueError("positions must be an int32 tensor [tokens] or [axes, tokens]")
-            if positions.dim() == 2:
-                axes = positions.shape[0]
-            pp = _dense("positions", positions, (total,) if positions.dim() == 1 else (axes, total), _i32, index)
+            shape = positions.shape if isinstance(positions, _Tensor) else ()
+            if len(shape) == 2:
+                axes = shape[0]
+            if len(shape) not in (1, 2) or shape[-1] != total:
+                _bad("positions", positions, f"int32 [{total}] or [axes, {total}] on GPU {index}")
+            pp = _dense("positions", positions, shape, _i32, index)
         elif not placed:
             raise ValueError("positions are needed with freq")
     elif positions is not None or axis is not None:
@@ -799,20 +827,24 @@ def gdn_qk_norm_rope(q, k=None, positions=None, *, freq=None, axis=None, interle
         hk = k.shape[1]
         if k.shape[0] != total or k.shape[2] != d:
             raise ValueError(f"k must have shape [{total}, h_kv, {d}]")
-    elif k_weight is not None or k_out is not None:
-        raise ValueError("k_weight and k_out need k")
+    elif k_out is not None:
+        raise ValueError("k_out needs k")
     f = _norm_rope(total, d, q.dtype, gpu, positions, freq, axis, interleaved, rope_scale, q_weight, k_weight,
                    weight_bias, eps, False)
     if q_out is None:
-        q_out = _empty(q.shape, q.dtype, gpu, stream)
+        q_out = _new(q, gpu, stream)
+        qop = q_out.data_ptr()
+    else:
+        qop = _dense("q_out", q_out, q.shape, q.dtype, gpu)
     if k is not None:
         if k_out is None:
-            k_out = _empty(k.shape, q.dtype, gpu, stream)
-        kop = _dense("k_out", k_out, k.shape, q.dtype, gpu)
-    st = _load().gdn_qk_norm_rope(ctypes.byref(f), total, hq, hk, d, t, qp, qt, qh, kp, kt, kh,
-                                  _dense("q_out", q_out, q.shape, q.dtype, gpu), kop, _queue(gpu, stream))
-    if st:
-        raise GdnError(st, "gdn_qk_norm_rope")
+            k_out = _new(k, gpu, stream)
+            kop = k_out.data_ptr()
+        else:
+            kop = _dense("k_out", k_out, k.shape, q.dtype, gpu)
+    lib = _load()
+    _launch("gdn_qk_norm_rope", lambda queue: lib.gdn_qk_norm_rope(
+        ctypes.byref(f), total, hq, hk, d, t, qp, qt, qh, kp, kt, kh, qop, kop, queue), gpu, stream)
     return q_out, k_out
 
 
@@ -844,14 +876,16 @@ def gdn_kv_append(k, v, k_cache, v_cache, page_table, start, cu_seqlens=None, *,
         if q.shape[0] != total or q.shape[2] != c.d:
             raise ValueError(f"q must have shape [{total}, h_q, {c.d}]")
         if q_out is None:
-            q_out = _empty(q.shape, k.dtype, gpu, stream)
-        qop = _dense("q_out", q_out, q.shape, k.dtype, gpu)
-    elif q_weight is not None or q_out is not None:
-        raise ValueError("q_weight and q_out need q")
-    st = _load().gdn_kv_append(ctypes.byref(c), ctypes.byref(f), total, t, kp, kt, kh, vp, vt, vh, sp, cp, hq, qp, qt, qh,
-                               qop, _queue(gpu, stream))
-    if st:
-        raise GdnError(st, "gdn_kv_append")
+            q_out = _new(q, gpu, stream)
+            qop = q_out.data_ptr()
+        else:
+            qop = _dense("q_out", q_out, q.shape, k.dtype, gpu)
+    elif q_out is not None:
+        raise ValueError("q_out needs q")
+    lib = _load()
+    _launch("gdn_kv_append", lambda queue: lib.gdn_kv_append(
+        ctypes.byref(c), ctypes.byref(f), total, t, kp, kt, kh, vp, vt, vh, sp, cp, hq, qp, qt, qh, qop, queue),
+        gpu, stream)
     return q_out
 
 
@@ -892,11 +926,11 @@ def gdn_attn_extend(q, k_cache, v_cache, page_table, lens, cu_q=None, *, window=
     if max_len is None:
         max_len = c.max_pages * c.page_size
     if out is None:
-        out = _empty(q.shape, q.dtype, gpu, stream)
+        out = _new(q, gpu, stream)
         op = out.data_ptr()
     else:
         op = _dense("out", out, q.shape, q.dtype, gpu)
-    lp = None if lse is None else _dense("lse", lse, (total, hq), torch.float32, gpu)
+    lp = None if lse is None else _dense("lse", lse, (total, hq), _f32, gpu)
     dims = ExtendDims(total, max_q if cu_q is not None else min(max_q, 1), max_len, window, sinks, hq, t,
                       d ** -0.5 if scale is None else scale, qt, qh)
     lib = _load()
@@ -905,9 +939,8 @@ def gdn_attn_extend(q, k_cache, v_cache, page_table, lens, cu_q=None, *, window=
         if need:
             workspace = _empty(need, _u8, gpu, stream)
     wbytes = 0 if workspace is None else _check_workspace(workspace, q.device)
-    st = lib.gdn_attn_extend(ctypes.byref(c), ctypes.byref(dims), qp, _index("cu_q", cu_q, (c.n + 1,), gpu),
-                             _index("lens", lens, (c.n,), gpu), op, lp, None if workspace is None else workspace.data_ptr(),
-                             wbytes, _queue(gpu, stream))
-    if st:
-        raise GdnError(st, "gdn_attn_extend")
+    cp, np = _index("cu_q", cu_q, (c.n + 1,), gpu), _index("lens", lens, (c.n,), gpu)
+    wp = None if workspace is None else workspace.data_ptr()
+    _launch("gdn_attn_extend", lambda queue: lib.gdn_attn_extend(
+        ctypes.byref(c), ctypes.byref(dims), qp, cp, np, op, lp, wp, wbytes, queue), gpu, stream)
     return out

@@ -102,6 +102,26 @@ __device__ __forceinline__ bool find_span(const ExtendArgs& a, uint32_t unit, Sp
         qa = p.cu_q ? clamp_to(p.cu_q[s], total) : s;
         qb = p.cu_q ? clamp_to(p.cu_q[s + 1], total) : s + 1;
         local = slot - s * a.per_seq;
+    } else if (n <= 64) {
+        // A lane a sequence, the longest first: their tiles take longest, and what ends last then is short.
+        const int lane = threadIdx.x & 63;
+        int tiles = 0, len = -1;
+        if (lane < n) {
+            const int rows = rows_of(p, clamp_to(p.cu_q ? p.cu_q[lane + 1] : lane + 1, total) - clamp_to(p.cu_q ? p.cu_q[lane] : lane, total), g);
+            tiles = rows < a.rows_from || rows > a.rows_to ? 0 : (rows + M - 1) / M;
+            len = max(p.lens[lane], -1);
+        }
+        int before = 0;  // tiles of the sequences that come before the lane's
+        for (int x = 0; x < n; ++x) {
+            const int other = __builtin_amdgcn_readlane(len, x);
+            before += other > len || (other == len && x < lane) ? __builtin_amdgcn_readlane(tiles, x) : 0;
+        }
+        const uint64_t here = __ballot(slot >= before && slot < before + tiles);
+        if (!here) return false;
+        s = __builtin_ctzll(here);
+        qa = clamp_to(p.cu_q ? p.cu_q[s] : s, total);
+        qb = clamp_to(p.cu_q ? p.cu_q[s + 1] : s + 1, total);
+        local = slot - __builtin_amdgcn_readlane(before, s);
     } else if (n <= kExactSeqs) {
         // the tiles of the sequences that are taken, one after another: a lane counts a sequence's
         const int lane = threadIdx.x & 63;

@@ -32,12 +32,16 @@ __device__ __forceinline__ float2 turn(double pos, float freq, float scale)
 
 enum { kPacked, kSame, kFp8 };  // where keys go: k_out, a pool of T, an fp8 pool
 
-// First elements of the lane's two pieces of E / 2: halves of the same pairs, or neighbours.
-__device__ __forceinline__ void pieces_of(int lane, int piece, int rot, bool paired, int* a, int* b)
+// First elements of the lane's two pieces: both halves of the same pairs, and behind the rotated elements a
+// piece of either half of the rest, so that neighbouring lanes' pieces are neighbours in memory. Rows without
+// such pairs: a piece of either half.
+template <int D, int PIECE>
+__device__ __forceinline__ void pieces_of(int lane, int rot, bool paired, int* a, int* b)
 {
-    const bool split = paired && lane * 2 * piece < rot;
-    *a = split ? lane * piece : lane * 2 * piece;
-    *b = split ? lane * piece + rot / 2 : *a + piece;
+    const int split = paired ? rot : 0, first = lane * 2 * PIECE < split ? 0 : split;
+    const int size = first < split ? split : D - split;  // of the part that the lane is in
+    *a = first + (lane - first / (2 * PIECE)) * PIECE;
+    *b = *a + size / 2;
 }
 
 template <typename T, int D, int STORE>
@@ -51,18 +55,50 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(RopeCall p, int tok, int
     if (token0 >= p.total) return;  // past the grid's end
     const int tokens = p.total - token0 < tok ? (int)(p.total - token0) : tok;
 
+    // This thread's rows: head h of the token t, then every RPB-th. The next one's pieces are loaded while one
+    // is worked on, the first one's before the angles.
+    const int lane = threadIdx.x % LPR;
+    const int heads = p.h_q + p.h_kv * (STORE == kPacked ? 1 : 2);
+    const bool paired = !p.f.interleaved;
+    int ra, rb;  // pieces of a rotated row
+    pieces_of<D, PIECE>(lane, p.f.rot, paired, &ra, &rb);
+    const int va = lane * PIECE, vb = va + D / 2;  // of a V row
+    // Where the lanes of a store cover whole lines it bypasses the caches.
+    constexpr int LINE = 128 / (int)sizeof(T);
+    constexpr bool WHOLE = D / 2 % LINE == 0;
+    const bool whole = paired ? p.f.rot / 2 % LINE == 0 && (D - p.f.rot) / 2 % LINE == 0 : WHOLE;
+    int t = 0, h = threadIdx.x / LPR;
+    auto settle = [&]() __attribute__((always_inline)) {
+        while (h >= heads) {
+            h -= heads;
+            ++t;
+        }
+    };
+    Some<T> na, nb;
+    auto load = [&]() __attribute__((always_inline)) {
+        const int64_t token = token0 + t;
+        const bool is_q = h < p.h_q, rotates = h < p.h_q + p.h_kv;
+        const T* from = is_q       ? static_cast<const T*>(p.q) + token * p.q_token + h * p.q_head
+                        : rotates  ? static_cast<const T*>(p.k) + token * p.k_token + (h - p.h_q) * p.k_head
+                                   : static_cast<const T*>(p.v) + token * p.v_token + (h - p.h_q - p.h_kv) * p.v_head;
+        na.load(from + (rotates ? ra : va));
+        nb.load(from + (rotates ? rb : vb));
+    };
+    settle();
+    if (t < tokens) load();
+
     {  // tok * per <= kThreads: every thread one (token, pair) at most
-        const int t = threadIdx.x / per, x = threadIdx.x - t * per;
-        const int64_t token = token0 + (t < tokens ? t : tokens - 1);
-        int64_t at = 0, row = 0;
+        const int y = threadIdx.x / per, x = threadIdx.x - y * per;
+        const int64_t token = token0 + (y < tokens ? y : tokens - 1);
+        int64_t at = 0;
         if constexpr (STORE != kPacked) {
             bool mine;
             const int64_t first = token0 + (int)(threadIdx.x & ~63u) / per;  // of the wave's first lane
-            row = pool_row(p, token, (int)(first < p.total ? first : p.total - 1), 0, page_shift, &mine, &at);
-            if (x == 0 && t < tokens) s_row[t] = mine ? row : -2;
+            const int64_t row = pool_row(p, token, (int)(first < p.total ? first : p.total - 1), 0, page_shift, &mine, &at);
+            if (x == 0 && y < tokens) s_row[y] = mine ? row : -2;
             if (!mine) at = 0;
         }
-        if (half > 0 && t < tokens) {
+        if (half > 0 && y < tokens) {
             if (STORE == kPacked || p.f.pos) {
                 int axis = p.f.axis ? p.f.axis[x] : 0;
                 axis = axis < p.f.axes ? axis : p.f.axes - 1;
@@ -75,36 +111,22 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(RopeCall p, int tok, int
     }
     __syncthreads();
 
-    const int lane = threadIdx.x % LPR;
-    const int heads = p.h_q + p.h_kv * (STORE == kPacked ? 1 : 2);
-    const bool paired = !p.f.interleaved;
-    int ra, rb;  // pieces of a rotated row
-    pieces_of(lane, PIECE, p.f.rot, paired, &ra, &rb);
-    const bool turns = lane * E < p.f.rot;
-    int t = 0, h = threadIdx.x / LPR;
-    for (;; h += RPB) {
-        while (h >= heads) {
-            h -= heads;
-            ++t;
-        }
-        if (t >= tokens) break;
+    while (t < tokens) {
         const int64_t token = token0 + t;
-        const bool is_q = h < p.h_q, is_k = !is_q && h < p.h_q + p.h_kv;
+        const int y = t;
+        const bool is_q = h < p.h_q, is_k = !is_q && h < p.h_q + p.h_kv, rotates = is_q || is_k;
         const int head = is_q ? h : is_k ? h - p.h_q : h - p.h_q - p.h_kv;
+        const int a = rotates ? ra : va, b = rotates ? rb : vb;
+        Some<T> xa = na, xb = nb;
+        h += RPB;
+        settle();
+        if (t < tokens) load();
         int64_t row = 0;
         if constexpr (STORE != kPacked) {
-            row = s_row[t];
+            row = s_row[y];
             if (row == -2 || (row < 0 && !is_q)) continue;  // the lanes of a row go together
             row += (int64_t)head << page_shift;
         }
-        const T* from = is_q ? static_cast<const T*>(p.q) + token * p.q_token + head * p.q_head
-                      : is_k ? static_cast<const T*>(p.k) + token * p.k_token + head * p.k_head
-                             : static_cast<const T*>(p.v) + token * p.v_token + head * p.v_head;
-        const bool rotates = is_q || is_k;
-        const int a = rotates ? ra : lane * E, b = rotates ? rb : lane * E + PIECE;
-        Some<T> xa, xb;
-        xa.load(from + a);
-        xb.load(from + b);
         float f[E];
         xa.get(f);
         xb.get(f + PIECE);
@@ -135,27 +157,35 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(RopeCall p, int tok, int
 #pragma unroll
             for (int i = 0; i < E; ++i) f[i] = f[i] * unit * inv * (p.f.weight_bias + w[i]);
         }
-        if (rotates && turns) {
-            const int at = t * half + (paired ? ra : lane * PIECE);
+        if (rotates && paired && a < p.f.rot) {  // PIECE pairs, an element of each in either piece
             float c[PIECE], s[PIECE];
+            const int at = y * half + a;
 #pragma unroll
             for (int i = 0; i < PIECE; i += 4) {
                 *reinterpret_cast<f32x4_t*>(c + i) = *reinterpret_cast<const f32x4_t*>(s_cos + at + i);
                 *reinterpret_cast<f32x4_t*>(s + i) = *reinterpret_cast<const f32x4_t*>(s_sin + at + i);
             }
-            if (paired) {
 #pragma unroll
-                for (int i = 0; i < PIECE; ++i) {
-                    const float x = f[i], y = f[PIECE + i];
-                    f[i] = x * c[i] - y * s[i];
-                    f[PIECE + i] = y * c[i] + x * s[i];
-                }
-            } else {
+            for (int i = 0; i < PIECE; ++i) {
+                const float x = f[i], z = f[PIECE + i];
+                f[i] = x * c[i] - z * s[i];
+                f[PIECE + i] = z * c[i] + x * s[i];
+            }
+        }
+        if (rotates && !paired) {  // PIECE / 2 pairs in each piece
 #pragma unroll
-                for (int i = 0; i < PIECE; ++i) {
-                    const float x = f[2 * i], y = f[2 * i + 1];
-                    f[2 * i] = x * c[i] - y * s[i];
-                    f[2 * i + 1] = y * c[i] + x * s[i];
+            for (int half_row = 0; half_row < 2; ++half_row) {
+                const int from = half_row ? b : a, at = y * half + from / 2;
+                if (from < p.f.rot) {
+#pragma unroll
+                    for (int i = 0; i < PIECE / 2; ++i) {
+                        const float c = s_cos[at + i], s = s_sin[at + i];
+                        float& u = f[half_row * PIECE + 2 * i];
+                        float& z = f[half_row * PIECE + 2 * i + 1];
+                        const float x = u;
+                        u = x * c - z * s;
+                        z = z * c + x * s;
+                    }
                 }
             }
         }
@@ -181,8 +211,15 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(RopeCall p, int tok, int
                                      : static_cast<T*>(is_k ? p.c.k : p.c.v) + row * D;
             xa.set(f);
             xb.set(f + PIECE);
-            *reinterpret_cast<u32x4_t*>(to + a) = xa.x;
-            *reinterpret_cast<u32x4_t*>(to + b) = xb.x;
+            if (rotates ? whole : WHOLE) {
+                asm volatile("" ::: "memory");  // the compiler would make both ways' stores one, of the other kind
+                __builtin_nontemporal_store(xa.x, reinterpret_cast<u32x4_t*>(to + a));
+                __builtin_nontemporal_store(xb.x, reinterpret_cast<u32x4_t*>(to + b));
+                asm volatile("" ::: "memory");
+            } else {
+                *reinterpret_cast<u32x4_t*>(to + a) = xa.x;
+                *reinterpret_cast<u32x4_t*>(to + b) = xb.x;
+            }
         }
     }
 }
@@ -191,9 +228,13 @@ template <typename T, int D, int STORE>
 hipError_t launch_t(const RopeCall& c)
 {
     const int per = c.f.rot > 0 ? c.f.rot / 2 : 1;
-    int64_t tok = c.total / 2048;
-    const int most = kThreads / per < kTokens ? kThreads / per : kTokens;
-    tok = tok < 1 ? 1 : tok > most ? most : tok;
+    constexpr int RPB = kThreads * 2 * Some<T>::E / D;
+    const int64_t heads = c.h_q + (int64_t)c.h_kv * (STORE == kPacked ? 1 : 2);
+    int64_t tok = (4 * RPB + heads - 1) / heads, most = c.total / 2048;
+    if (most > kThreads / per) most = kThreads / per;
+    if (most > kTokens) most = kTokens;
+    tok = tok > most ? most : tok;
+    tok = tok < 1 ? 1 : tok;
     hipLaunchKernelGGL((rope_kernel<T, D, STORE>), grid_of((c.total + tok - 1) / tok), dim3(kThreads), 0, c.stream, c,
                        (int)tok, STORE == kPacked ? 0 : __builtin_ctz((unsigned)c.c.page_size));
     return hipGetLastError();

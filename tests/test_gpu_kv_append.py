@@ -205,7 +205,7 @@ def test_refusals():
     cu, st, f, w = ints([0, 20]), ints([0]), freqs(32).to(DEV), weights(64, BF, 1).to(DEV)
     before = cache.k.clone()
     bad = [dict(k=k[:, :1]), dict(q=k.float()), dict(q=k[:19]), dict(start=st.long()), dict(cu_seqlens=cu[:1]), dict(freq=f.double()),
-           dict(positions=ints([0] * 19)), dict(k_weight=w.float()), dict(q_weight=w), dict(axis=f), dict(freq=None, positions=ints([0] * 20))]
+           dict(positions=ints([0] * 19)), dict(k_weight=w.float()), dict(q_out=k), dict(q_weight=w[:32]), dict(axis=f), dict(freq=None, positions=ints([0] * 20))]
     for over in bad:
         a = dict(k=k, v=k, k_cache=cache.k, v_cache=cache.v, page_table=cache.page_table, start=st, cu_seqlens=cu, freq=f)
         a.update(over)

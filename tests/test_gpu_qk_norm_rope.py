@@ -202,7 +202,7 @@ def test_empty_and_refusals():
     pos, freq, w = torch.zeros(4, dtype=torch.int32, device=DEV), freqs(32).to(DEV), weights(64, BF, 1).to(DEV)
     bad = [dict(positions=None), dict(positions=pos.long()), dict(positions=pos[:3]), dict(freq=freq.double()),
            dict(freq=freq.cpu()), dict(freq=None), dict(axis=pos), dict(q_weight=w.float()), dict(k_weight=w[:32]),
-           dict(q=x.half()), dict(q=x.transpose(1, 2)), dict(k=x[:3]), dict(q_out=x[:, :1]), dict(k=None, k_weight=w)]
+           dict(q=x.half()), dict(q=x.transpose(1, 2)), dict(k=x[:3]), dict(q_out=x[:, :1]), dict(k=None, k_out=x)]
     for over in bad:
         a = dict(q=x, k=x, positions=pos, freq=freq)
         a.update(over)
