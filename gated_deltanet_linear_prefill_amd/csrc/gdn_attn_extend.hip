@@ -2,15 +2,16 @@
 //
 // Rows. The G = h_q / h_kv heads of a KV head read the same keys, so the rows of one (sequence, KV
 // head) are numbered position-major, row r being position r / G, head r % G, and a workgroup takes
-// M = 16 CT of them. Sequence s has the tiles [floor(cu[s] G / M) + s, floor(cu[s + 1] G / M) + s + 1),
-// which are disjoint and enough; a workgroup without a tile leaves.
+// M = 16 CT of them, over a part of the positions that they see (gdn_extend.hpp).
 //
 // Positions. What a tile's rows see together is [0, sinks) and the stretch from the first row's window
 // to the last row. Both are taken in whole 16-position blocks, which never cross a page, and numbered
 // through ("virtual" positions); ranges and steps are of these, so that a window costs its own
 // length and no page outside it is looked at.
 //
-// Bound by the bytes of the cache. A wave takes 32 positions (16 for long rows) of K and V into
+// Bound by the bytes of the cache: one token of each of 64 sequences of up to 8192 positions, d = 128, 32/8
+// heads, runs at 5.2 TB/s with the join (212 us), 16 sequences of 4 tokens at 4.0 (72 us, 4.7 of them the join's), 32
+// behind a window of 4096, d = 256, at 4.1 (59 us). A wave takes 32 positions (16 for long rows) of K and V into
 // registers, for all M rows, with its own softmax state; waves are joined in LDS, ranges by a second
 // kernel through the workspace. 16x16 MFMA, one row per column: S^T = K Q^T takes 16-byte pieces of K
 // rows as its A operand as they were loaded, and its result is the B operand of O^T = V^T P^T, if
@@ -27,6 +28,7 @@ namespace {
 
 constexpr int kWaves = 4;
 constexpr int kRange = 32 * kWaves;  // ranges are multiples of this: a step of every wave
+static_assert(kRange == kStep, "shares are of whole steps");
 
 template <typename T, bool FP8, int D, int CT>
 struct Cfg {
@@ -115,19 +117,15 @@ __global__ void __launch_bounds__(64 * kWaves, (Cfg<T, FP8, D, CT>::PER_SIMD)) e
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 15, g = lane >> 4;
-    // ranges of one index lie together in the grid: late ones, which few tiles have, spread over all XCDs
-    const uint32_t units = (uint32_t)a.slots * (uint32_t)p.c.h_kv;
-    const uint32_t unit = block_index() % units;
-    const int rg = (int)(block_index() / units);
-    if (rg >= a.ranges) return;  // past the grid's end
-    Span t;
-    if (!find_span<M>(a, unit, &t)) return;
+    Part part;
+    if (!find_part<M>(a, block_index(), &part)) return;
+    const Span& t = part.t;
     const int kvh = t.head;
-    const int64_t begin64 = rg * a.range;
-    if (rg > 0 && begin64 >= t.len) return;  // the join does not read this range
-    const bool whole = t.len <= a.range;     // nothing to join
+    const int64_t begin64 = part.rg * part.range;
+    if (part.rg > 0 && begin64 >= t.len) return;  // the join does not read this range
+    const bool whole = t.len <= part.range;       // nothing to join
     const int begin = (int)begin64;
-    const int end = t.len - begin < a.range ? t.len : (int)(begin64 + a.range);
+    const int end = t.len - begin < part.range ? t.len : (int)(begin64 + part.range);
 
     // Q: row r of the tile, rows past the sequence's repeat its last
     const int left = t.rows - t.row0, have = left < M ? left : M;
@@ -508,7 +506,7 @@ __global__ void __launch_bounds__(64 * kWaves, (Cfg<T, FP8, D, CT>::PER_SIMD)) e
                 else *reinterpret_cast<f32x4_t*>(out) = sum;
                 if (p.lse && el == 0) p.lse[to] = le > 0.f ? (top + __builtin_amdgcn_logf(le)) * kLn2 : (le == le ? -INFINITY : le);
             } else {
-                const int64_t to = ((int64_t)unit * a.ranges + rg) * M + tr;
+                const int64_t to = part.at * M + tr;
                 *reinterpret_cast<f32x4_t*>(a.part_o + to * D + el) = sum;
                 if (el == 0) a.part_ml[to] = make_float4(top, ls, le, 0.f);
             }
@@ -540,17 +538,18 @@ __global__ void __launch_bounds__(16 * kJoinGroups) extend_join_kernel(ExtendArg
     const int64_t unit = tr64 / M;
     const int tr = (int)(tr64 - unit * M);
     if (unit >= units) return;  // past the grid's end
-    Span t;
-    if (!find_span<M>(a, (uint32_t)unit, &t)) return;
-    const int kvh = t.head;
-    if (t.len <= a.range || t.row0 + tr >= t.rows) return;  // written by its only range
-    const int used = (int)((t.len + a.range - 1) / a.range);
-    const float4* ml = a.part_ml + (unit * a.ranges) * M + tr;
+    Part part;
+    if (!find_parts<M>(a, (uint32_t)unit, &part)) return;
+    const Span& t = part.t;
+    const int kvh = t.head, used = part.rg;
+    if (t.row0 + tr >= t.rows) return;
+    const int64_t step = part.step * M;
+    const float4* ml = a.part_ml + part.at * M + tr;
     const int y = threadIdx.x / 16, el = (int)(block_index() % (D / 64)) * 64 + threadIdx.x % 16 * 4;
-    const float* po = a.part_o + ((unit * a.ranges) * M + tr) * D + el;
+    const float* po = a.part_o + (part.at * M + tr) * D + el;
 
     float top = -INFINITY;
-    for (int x = threadIdx.x; x < used; x += blockDim.x) top = fmaxf(top, ml[(int64_t)x * M].x);
+    for (int x = threadIdx.x; x < used; x += blockDim.x) top = fmaxf(top, ml[x * step].x);
 #pragma unroll
     for (int off = 32; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, 64));
     if (threadIdx.x % 64 == 0) s_m[threadIdx.x / 64] = top;
@@ -561,12 +560,12 @@ __global__ void __launch_bounds__(16 * kJoinGroups) extend_join_kernel(ExtendArg
     float ls = 0.f, le = 0.f;
 #pragma unroll 4
     for (int x = y; x < used; x += groups) {
-        const float4 v = ml[(int64_t)x * M];
-        const f32x4_t part = *reinterpret_cast<const f32x4_t*>(po + (int64_t)x * M * D);
+        const float4 v = ml[x * step];
+        const f32x4_t sums = *reinterpret_cast<const f32x4_t*>(po + x * step * D);
         const float f = v.x == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(v.x - top);
         ls += v.y * f;
         le += v.z * f;
-        sum += part * f;
+        sum += sums * f;
     }
     s_o[y][threadIdx.x % 16] = sum;
     if (threadIdx.x % 16 == 0) s_l[y] = make_float2(ls, le);
@@ -602,33 +601,43 @@ __global__ void __launch_bounds__(256) extend_join_rows_kernel(ExtendArgs a)
     const uint32_t unit = block_index() / (M / ROWS);
     const int tr = (int)(block_index() % (M / ROWS)) * ROWS + threadIdx.x / LANES, lane = threadIdx.x % LANES;
     if (unit >= (uint32_t)a.slots * (uint32_t)p.c.h_kv) return;  // past the grid's end
-    Span t;
-    if (!find_span<M>(a, unit, &t)) return;
-    const int r = t.row0 + tr;
-    if (t.len <= a.range) return;  // written by its only range
-    const int used = (int)((t.len + a.range - 1) / a.range);
-    const int64_t at = (int64_t)unit * a.ranges * M + tr;
-    const float4 ml = lane < used && r < t.rows ? a.part_ml[at + (int64_t)lane * M] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+    Part part;
+    if (!find_parts<M>(a, unit, &part)) return;
+    const Span& t = part.t;
+    const int r = t.row0 + tr, used = part.rg;
+    const int64_t at = part.at * M + tr, step = part.step * M;
     const float* from = a.part_o + at * D + lane * 4;
-    float top = ml.x;
+    const bool there = r < t.rows;
+    float top = -INFINITY;
+    for (int x = lane; x < used; x += LANES)
+        if (there) top = fmaxf(top, a.part_ml[at + x * step].x);
 #pragma unroll
-    for (int off = kFewRanges / 2; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, LANES));
-    top = __shfl(top, 0, LANES);
-    const float w = ml.x == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(ml.x - top);
-    float l = ml.y * w, e = ml.z * w;
+    for (int off = LANES / 2; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, LANES));
+    float l = 0.f, e = 0.f;
+    f32x4_t o = {0.f, 0.f, 0.f, 0.f};
+    for (int x0 = 0; x0 < used; x0 += kFewRanges) {
+        const int some = used - x0 < kFewRanges ? used - x0 : kFewRanges;
+        if (lane < kFewRanges) {
+            const float4 ml = lane < some && there ? a.part_ml[at + (x0 + lane) * step] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+            const float w = ml.x == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(ml.x - top);
+            l += ml.y * w;
+            e += ml.z * w;
+            s_w[threadIdx.x / LANES][lane] = w;
+        }
+        __syncthreads();
+        if (there)
+#pragma unroll 8
+            for (int x = 0; x < some; ++x)
+                o += *reinterpret_cast<const f32x4_t*>(from + (x0 + x) * step * D) * s_w[threadIdx.x / LANES][x];
+        __syncthreads();
+    }
 #pragma unroll
     for (int off = kFewRanges / 2; off >= 1; off >>= 1) {
         l += __shfl_xor(l, off, LANES);
         e += __shfl_xor(e, off, LANES);
     }
     l = __shfl(l, 0, LANES);
-    if (lane < kFewRanges) s_w[threadIdx.x / LANES][lane] = w;
-    __syncthreads();
-    if (r >= t.rows) return;
-    f32x4_t o = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8
-    for (int x = 0; x < used; ++x)
-        o += *reinterpret_cast<const f32x4_t*>(from + (int64_t)x * M * D) * s_w[threadIdx.x / LANES][x];
+    if (!there) return;
     o *= l > 0.f ? 1.f / l : (l == l ? 0.f : l);
     const int i = (int)((uint32_t)r / (uint32_t)t.g);
     const int64_t to = (t.q0 + i) * p.d.h_q + t.head * t.g + r - i * t.g;
@@ -642,7 +651,7 @@ template <typename T, int D, int M>
 hipError_t launch_join(const ExtendArgs& a)
 {
     const int64_t units = (int64_t)a.slots * a.c.c.h_kv;
-    if (a.ranges <= kFewRanges) {
+    if (a.ranges <= kFewRanges) {  // (or about so many)
         hipLaunchKernelGGL((extend_join_rows_kernel<T, D, M>), grid_of(units * (M * D / 1024)), dim3(256), 0, a.c.stream, a);
         return hipGetLastError();
     }
@@ -679,7 +688,7 @@ template <typename T, bool FP8, int D, int CT>
 hipError_t launch_ct(const ExtendCall& c, const ExtendPlan& pl, void* ws)
 {
     const ExtendArgs a = extend_args(c, pl, ws);
-    hipLaunchKernelGGL((extend_kernel<T, FP8, D, CT>), grid_of(pl.units * pl.ranges), dim3(64 * kWaves), 0, c.stream, a);
+    hipLaunchKernelGGL((extend_kernel<T, FP8, D, CT>), grid_of(pl.workgroups()), dim3(64 * kWaves), 0, c.stream, a);
     const hipError_t e = hipGetLastError();
     return e != hipSuccess || pl.ranges == 1 ? e : launch_extend_join(a, pl.m);
 }
@@ -732,21 +741,30 @@ ExtendPlan stream_plan(const gdn_kv_cache& c, const gdn_extend_dims& d, int64_t 
     const int64_t tiles = (d.total_q * g + p.m - 1) / p.m;
     const int64_t likely = tiles < p.slots ? tiles : p.slots, real = (likely > c.n ? likely : c.n) * c.h_kv;
     const int64_t len = extend_longest(c, d, p.m), steps = len > 0 ? (len + kRange - 1) / kRange : 1;
-    // As many ranges as fill the chip once: `fill` workgroups run at a time, and late ones cost a round. Where the
-    // tiles alone do, ranges of about eight steps, so that late ones fill the CUs that are done. Measured
-    // (us, workgroups 128 / 256 / 512 / 1024): 32 sequences behind a window of 4096, d = 256, 16/2 heads 77 / 58 / 63 / 65; 16 of 4
-    // tokens after up to 8192, d = 128, 32/8 150 / 91 / 75 / 82; 8 of one token 80 / 49 / 42 / 43; 8 of 16 (64 rows) 104 / 64 / 75 / 94;
-    // one token after 32767, d = 256 23 / 21 / 23 / 23. Up to four steps stay together, which spares the
-    // second launch.
-    const int64_t fill = c.d == 256 || p.m == 64 ? 256 : 512;
+    // As many parts as fill the chip once: `fill` workgroups run at a time, and late ones cost a round. Where the
+    // tiles alone do, parts of about eight steps, so that late ones fill the CUs that are done. Measured
+    // (us, workgroups 256 / 512 / 640): 32 sequences behind a window of 4096, d = 256, 16/2 heads 59 / 69 / -; 24 of up to 8000, fp8,
+    // d = 256 45 / 36 / -; 16 of 4 tokens after up to 8192, d = 128, 32/8 83 / 72 / 76; 8 of 16 tokens (64 rows) 57 / 67 / -. Up to
+    // four steps stay together, which spares the second launch.
+    // Up to 64 sequences are divided by their lengths, on the GPU, instead of by max_len (us, by max_len / by
+    // lengths; all drawn up to the bound): 16 of 4 tokens as above 82 / 72, 64 of one token, up to 8192, d = 128, 32/8
+    // heads 234 / 212, 40 of them 160 / 143, 32 behind a window 59 / 59.
+    const int64_t fill = (c.d == 256 && !(c.store == GDN_FP8 && p.m == 16)) || p.m == 64 ? 256 : 512;
     int64_t ranges = real >= fill ? (real * steps / 8 < 4096 ? real * steps / 8 : 4096) / real : fill / real;
     if (ranges > (steps + 1) / 2) ranges = (steps + 1) / 2;
+    if (c.n > 1 && c.n <= 64 && real < fill && steps >= 16 && ranges < 2) ranges = 2;
     if (steps <= 4) ranges = 1;
     if (ranges > 0x7fffffff / p.units) ranges = 0x7fffffff / p.units;  // the grid
     if (ranges < 1) ranges = 1;
     const int64_t per = (steps + ranges - 1) / ranges;
     p.range = per * kRange;
     p.ranges = (steps + per - 1) / per;
+    p.share = 0;
+    p.least = real >= fill ? 8 : 2;
+    // Shares are found by lanes, one a sequence, with sums of 32 bits. One sequence is divided by its bound,
+    // which spares 0.6 us of looking.
+    if (c.n > 1 && c.n <= 64 && p.ranges > 1 && c.n * (d.total_q * g / p.m + 1) * c.h_kv < (1 << 30) / (steps + 1))
+        p.share = real >= fill ? real * (p.ranges + 1) : fill;
     return p;
 }
 

@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(64 * S::WAVES, S::PER_SIMD) extend_tile_kernel
     }
     if (!whole) {  // this range's sums, for the join
         const float l = other_half_sum(st.l), e = ES == 2 && LSE ? other_half_sum(st.exact) : l;
-        const int64_t at = ((int64_t)unit * a.ranges + rg) * M + 32 * rw + (lane & 31);
+        const int64_t at = (int64_t)block_index() * M + 32 * rw + (lane & 31);
         if (r < w.rows) {
             float* to = a.part_o + at * D + 4 * half;
 #pragma unroll
@@ -424,6 +424,7 @@ hipError_t launch_d(const ExtendCall& c, const ExtendPlan& pl, void* ws)
 ExtendPlan extend_tile_plan(const gdn_kv_cache& c, const gdn_extend_dims& d)
 {
     ExtendPlan p;
+    p.share = p.least = 0;
     const int shape = shape_of(c, d);
     p.m = shape == kWide || shape == kCodes ? 256 : 128;
     const int64_t g = d.h_q / c.h_kv;

@@ -7,7 +7,7 @@
 namespace gdn {
 
 // Where the keys of a call's tiles are divided into ranges, sums go to the workspace,
-// [unit][range][row]: o [D] fp32 and (m, l, exact l, -).
+// [workgroup][row]: o [D] fp32 and (m, l, exact l, -).
 struct ExtendPlan {
     int m;          // rows of a tile (0: nothing is launched)
     int per_seq;    // tiles of every sequence, or 0: as many as its rows need, packed
@@ -15,10 +15,13 @@ struct ExtendPlan {
     int64_t units;  // ... of all KV heads
     int64_t range;  // virtual positions of a range
     int64_t ranges;
+    int64_t share;  // workgroups that the call's positions are divided over by their lengths, or 0: by range
+    int least;      // ... with at least so many steps each
     int rows_from, rows_to;  // the sequences that are taken: by their rows (of a KV head)
+    int64_t workgroups() const { return share ? share + units : units * ranges; }
     size_t workspace(const gdn_kv_cache& c) const
     {
-        return m == 0 || ranges == 1 ? 0 : (size_t)(units * ranges * m) * (c.d * sizeof(float) + sizeof(float4));
+        return m == 0 || ranges == 1 ? 0 : (size_t)(workgroups() * m) * (c.d * sizeof(float) + sizeof(float4));
     }
 };
 
@@ -26,9 +29,19 @@ struct ExtendArgs {
     ExtendCall c;
     int64_t range;
     int ranges, slots, per_seq, rows_from, rows_to, page_shift;
+    int share, least, longest;  // longest: virtual positions that a tile may have
     float* part_o;
     float4* part_ml;
 };
+
+// Virtual positions that a tile of m rows may have.
+inline int64_t extend_longest(const gdn_kv_cache& c, const gdn_extend_dims& d, int m)
+{
+    if (d.window == 0) return d.max_len;
+    const int64_t g = d.h_q / c.h_kv;
+    const int64_t w = d.window + (m - 1) / g + 1 + 15 + (d.sinks + 15) / 16 * 16;
+    return w < d.max_len ? w : d.max_len;
+}
 
 inline ExtendArgs extend_args(const ExtendCall& c, const ExtendPlan& p, void* ws)
 {
@@ -41,18 +54,12 @@ inline ExtendArgs extend_args(const ExtendCall& c, const ExtendPlan& p, void* ws
     a.rows_from = p.rows_from;
     a.rows_to = p.rows_to;
     a.page_shift = __builtin_ctz((unsigned)c.c.page_size);
+    a.share = (int)p.share;
+    a.least = p.least;
+    a.longest = (int)extend_longest(c.c, c.d, p.m);
     a.part_o = static_cast<float*>(ws);
-    a.part_ml = reinterpret_cast<float4*>(a.part_o + p.units * p.ranges * p.m * c.c.d);
+    a.part_ml = reinterpret_cast<float4*>(a.part_o + p.workgroups() * p.m * c.c.d);
     return a;
-}
-
-// Virtual positions that a tile of m rows may have.
-inline int64_t extend_longest(const gdn_kv_cache& c, const gdn_extend_dims& d, int m)
-{
-    if (d.window == 0) return d.max_len;
-    const int64_t g = d.h_q / c.h_kv;
-    const int64_t w = d.window + (m - 1) / g + 1 + 15 + (d.sinks + 15) / 16 * 16;
-    return w < d.max_len ? w : d.max_len;
 }
 
 hipError_t launch_extend_join(const ExtendArgs& a, int m);
@@ -83,6 +90,40 @@ constexpr int kExactSeqs = 256;
 __device__ __forceinline__ int rows_of(const ExtendCall& p, int len_q, int g)
 {
     return len_q <= 0 ? 0 : (len_q < p.d.max_q ? len_q : (int)p.d.max_q) * g;
+}
+
+// A sequence's length as the call takes it.
+__device__ __forceinline__ int length_of(const ExtendCall& p, int s)
+{
+    const int len = p.lens[s] < p.d.max_len ? p.lens[s] : (int)p.d.max_len;
+    return len < 0 ? 0 : len;
+}
+
+// Tile `local` of sequence s, which has the rows from qa to qb - 1 and the length len, or false if there is none.
+template <int M>
+__device__ __forceinline__ bool span_at(const ExtendArgs& a, int s, int qa, int qb, int len, int local, Span* t)
+{
+    const ExtendCall& p = a.c;
+    const int g = p.d.h_q / p.c.h_kv;
+    const int len_q = qb - qa;
+    if (len_q <= 0 || local < 0) return false;
+    t->seq = s;
+    t->q0 = qa;
+    t->g = g;
+    t->rows = rows_of(p, len_q, g);
+    if (t->rows < a.rows_from || t->rows > a.rows_to) return false;
+    const int tiles = (t->rows + M - 1) / M;
+    if (local >= tiles) return false;
+    t->row0 = (tiles - 1 - local) * M;  // the last, which see most, first
+    t->shift = len - len_q;
+    t->first = t->shift + t->row0 / g;
+    t->last = t->shift + ((t->row0 + M < t->rows ? t->row0 + M : t->rows) - 1) / g;
+    const int w = (int)p.d.window, lo = w && t->first >= w ? (t->first - w + 1) & ~15 : 0;
+    const int sinks = (int)((p.d.sinks + 15) & ~15);
+    t->sink = sinks < lo ? sinks : lo;
+    t->skip = lo - t->sink;
+    t->len = t->last < 0 ? 0 : t->last + 1 - t->skip;
+    return true;
 }
 
 // A workgroup's tile, or false where there is none. Workgroups without one come last, where the tiles are
@@ -169,28 +210,136 @@ __device__ __forceinline__ bool find_span(const ExtendArgs& a, uint32_t unit, Sp
         qb = p.cu_q ? clamp_to(p.cu_q[s + 1], total) : s + 1;
         local = slot - ((int)((int64_t)qa * g / M) + s);
     }
-    const int len_q = qb - qa;
-    if (len_q <= 0 || local < 0) return false;
-    t->seq = s;
-    t->q0 = qa;
-    t->g = g;
-    t->rows = rows_of(p, len_q, g);
-    if (t->rows < a.rows_from || t->rows > a.rows_to) return false;
-    const int tiles = (t->rows + M - 1) / M;
-    if (local >= tiles) return false;
-    t->row0 = (tiles - 1 - local) * M;  // the last, which see most, first
-    int len = p.lens[s];
-    len = len < p.d.max_len ? len : (int)p.d.max_len;
-    len = len < 0 ? 0 : len;
-    t->shift = len - len_q;
-    t->first = t->shift + t->row0 / g;
-    t->last = t->shift + ((t->row0 + M < t->rows ? t->row0 + M : t->rows) - 1) / g;
-    const int w = (int)p.d.window, lo = w && t->first >= w ? (t->first - w + 1) & ~15 : 0;
-    const int sinks = (int)((p.d.sinks + 15) & ~15);
-    t->sink = sinks < lo ? sinks : lo;
-    t->skip = lo - t->sink;
-    t->len = t->last < 0 ? 0 : t->last + 1 - t->skip;
-    return true;
+    return span_at<M>(a, s, qa, qb, length_of(p, s), local, t);
+}
+
+// What a workgroup takes of a tile: virtual positions [rg * range, rg * range + range). Its sums, where the
+// tile has others, go to part `at` of the workspace; for the join, at is that of range 0, the next lie `step`
+// after one another.
+struct Part {
+    Span t;
+    int64_t range, at, step;
+    int rg;
+};
+
+// A share's least unit: the positions that a workgroup's four waves take in a step.
+constexpr int kStep = 128;
+
+// The call's positions divided over about a.share workgroups by the lengths that the sequences have, one a
+// lane: its tiles, the ranges of each, and the workgroups before its own. Lengths are only known here; ranges
+// of a bound on them are too long for what is shorter, and fill the chip badly (16 sequences of 4 tokens, of up
+// to 8192 positions, 82 us against 72). The last range of a tile is the shortest; in whole steps of the workgroup it would be
+// shorter still, and the same for one XCD in eight (64 us against 59 for 32 sequences behind a window).
+template <int M>
+struct Shares {
+    int qa, qb, len, tiles, steps, ranges, before;  // of the lane's sequence
+
+    // Sums of the lanes up to each.
+    __device__ __forceinline__ static int upto(int x)
+    {
+        x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xf, 0xf, false);  // row_shr:1
+        x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xf, 0xf, false);
+        x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xf, 0xf, false);
+        x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xf, 0xf, false);
+        x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xa, 0xf, false);  // row_bcast:15, :31
+        x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, false);
+        return x;
+    }
+
+    __device__ __forceinline__ explicit Shares(const ExtendArgs& a)
+    {
+        const ExtendCall& p = a.c;
+        const int lane = threadIdx.x & 63, g = p.d.h_q / p.c.h_kv, total = (int)p.d.total_q;
+        qa = qb = len = tiles = steps = 0;
+        if (lane < (int)p.c.n) {
+            qa = clamp_to(p.cu_q ? p.cu_q[lane] : lane, total);
+            qb = clamp_to(p.cu_q ? p.cu_q[lane + 1] : lane + 1, total);
+            len = length_of(p, lane);
+            const int rows = rows_of(p, qb - qa, g);
+            int sight = len - (qb - qa) + (qb - qa < p.d.max_q ? qb - qa : (int)p.d.max_q);  // to the last row's
+            sight = sight < a.longest ? sight : a.longest;
+            tiles = rows <= 0 || rows < a.rows_from || rows > a.rows_to ? 0 : (rows + M - 1) / M;
+            steps = sight <= kStep ? 1 : (sight + kStep - 1) / kStep;
+        }
+        // the share of one: as short as keeps all of them running at once, for what comes late costs a round
+        const int mine = tiles * p.c.h_kv;
+        int per = max((__builtin_amdgcn_readlane(upto(mine * steps), 63) + a.share - 1) / a.share, a.least), sums;
+        for (int x = 0;; ++x, per += (per + 15) / 16) {
+            ranges = (int)((uint32_t)(steps + per - 1) / (uint32_t)per);
+            sums = upto(mine * ranges);
+            if (x == 8 || __builtin_amdgcn_readlane(sums, 63) <= a.share) break;
+        }
+        before = sums - mine * ranges;
+    }
+
+    // Positions of a range of sequence s, whole steps of a wave.
+    __device__ __forceinline__ int64_t range(int s) const
+    {
+        const int n = __builtin_amdgcn_readlane(ranges, s);
+        return (int64_t)(((uint32_t)__builtin_amdgcn_readlane(steps, s) * (kStep / 32) + n - 1) / (uint32_t)n) * 32;
+    }
+
+    __device__ __forceinline__ bool span(const ExtendArgs& a, int s, int local, Span* t) const
+    {
+        return span_at<M>(a, s, __builtin_amdgcn_readlane(qa, s), __builtin_amdgcn_readlane(qb, s),
+                          __builtin_amdgcn_readlane(len, s), local, t);
+    }
+};
+
+// A workgroup's part, or false where there is none.
+template <int M>
+__device__ __forceinline__ bool find_part(const ExtendArgs& a, uint32_t index, Part* x)
+{
+    const ExtendCall& p = a.c;
+    x->at = index;
+    if (!a.share) {
+        // ranges of one index lie together in the grid: late ones, which few tiles have, spread over all XCDs
+        const uint32_t units = (uint32_t)a.slots * (uint32_t)p.c.h_kv, unit = index % units;
+        x->rg = (int)(index / units);
+        x->range = a.range;
+        return x->rg < a.ranges && find_span<M>(a, unit, &x->t);
+    }
+    if (index >= (uint32_t)a.share + (uint32_t)a.slots * (uint32_t)p.c.h_kv) return false;  // past the grid's end
+    const Shares<M> sh(a);
+    const int slot = (int)index;
+    const uint64_t here = __ballot(slot >= sh.before && slot < sh.before + sh.tiles * sh.ranges * p.c.h_kv);
+    if (!here) return false;
+    const int s = __builtin_ctzll(here);
+    const uint32_t tiles = (uint32_t)__builtin_amdgcn_readlane(sh.tiles, s);
+    const uint32_t local = (uint32_t)(slot - __builtin_amdgcn_readlane(sh.before, s)), tile = local / (uint32_t)p.c.h_kv;
+    x->t.head = (int)(local - tile * (uint32_t)p.c.h_kv);
+    x->rg = (int)(tile / tiles);
+    x->range = sh.range(s);
+    return sh.span(a, s, (int)(tile - (uint32_t)x->rg * tiles), &x->t);
+}
+
+// The parts of a unit, a tile of a KV head, or false where it has one or none; rg is their number.
+template <int M>
+__device__ __forceinline__ bool find_parts(const ExtendArgs& a, uint32_t unit, Part* x)
+{
+    const ExtendCall& p = a.c;
+    if (!a.share) {
+        if (!find_span<M>(a, unit, &x->t)) return false;
+        x->at = unit;
+        x->step = (int64_t)a.slots * p.c.h_kv;
+        x->range = a.range;
+    } else {
+        const Shares<M> sh(a);
+        const int slot = (int)(unit / (uint32_t)p.c.h_kv), upto = sh.upto(sh.tiles);
+        const uint64_t here = __ballot(slot >= upto - sh.tiles && slot < upto);
+        if (!here) return false;
+        const int s = __builtin_ctzll(here), tiles = __builtin_amdgcn_readlane(sh.tiles, s);
+        const int local = slot - (__builtin_amdgcn_readlane(upto, s) - tiles);
+        x->t.head = (int)(unit - (uint32_t)slot * (uint32_t)p.c.h_kv);
+        if (!sh.span(a, s, local, &x->t)) return false;
+        x->step = (int64_t)tiles * p.c.h_kv;
+        x->at = (int64_t)__builtin_amdgcn_readlane(sh.before, s) + (int64_t)local * p.c.h_kv + x->t.head;
+        x->range = sh.range(s);
+    }
+    if (x->t.len <= x->range) return false;  // written by its only workgroup
+    x->rg = (int)((x->t.len + x->range - 1) / x->range);
+    // sequences that overlap may ask for more than the grid has, whose sums are not there
+    return !a.share || x->at + (x->rg - 1) * x->step < (int64_t)a.share + (int64_t)a.slots * p.c.h_kv;
 }
 
 }  // namespace

@@ -64,7 +64,7 @@ int main()
     expect("extend: heads", call(), GDN_ERR_SHAPE);
     // sizes over their whole ranges
     for (int64_t pages : {(int64_t)1, (int64_t)500, (int64_t)1 << 17, ((int64_t)1 << 27) - 4097})
-        for (int64_t n : {(int64_t)1, (int64_t)77, (int64_t)1 << 20})
+        for (int64_t n : {(int64_t)1, (int64_t)40, (int64_t)77, (int64_t)1 << 20})
             for (int64_t total : {(int64_t)1, (int64_t)1000, (int64_t)1 << 24, ((int64_t)1 << 30)})
                 for (int64_t max_q : {(int64_t)1, (int64_t)40, huge})
                     for (int64_t window : {(int64_t)0, (int64_t)1, (int64_t)5000, huge})
