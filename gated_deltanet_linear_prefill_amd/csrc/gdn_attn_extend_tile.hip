@@ -7,6 +7,17 @@
 // lane, loaded a unit ahead, and takes a group's from there into the scalar unit, where its address
 // and how many of its bytes exist are formed; the rest of a group reads as zeros.
 //
+// Bound by the matrix units and the softmax between them, which a wave does one after the other and two waves
+// of a SIMD overlap in part: 8192 tokens behind a window of 4096, d = 128, 16/2 heads, 286 us (0.97 PFLOP/s, 48% of the
+// cycles in matrix instructions, with 145 vector instructions to 32 of them in a step); 4096 tokens after
+// 28672, d = 256, 16/2 heads 1.84 ms (1.13 PFLOP/s; 1.81 from a packed copy); 24 sequences of 1 to 700 tokens
+// after up to 4096, 32/8 heads, d = 128, 335 us. Two groups of waves of which one multiplies while the other
+// takes its softmax were slower (406 us of the first): their registers did not fit.
+//
+// fp8 pages are staged as codes, 8 KiB of LDS, and converted to bf16 beside the step that uses the unit
+// before: 512 tokens after 32256, d = 256, 16/2 heads 285 us with 16 of join (converted on their way from
+// global memory by the threads that wait for them: 1067).
+//
 // Ranges. A tile's keys are divided into ranges of a fixed length where the tiles alone would not fill
 // the chip, and joined by the second kernel of gdn_attn_extend.hip.
 #include "gdn_extend.hpp"

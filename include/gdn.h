@@ -1,9 +1,10 @@
 /*
  * gdn.h -- C ABI of libgdn.so: the Gated DeltaNet layer recurrence on AMD Instinct
  * MI355X (gfx950), prefill and batch-1 decode; and, for the softmax-attention layers that a
- * hybrid model runs between those layers, a paged key-value cache (gdn_kv_*) and attention
- * over it and over packed prompts (gdn_attn_*; their own section at the end, with the
- * layouts and limits that differ from those stated here).
+ * hybrid model runs between those layers, a paged key-value cache (gdn_kv_*), attention
+ * over it and over packed prompts (gdn_attn_*), and the norms and rotary positions of their
+ * queries and keys (gdn_qk_norm_rope, gdn_kv_append); two sections of their own at the end,
+ * with the layouts and limits that differ from those stated here.
  *
  * Source of the operation: "Optimizing on-device inference for Apple Silicon"
  * (Perplexity, 2026).
@@ -556,9 +557,11 @@ gdn_status gdn_kv_append(const gdn_kv_cache* cache, const gdn_norm_rope* f, int6
  * divided by them, positions from max_len on are not read, and a sequence's rows from max_q on are
  * not computed (and left as they are in out and lse). Softmax, rounding and NaN as for
  * gdn_attn_prefill and gdn_attn_decode; a key that a row may not see contributes nothing to it,
- * whatever it holds. Keys may be divided into ranges that a second kernel joins, in a fixed order;
- * workspace then has gdn_attn_extend_workspace_bytes(cache, dims) bytes (0 when nothing is divided,
- * and for invalid arguments).
+ * whatever it holds. Keys may be divided into ranges that a second kernel joins, in a fixed order, by
+ * the sizes, the bounds and, for up to 64 sequences of few rows, the batch's lengths: the same call gives
+ * the same bits, and a sequence in another batch the same to the rounding of its sums. workspace then has
+ * gdn_attn_extend_workspace_bytes(cache, dims) bytes (0 when nothing is divided, and for invalid
+ * arguments).
  */
 typedef struct {
     int64_t total_q; /* rows of q, out and lse; total_q * h_q / h_kv below 2^31 - 2^16   */
