@@ -152,3 +152,48 @@ def test_page_ids_past_31_bits_of_rows():
         assert torch.equal(a, b)
     del pool, scale
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("hq,hk,d,page,store,dtype", [(8, 2, 128, 16, BF, BF), (16, 2, 256, 64, F8, BF), (4, 2, 64, 32, BF, BF), (4, 1, 128, 16, F32, F32), (16, 1, 256, 16, BF, BF)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (300, 20)])
+def test_uneven_lengths_and_loose_bounds(hq, hk, d, page, store, dtype, window, sinks):
+    """Few rows of sequences whose lengths are far apart, empty ones and ones without rows among them, under a
+    bound on the lengths that is many times theirs, as a captured graph has it; and some tokens beyond max_q."""
+    lens = [9000, 1, 0, 130, 700, 64, 2500, 17, 5000, 40, 333]
+    lens_q = [2, 1, 1, 0, 5, 3, 4, 1, 1, 6, 2]
+    cache = Cache(lens, page, hk, d, store, seed=2, extra_width=1 + 40000 // page)
+    fill(cache, 2, nan_behind=lens)
+    q = queries(sum(lens_q), hq, d, dtype)
+    for max_len in (None, 9000):
+        for most in (6, 4):
+            lse = torch.full(q.shape[:2], 7.0, device=DEV)
+            out = torch.full(q.shape, 7.0, dtype=dtype, device=DEV)
+            gdn.gdn_attn_extend(q.to(DEV), *cache.args(), ints(lens), ints(offsets(lens_q)), window=window, sinks=sinks, max_q=most,
+                                max_len=max_len, out=out, lse=lse, **cache.scales())
+            at = 0
+            for s, (m, length) in enumerate(zip(lens_q, lens)):
+                done = min(m, most)
+                assert bool((out[at + done:at + m] == 7.0).all()) and bool((lse[at + done:at + m] == 7.0).all())
+                k, v, there = dense(cache, s, length)
+                allowed = (sight(m, length, window, sinks) & there[None])[:done]
+                for h in range(hq if done else 0):
+                    ref = attn_ref.attend(q[at:at + done, h], k[:, h * hk // hq], v[:, h * hk // hq], d ** -0.5, allowed)
+                    attn_ref.check(out[at:at + done, h], lse[at:at + done, h], *ref, what=f"sequence {s} head {h}")
+                at += m
+
+
+def test_offsets_that_go_back():
+    """Offsets that decrease or lie past the tokens give their sequences no rows or fewer; the others are right."""
+    lens = [3000, 200, 900, 50]
+    cache = Cache(lens, 16, 2, 128, BF)
+    fill(cache, 3)
+    q = queries(12, 8, 128, BF)
+    out = gdn.gdn_attn_extend(q.to(DEV), *cache.args(), ints(lens), ints([0, 4, 2, 9, 4000]), max_q=8)
+    compare(cache, q, [2], [2998], out[:2], None, 128 ** -0.5)  # rows 2 and 3 are two sequences'
+    k, v, _ = dense(cache, 2, 900)
+    allowed = sight(7, 900, 0, 0)[2:]
+    for h in range(8):
+        attn_ref.check(out[4:9, h], None, *attn_ref.attend(q[4:9, h], k[:, h // 4], v[:, h // 4], 128 ** -0.5, allowed), what=f"head {h}")
+    k, v, _ = dense(cache, 3, 50)
+    for h in range(8):
+        attn_ref.check(out[9:, h], None, *attn_ref.attend(q[9:, h], k[:, h // 4], v[:, h // 4], 128 ** -0.5, sight(3, 50, 0, 0)), what=f"head {h}")
