@@ -126,6 +126,28 @@ __device__ __forceinline__ bool span_at(const ExtendArgs& a, int s, int qa, int 
     return true;
 }
 
+// Workgroup i of a sequence's takes tile *tile of its `pairs` (range, head): the tiles of a pair, which read the
+// same keys, at the same time and on one XCD, whose L2 they share (workgroups i and i + 8).
+// 8 tokens after 32760, d = 256, 16/2 heads (two tiles) 37 us without and 33 with it; tiles of many rows, which read
+// slower, are as fast either way.
+__device__ __forceinline__ uint32_t pair_of(uint32_t i, uint32_t pairs, uint32_t tiles, uint32_t* tile)
+{
+    const uint32_t eight = i / (8 * tiles), rest = i - eight * 8 * tiles, left = pairs - 8 * eight;
+    const uint32_t row = left < 8 ? left : 8;
+    *tile = rest / row;
+    return 8 * eight + rest - *tile * row;
+}
+
+// One sequence's workgroups in that order: the number [range][tile][head] of workgroup `index`.
+__device__ __forceinline__ uint32_t together(const ExtendArgs& a, uint32_t index)
+{
+    const uint32_t h = (uint32_t)a.c.c.h_kv;
+    if (a.c.c.n > 1 || a.slots == 1 || a.ranges == 1) return index;
+    uint32_t tile;
+    const uint32_t pair = pair_of(index, h * (uint32_t)a.ranges, (uint32_t)a.slots, &tile), rg = pair / h;
+    return (rg * (uint32_t)a.slots + tile) * h + (pair - rg * h);
+}
+
 // A workgroup's tile, or false where there is none. Workgroups without one come last, where the tiles are
 // counted: in between they cost more than they seem to (one in nine of them made a call of 256
 // others, one a CU, take two rounds: 260 us instead of 155).
@@ -294,10 +316,14 @@ __device__ __forceinline__ bool find_part(const ExtendArgs& a, uint32_t index, P
     x->at = index;
     if (!a.share) {
         // ranges of one index lie together in the grid: late ones, which few tiles have, spread over all XCDs
-        const uint32_t units = (uint32_t)a.slots * (uint32_t)p.c.h_kv, unit = index % units;
+        const uint32_t units = (uint32_t)a.slots * (uint32_t)p.c.h_kv;
+        if (index >= units * (uint64_t)a.ranges) return false;  // past the grid's end
+        index = together(a, index);
+        x->at = index;
+        const uint32_t unit = index % units;
         x->rg = (int)(index / units);
         x->range = a.range;
-        return x->rg < a.ranges && find_span<M>(a, unit, &x->t);
+        return find_span<M>(a, unit, &x->t);
     }
     if (index >= (uint32_t)a.share + (uint32_t)a.slots * (uint32_t)p.c.h_kv) return false;  // past the grid's end
     const Shares<M> sh(a);
@@ -306,11 +332,14 @@ __device__ __forceinline__ bool find_part(const ExtendArgs& a, uint32_t index, P
     if (!here) return false;
     const int s = __builtin_ctzll(here);
     const uint32_t tiles = (uint32_t)__builtin_amdgcn_readlane(sh.tiles, s);
-    const uint32_t local = (uint32_t)(slot - __builtin_amdgcn_readlane(sh.before, s)), tile = local / (uint32_t)p.c.h_kv;
-    x->t.head = (int)(local - tile * (uint32_t)p.c.h_kv);
-    x->rg = (int)(tile / tiles);
+    const uint32_t before = (uint32_t)__builtin_amdgcn_readlane(sh.before, s), h = (uint32_t)p.c.h_kv;
+    uint32_t tile;
+    const uint32_t pair = pair_of(index - before, h * (uint32_t)__builtin_amdgcn_readlane(sh.ranges, s), tiles, &tile), rg = pair / h;
+    x->rg = (int)rg;
+    x->t.head = (int)(pair - rg * h);
+    x->at = before + (rg * tiles + tile) * h + (pair - rg * h);
     x->range = sh.range(s);
-    return sh.span(a, s, (int)(tile - (uint32_t)x->rg * tiles), &x->t);
+    return sh.span(a, s, (int)tile, &x->t);
 }
 
 // The parts of a unit, a tile of a KV head, or false where it has one or none; rg is their number.
