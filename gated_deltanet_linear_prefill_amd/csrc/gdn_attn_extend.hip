@@ -731,7 +731,21 @@ ExtendPlan stream_plan(const gdn_kv_cache& c, const gdn_extend_dims& d, int64_t 
 {
     ExtendPlan p;
     const int64_t g = d.h_q / c.h_kv, most = d.max_q * g, rows = most < to ? most : to;
-    p.m = rows <= 16 ? 16 : rows <= 32 || c.d == 256 ? 32 : 64;
+    // Rows of a tile. Larger ones read the keys less often, but take up to 512 registers, with one wave a SIMD, whose
+    // every step waits for its loads; tiles of 16 rows have two, and the ones of a sequence share what they
+    // read in an L2 (pair_of). These win while what they ask for, the keys of every tile, stays below some 200 MB, and for
+    // fp8 pages with d = 256, whose larger tiles copy O between registers. Measured (us, 16 / larger; MB): d = 256, 16/2 heads
+    // 8 tokens after 4000 (33) 18 / 23, 16000 (134) 25 / 27, 32760 (268) 36 / 34, 8 sequences of 8 after up to 8192
+    // (537) 43 / 37, 32 of 4 (1074) 110 / 74; fp8 8 after 32760 (134) 29 / 32, 32 of 4 to 8 (537) 72 / 81, 64 of 8 after up to 16000
+    // (2100) 296 / 352; d = 128, 32/8 heads 16 after 4000, fp8 (34) 18 / 25, 4 sequences of 16 after 1000 (67) 18 / 25, 8 of 8 after
+    // up to 8192 (537) 46 / 41, 16 of 8, fp8 (537) 75 / 53; d = 64 8 of 16 after 2000 (67) 17 / 21; fp32, d = 256 8 after 4000 (67) 29 / 41.
+    const int64_t each16 = (rows + 15) / 16, sparse = d.total_q * g / 16 + c.n;
+    const int64_t tiles16 = (each16 <= sparse / c.n ? c.n * each16 : sparse) * c.h_kv;
+    const int64_t step_bytes = (int64_t)kRange * 2 * c.d * (c.store == GDN_FP8 ? 1 : c.store == GDN_F32 ? 4 : 2);
+    const int64_t steps16 = (extend_longest(c, d, 16) + kRange - 1) / kRange;
+    const bool narrow = rows <= 64 && c.n <= 64 && (tiles16 * steps16 <= (INT64_C(192) << 20) / step_bytes ||
+                                                    (c.d == 256 && c.store == GDN_FP8 && d.dtype == GDN_BF16));
+    p.m = rows <= 16 || narrow ? 16 : rows <= 32 || c.d == 256 ? 32 : 64;
     const int64_t packed = d.total_q * g / p.m + c.n, each = (rows + p.m - 1) / p.m;
     p.per_seq = each <= packed / c.n ? (int)each : 0;
     p.slots = p.per_seq ? c.n * each : packed;

@@ -197,3 +197,34 @@ def test_offsets_that_go_back():
     k, v, _ = dense(cache, 3, 50)
     for h in range(8):
         attn_ref.check(out[9:, h], None, *attn_ref.attend(q[9:, h], k[:, h // 4], v[:, h // 4], 128 ** -0.5, sight(3, 50, 0, 0)), what=f"head {h}")
+
+
+@pytest.mark.parametrize("dtype,store", [(BF, BF), (BF, F8), (F32, F32), (F32, F8)])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("lens_q,lens,hq,hk", [([7], [900], 4, 1), ([3, 5, 0, 6], [700, 5, 40, 1500], 8, 2), ([16, 9], [600, 130], 8, 2), ([13, 1, 16], [13, 900, 17], 4, 1)])
+def test_larger_tiles_of_few_rows(lens_q, lens, hq, hk, d, dtype, store):
+    """17 to 64 rows of a KV head under bounds that ask for much reading: tiles of 32 and 64 rows, whole and in part,
+    with and without a window; under tight bounds the tiles are of 16 rows."""
+    cache = Cache(lens, 16, hk, d, store, seed=4, extra_width=200000)
+    fill(cache, 4, nan_behind=None)
+    q = queries(sum(lens_q), hq, d, dtype)
+    for window, sinks in ((0, 0), (1000000, 3)):
+        lse = torch.zeros(q.shape[:2], device=DEV)
+        for max_len in (None, max(lens)):
+            out = gdn.gdn_attn_extend(q.to(DEV), *cache.args(), ints(lens), ints(offsets(lens_q)), max_q=max(lens_q), max_len=max_len, window=window,
+                                      sinks=sinks, lse=lse, **cache.scales())
+            compare(cache, q, lens_q, lens, out, lse, d ** -0.5, window, sinks)
+
+
+@pytest.mark.parametrize("window,sinks", [(0, 0), (90, 4)])
+def test_more_sequences_than_lanes_with_drafts(window, sinks):
+    """fp8 pages with d = 256 and 70 sequences: tiles of 32 rows, in slots that are not divided by lengths."""
+    rng = random.Random(5)
+    lens_q = [rng.choice((0, 1, 3, 5, 8)) for _ in range(70)]
+    lens = [rng.choice((0, 1, 40, 300)) + m for m in lens_q]
+    cache = Cache(lens, 16, 1, 256, F8, seed=4)
+    fill(cache, 4, nan_behind=lens)
+    q = queries(sum(lens_q), 6, 256, BF)
+    lse = torch.zeros(q.shape[:2], device=DEV)
+    out = gdn.gdn_attn_extend(q.to(DEV), *cache.args(), ints(lens), ints(offsets(lens_q)), max_q=8, window=window, sinks=sinks, lse=lse, **cache.scales())
+    compare(cache, q, lens_q, lens, out, lse, 256 ** -0.5, window, sinks)
