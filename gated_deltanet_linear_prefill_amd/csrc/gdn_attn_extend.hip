@@ -723,28 +723,41 @@ hipError_t launch_d(const ExtendCall& c, const ExtendPlan& pl, void* ws)
 }
 
 // Rows of a KV head up to which a sequence is taken by the kernel of this file; longer ones by the tiles of
-// gdn_attn_extend_tile.hip.
+// gdn_attn_extend_tile.hip, where the call is not small (narrow_tiles).
 constexpr int kStreamRows = 64;
+
+// Whether tiles are of 16 rows. Larger ones read the keys less often, but the ones of extend_kernel take up to 512
+// registers, with one wave a SIMD whose every step waits for its loads, and the ones of gdn_attn_extend_tile.hip start and
+// end slowly (15 to 20 us); tiles of 16 rows have two waves a SIMD, and the ones of a sequence share what they read in
+// an L2 (pair_of). They win while what they ask for, the keys of every tile, stays below some 200 MB (fp32, whose tiles of
+// many rows are slowest: 512), in up to 768 tiles, and for fp8 pages with d = 256, up to 64 rows. Measured
+// (us, 16 / larger; MB). Up to 64 rows: d = 256, 16/2 heads 8 tokens after 4000 (33) 18 / 23, 16000 (134) 25 / 27, 32760 (268) 36 / 34,
+// 8 sequences of 8 after up to 8192 (537) 43 / 37, 32 of 4 (1074) 110 / 74; fp8 8 after 32760 (134) 29 / 32, 32 of 4 to 8
+// (537) 72 / 81, 64 of 8 after up to 16000 (2100) 296 / 352; d = 128, 32/8 heads 16 after 4000, fp8 (34) 18 / 25, 8 of 8 after up to
+// 8192 (537) 46 / 41, 16 of 8, fp8 (537) 75 / 53; fp32, d = 256 8 after 4000 (67) 29 / 41, 8 of 4 after up to 8192 (537) 60 / 62. More rows:
+// d = 256 16 after 4000 (67) 20 / 40, 128 after 1000 (151) 26 / 40, 256 after 1000 (336) 35 / 43, fp8 64 after 2000 (71) 24 / 66, 512 from the
+// start (134) 18 / 43; d = 128 32 after 2000 (71) 18 / 25, 256 after 1000 (168) 30 / 30, 512 from the start (268) 22 / 18, 4 sequences of 20 to 200
+// after up to 500 28 / 20, 16 of 60 from the start (126, 1920 tiles) 21 / 17, d = 256
+// 64 of 10 to 20 after up to 100 (134, about 1000) 34 / 25; d = 64 16/16 heads 512 from the start (67) 11 / 14; fp32, d =
+// 256 128 after 1000 (302) 50 / 225, d = 128, 8/2 heads 64 after 4000 (138) 28 / 110.
+bool narrow_tiles(const gdn_kv_cache& c, const gdn_extend_dims& d, int64_t rows)
+{
+    const int64_t g = d.h_q / c.h_kv, each = (rows + 15) / 16, sparse = d.total_q * g / 16 + c.n;
+    const int64_t tiles = (each <= sparse / c.n ? c.n * each : sparse) * c.h_kv;
+    const int64_t step_bytes = (int64_t)kRange * 2 * c.d * (c.store == GDN_FP8 ? 1 : c.store == GDN_F32 ? 4 : 2);
+    const int64_t steps = (extend_longest(c, d, 16) + kRange - 1) / kRange;
+    if (c.n > 64) return false;  // whose tiles of a sequence lie apart
+    if (rows <= 64 && c.d == 256 && c.store == GDN_FP8 && d.dtype == GDN_BF16) return true;
+    const int64_t most = c.store == GDN_F32 ? 512 : 192;
+    return tiles <= 768 && tiles * steps <= (most << 20) / step_bytes;
+}
 
 // How the sequences of up to `to` rows are taken.
 ExtendPlan stream_plan(const gdn_kv_cache& c, const gdn_extend_dims& d, int64_t to)
 {
     ExtendPlan p;
     const int64_t g = d.h_q / c.h_kv, most = d.max_q * g, rows = most < to ? most : to;
-    // Rows of a tile. Larger ones read the keys less often, but take up to 512 registers, with one wave a SIMD, whose
-    // every step waits for its loads; tiles of 16 rows have two, and the ones of a sequence share what they
-    // read in an L2 (pair_of). These win while what they ask for, the keys of every tile, stays below some 200 MB, and for
-    // fp8 pages with d = 256, whose larger tiles copy O between registers. Measured (us, 16 / larger; MB): d = 256, 16/2 heads
-    // 8 tokens after 4000 (33) 18 / 23, 16000 (134) 25 / 27, 32760 (268) 36 / 34, 8 sequences of 8 after up to 8192
-    // (537) 43 / 37, 32 of 4 (1074) 110 / 74; fp8 8 after 32760 (134) 29 / 32, 32 of 4 to 8 (537) 72 / 81, 64 of 8 after up to 16000
-    // (2100) 296 / 352; d = 128, 32/8 heads 16 after 4000, fp8 (34) 18 / 25, 4 sequences of 16 after 1000 (67) 18 / 25, 8 of 8 after
-    // up to 8192 (537) 46 / 41, 16 of 8, fp8 (537) 75 / 53; d = 64 8 of 16 after 2000 (67) 17 / 21; fp32, d = 256 8 after 4000 (67) 29 / 41.
-    const int64_t each16 = (rows + 15) / 16, sparse = d.total_q * g / 16 + c.n;
-    const int64_t tiles16 = (each16 <= sparse / c.n ? c.n * each16 : sparse) * c.h_kv;
-    const int64_t step_bytes = (int64_t)kRange * 2 * c.d * (c.store == GDN_FP8 ? 1 : c.store == GDN_F32 ? 4 : 2);
-    const int64_t steps16 = (extend_longest(c, d, 16) + kRange - 1) / kRange;
-    const bool narrow = rows <= 64 && c.n <= 64 && (tiles16 * steps16 <= (INT64_C(192) << 20) / step_bytes ||
-                                                    (c.d == 256 && c.store == GDN_FP8 && d.dtype == GDN_BF16));
+    const bool narrow = narrow_tiles(c, d, rows);
     p.m = rows <= 16 || narrow ? 16 : rows <= 32 || c.d == 256 ? 32 : 64;
     const int64_t packed = d.total_q * g / p.m + c.n, each = (rows + p.m - 1) / p.m;
     p.per_seq = each <= packed / c.n ? (int)each : 0;
@@ -794,7 +807,7 @@ struct Plans {
 Plans make_plans(const gdn_kv_cache& c, const gdn_extend_dims& d)
 {
     const int64_t most = d.max_q * (d.h_q / c.h_kv);
-    const bool only_stream = most <= kStreamRows || (d.dtype == GDN_F32 && c.store == GDN_FP8);
+    const bool only_stream = most <= kStreamRows || narrow_tiles(c, d, most) || (d.dtype == GDN_F32 && c.store == GDN_FP8);
     const bool both = !only_stream && c.n > 1 && c.store != GDN_BF16;
     Plans p;
     p.stream.m = p.tiles.m = 0;

@@ -13,6 +13,25 @@ from test_gpu_kv_cache import BF, DEV, F8, F32, Cache, ints, offsets
 pytestmark = pytest.mark.gpu
 
 
+@pytest.fixture(autouse=True, params=["as they are", "among empty sequences"])
+def batch(request, monkeypatch):
+    """Every test twice: small calls take tiles of 16 rows, the same sequences among 70 empty ones larger tiles."""
+    if request.param == "as they are":
+        return
+    plain = gdn.gdn_attn_extend
+
+    def call(q, k_cache, v_cache, page_table, lens, cu_q=None, **kw):
+        tensors = all(isinstance(x, torch.Tensor) and x.is_cuda and x.dtype == torch.int32 for x in (page_table, lens, cu_q))
+        if tensors and "workspace" not in kw and kw.get("max_q") != 1:
+            with torch.cuda.stream(kw.get("stream")):
+                page_table = torch.cat([page_table, page_table.new_full((70, page_table.shape[1]), -1)])
+                lens = torch.cat([lens, lens.new_zeros(70)])
+                cu_q = torch.cat([cu_q, cu_q[-1:].expand(70)])
+        return plain(q, k_cache, v_cache, page_table, lens, cu_q, **kw)
+
+    monkeypatch.setattr(gdn, "gdn_attn_extend", call)
+
+
 def queries(total, hq, d, dtype, seed=1):
     return (1.5 * torch.randn(total, hq, d, generator=torch.Generator().manual_seed(seed))).to(dtype)
 

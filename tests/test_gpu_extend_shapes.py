@@ -9,7 +9,7 @@ import torch
 import attn_ref
 import gated_deltanet_linear_prefill_amd as gdn
 from test_gpu_attn_decode import dense, fill
-from test_gpu_attn_extend import compare, queries, sight
+from test_gpu_attn_extend import batch, compare, queries, sight  # noqa: F401
 from test_gpu_kv_cache import BF, DEV, F8, F32, Cache, ints, offsets
 
 pytestmark = pytest.mark.gpu
