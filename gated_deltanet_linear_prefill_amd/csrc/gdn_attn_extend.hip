@@ -729,8 +729,8 @@ constexpr int kStreamRows = 64;
 // Whether tiles are of 16 rows. Larger ones read the keys less often, but the ones of extend_kernel take up to 512
 // registers, with one wave a SIMD whose every step waits for its loads, and the ones of gdn_attn_extend_tile.hip start and
 // end slowly (15 to 20 us); tiles of 16 rows have two waves a SIMD, and the ones of a sequence share what they read in
-// an L2 (pair_of). They win while what they ask for, the keys of every tile, stays below some 200 MB (fp32, whose tiles of
-// many rows are slowest: 512), in up to 768 tiles, and for fp8 pages with d = 256, up to 64 rows. Measured
+// an L2 (pair_of). They win while what they ask for, the keys of every tile, stays below some 200 MB (fp32: 512, and
+// 2048 of more than 64 rows, whose tiles are slowest), in up to 768 tiles, and for fp8 pages with d = 256, up to 64 rows. Measured
 // (us, 16 / larger; MB). Up to 64 rows: d = 256, 16/2 heads 8 tokens after 4000 (33) 18 / 23, 16000 (134) 25 / 27, 32760 (268) 36 / 34,
 // 8 sequences of 8 after up to 8192 (537) 43 / 37, 32 of 4 (1074) 110 / 74; fp8 8 after 32760 (134) 29 / 32, 32 of 4 to 8
 // (537) 72 / 81, 64 of 8 after up to 16000 (2100) 296 / 352; d = 128, 32/8 heads 16 after 4000, fp8 (34) 18 / 25, 8 of 8 after up to
@@ -739,7 +739,8 @@ constexpr int kStreamRows = 64;
 // start (134) 18 / 43; d = 128 32 after 2000 (71) 18 / 25, 256 after 1000 (168) 30 / 30, 512 from the start (268) 22 / 18, 4 sequences of 20 to 200
 // after up to 500 28 / 20, 16 of 60 from the start (126, 1920 tiles) 21 / 17, d = 256
 // 64 of 10 to 20 after up to 100 (134, about 1000) 34 / 25; d = 64 16/16 heads 512 from the start (67) 11 / 14; fp32, d =
-// 256 128 after 1000 (302) 50 / 225, d = 128, 8/2 heads 64 after 4000 (138) 28 / 110.
+// 256 128 after 1000 (302) 50 / 225, 4000 (1110) 125 / 228, d = 128, 8/2 heads 64 after 4000 (138) 28 / 110, 16/2 heads 256 after 3000
+// (1680) 93 / 114.
 bool narrow_tiles(const gdn_kv_cache& c, const gdn_extend_dims& d, int64_t rows)
 {
     const int64_t g = d.h_q / c.h_kv, each = (rows + 15) / 16, sparse = d.total_q * g / 16 + c.n;
@@ -748,7 +749,7 @@ bool narrow_tiles(const gdn_kv_cache& c, const gdn_extend_dims& d, int64_t rows)
     const int64_t steps = (extend_longest(c, d, 16) + kRange - 1) / kRange;
     if (c.n > 64) return false;  // whose tiles of a sequence lie apart
     if (rows <= 64 && c.d == 256 && c.store == GDN_FP8 && d.dtype == GDN_BF16) return true;
-    const int64_t most = c.store == GDN_F32 ? 512 : 192;
+    const int64_t most = c.store != GDN_F32 ? 192 : rows <= 64 ? 512 : 2048;
     return tiles <= 768 && tiles * steps <= (most << 20) / step_bytes;
 }
 
