@@ -130,12 +130,36 @@ __device__ __forceinline__ bool span_at(const ExtendArgs& a, int s, int qa, int 
 // same keys, at the same time and on one XCD, whose L2 they share (workgroups i and i + 8).
 // 8 tokens after 32760, d = 256, 16/2 heads (two tiles) 37 us without and 33 with it; tiles of many rows, which read
 // slower, are as fast either way.
-__device__ __forceinline__ uint32_t pair_of(uint32_t i, uint32_t pairs, uint32_t tiles, uint32_t* tile)
+__host__ __device__ __forceinline__ uint32_t pair_of(uint32_t i, uint32_t pairs, uint32_t tiles, uint32_t* tile)
 {
     const uint32_t eight = i / (8 * tiles), rest = i - eight * 8 * tiles, left = pairs - 8 * eight;
     const uint32_t row = left < 8 ? left : 8;
     *tile = rest / row;
     return 8 * eight + rest - *tile * row;
+}
+
+// The part that workgroup `index` of a call divided by lengths takes. A sequence's parts are a block from `before` on, one for
+// each range of its tiles of h heads. The grid and the workspace hold it as a whole or not at all: sequences that
+// overlap (offsets that go back) may ask for more than the `parts` that there are, and that order would send
+// workgroups at the grid's end past it.
+struct SharePart {
+    uint32_t tile, rg, head, at;  // at: its place in the workspace
+};
+
+__host__ __device__ __forceinline__ bool block_fits(uint32_t before, uint32_t tiles, uint32_t ranges, uint32_t h, uint32_t parts)
+{
+    return before + (uint64_t)tiles * ranges * h <= parts;
+}
+
+__host__ __device__ __forceinline__ bool share_part(uint32_t index, uint32_t before, uint32_t tiles, uint32_t ranges, uint32_t h,
+                                                    uint32_t parts, SharePart* x)
+{
+    if (!block_fits(before, tiles, ranges, h, parts)) return false;
+    const uint32_t pair = pair_of(index - before, h * ranges, tiles, &x->tile);
+    x->rg = pair / h;
+    x->head = pair - x->rg * h;
+    x->at = before + (x->rg * tiles + x->tile) * h + x->head;
+    return true;
 }
 
 // One sequence's workgroups in that order: the number [range][tile][head] of workgroup `index`.
@@ -325,21 +349,22 @@ __device__ __forceinline__ bool find_part(const ExtendArgs& a, uint32_t index, P
         x->range = a.range;
         return find_span<M>(a, unit, &x->t);
     }
-    if (index >= (uint32_t)a.share + (uint32_t)a.slots * (uint32_t)p.c.h_kv) return false;  // past the grid's end
+    const uint32_t h = (uint32_t)p.c.h_kv, parts = (uint32_t)a.share + (uint32_t)a.slots * h;
+    if (index >= parts) return false;  // past the grid's end
     const Shares<M> sh(a);
     const int slot = (int)index;
     const uint64_t here = __ballot(slot >= sh.before && slot < sh.before + sh.tiles * sh.ranges * p.c.h_kv);
     if (!here) return false;
     const int s = __builtin_ctzll(here);
-    const uint32_t tiles = (uint32_t)__builtin_amdgcn_readlane(sh.tiles, s);
-    const uint32_t before = (uint32_t)__builtin_amdgcn_readlane(sh.before, s), h = (uint32_t)p.c.h_kv;
-    uint32_t tile;
-    const uint32_t pair = pair_of(index - before, h * (uint32_t)__builtin_amdgcn_readlane(sh.ranges, s), tiles, &tile), rg = pair / h;
-    x->rg = (int)rg;
-    x->t.head = (int)(pair - rg * h);
-    x->at = before + (rg * tiles + tile) * h + (pair - rg * h);
+    SharePart w;
+    if (!share_part(index, (uint32_t)__builtin_amdgcn_readlane(sh.before, s), (uint32_t)__builtin_amdgcn_readlane(sh.tiles, s),
+                    (uint32_t)__builtin_amdgcn_readlane(sh.ranges, s), h, parts, &w))
+        return false;
+    x->rg = (int)w.rg;
+    x->t.head = (int)w.head;
+    x->at = w.at;
     x->range = sh.range(s);
-    return sh.span(a, s, (int)tile, &x->t);
+    return sh.span(a, s, (int)w.tile, &x->t);
 }
 
 // The parts of a unit, a tile of a KV head, or false where it has one or none; rg is their number.
@@ -361,14 +386,17 @@ __device__ __forceinline__ bool find_parts(const ExtendArgs& a, uint32_t unit, P
         const int local = slot - (__builtin_amdgcn_readlane(upto, s) - tiles);
         x->t.head = (int)(unit - (uint32_t)slot * (uint32_t)p.c.h_kv);
         if (!sh.span(a, s, local, &x->t)) return false;
+        const int before = __builtin_amdgcn_readlane(sh.before, s);
+        if (!block_fits((uint32_t)before, (uint32_t)tiles, (uint32_t)__builtin_amdgcn_readlane(sh.ranges, s), (uint32_t)p.c.h_kv,
+                        (uint32_t)a.share + (uint32_t)a.slots * (uint32_t)p.c.h_kv))
+            return false;  // nobody wrote its sums
         x->step = (int64_t)tiles * p.c.h_kv;
-        x->at = (int64_t)__builtin_amdgcn_readlane(sh.before, s) + (int64_t)local * p.c.h_kv + x->t.head;
+        x->at = (int64_t)before + (int64_t)local * p.c.h_kv + x->t.head;
         x->range = sh.range(s);
     }
     if (x->t.len <= x->range) return false;  // written by its only workgroup
     x->rg = (int)((x->t.len + x->range - 1) / x->range);
-    // sequences that overlap may ask for more than the grid has, whose sums are not there
-    return !a.share || x->at + (x->rg - 1) * x->step < (int64_t)a.share + (int64_t)a.slots * p.c.h_kv;
+    return true;
 }
 
 }  // namespace
