@@ -506,7 +506,7 @@ __global__ void __launch_bounds__(64 * kWaves, (Cfg<T, FP8, D, CT>::PER_SIMD)) e
                 else *reinterpret_cast<f32x4_t*>(out) = sum;
                 if (p.lse && el == 0) p.lse[to] = le > 0.f ? (top + __builtin_amdgcn_logf(le)) * kLn2 : (le == le ? -INFINITY : le);
             } else {
-                const int64_t to = part.at * M + tr;
+                const int64_t to = part.at + tr;
                 *reinterpret_cast<f32x4_t*>(a.part_o + to * D + el) = sum;
                 if (el == 0) a.part_ml[to] = make_float4(top, ls, le, 0.f);
             }
@@ -543,10 +543,10 @@ __global__ void __launch_bounds__(16 * kJoinGroups) extend_join_kernel(ExtendArg
     const Span& t = part.t;
     const int kvh = t.head, used = part.rg;
     if (t.row0 + tr >= t.rows) return;
-    const int64_t step = part.step * M;
-    const float4* ml = a.part_ml + part.at * M + tr;
+    const int64_t step = part.step;
+    const float4* ml = a.part_ml + part.at + tr;
     const int y = threadIdx.x / 16, el = (int)(block_index() % (D / 64)) * 64 + threadIdx.x % 16 * 4;
-    const float* po = a.part_o + (part.at * M + tr) * D + el;
+    const float* po = a.part_o + (part.at + tr) * D + el;
 
     float top = -INFINITY;
     for (int x = threadIdx.x; x < used; x += blockDim.x) top = fmaxf(top, ml[x * step].x);
@@ -605,7 +605,7 @@ __global__ void __launch_bounds__(256) extend_join_rows_kernel(ExtendArgs a)
     if (!find_parts<M>(a, unit, &part)) return;
     const Span& t = part.t;
     const int r = t.row0 + tr, used = part.rg;
-    const int64_t at = part.at * M + tr, step = part.step * M;
+    const int64_t at = part.at + tr, step = part.step;
     const float* from = a.part_o + at * D + lane * 4;
     const bool there = r < t.rows;
     float top = -INFINITY;
@@ -787,7 +787,7 @@ ExtendPlan stream_plan(const gdn_kv_cache& c, const gdn_extend_dims& d, int64_t 
     const int64_t per = (steps + ranges - 1) / ranges;
     p.range = per * kRange;
     p.ranges = (steps + per - 1) / per;
-    p.share = 0;
+    p.share = p.packed = 0;
     p.least = real >= fill ? 8 : 2;
     // Shares are found by lanes, one a sequence, with sums of 32 bits. One sequence is divided by its bound,
     // which spares 0.6 us of looking.

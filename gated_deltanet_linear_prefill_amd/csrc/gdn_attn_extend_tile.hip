@@ -343,7 +343,7 @@ __global__ void __launch_bounds__(64 * S::WAVES, S::PER_SIMD) extend_tile_kernel
     }
     if (!whole) {  // this range's sums, for the join
         const float l = other_half_sum(st.l), e = ES == 2 && LSE ? other_half_sum(st.exact) : l;
-        const int64_t at = (int64_t)block_index() * M + 32 * rw + (lane & 31);
+        const int64_t at = rg * a.packed * p.c.h_kv + packed_row(a, w) + 32 * rw + (lane & 31);
         if (r < w.rows) {
             float* to = a.part_o + at * D + 4 * half;
 #pragma unroll
@@ -442,13 +442,15 @@ ExtendPlan extend_tile_plan(const gdn_kv_cache& c, const gdn_extend_dims& d)
     p.per_seq = c.n == 1 ? (int)((d.max_q * g + p.m - 1) / p.m) : 0;
     p.slots = c.n == 1 ? p.per_seq : d.total_q * g / p.m + c.n;
     p.units = p.slots * c.h_kv;
+    p.packed = d.total_q * g;
     // 256 workgroups of eight waves run at a time. Each costs its keys and what starting, masking, ending and
     // joining take, 15 to 20 us: as long as 280 keys (d = 256; a key takes 75 ns with 128 rows), 700 (128)
-    // or 1200 (64). Ranges are those that make this estimate least.
+    // or 1200 (64). Ranges are those that make this estimate least, as long as the join's grid, which has slots for tiles
+    // of all sequences, holds less than 2^31 workgroups.
     const int64_t tiles = (d.total_q * g + p.m - 1) / p.m * c.h_kv, len = extend_longest(c, d, p.m);
     const int64_t over = c.d == 256 ? 280 : c.d == 128 ? 700 : 1200;
     int64_t ranges = 1, least = (tiles + 255) / 256 * (len + over);
-    if (shape != kTwin)
+    if (shape != kTwin && p.units < (INT64_C(1) << 31) / (p.m * (c.d / 64)))
         for (int64_t r = 2; r <= 64 && len >= 512 * r && tiles * r <= 1024; ++r) {
             const int64_t cost = (tiles * r + 255) / 256 * (len / r + over) + over / 2;
             if (cost < least) {
@@ -456,8 +458,6 @@ ExtendPlan extend_tile_plan(const gdn_kv_cache& c, const gdn_extend_dims& d)
                 ranges = r;
             }
         }
-    if (p.units > 0 && ranges > 0x7fffffff / p.units) ranges = 0x7fffffff / p.units;  // the grid
-    if (ranges < 1) ranges = 1;
     const int64_t per = ((len + ranges - 1) / ranges + 255) / 256 * 256;  // whole units of every shape
     p.range = per > 0 ? per : 256;
     p.ranges = len > 0 ? (len + p.range - 1) / p.range : 1;

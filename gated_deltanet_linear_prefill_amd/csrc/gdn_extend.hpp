@@ -6,8 +6,10 @@
 
 namespace gdn {
 
-// Where the keys of a call's tiles are divided into ranges, sums go to the workspace,
-// [workgroup][row]: o [D] fp32 and (m, l, exact l, -).
+// Where the keys of a call's tiles are divided into ranges, sums go to the workspace, a row at a time:
+// o [D] fp32 and (m, l, exact l, -). Few rows: [workgroup][row of its tile]. Tiles of many rows:
+// [range][KV head][row], the rows of the call as they are packed, for a batch may leave most of its slots for tiles empty
+// (512 sequences of 732 tokens, fp8, d = 256: 21 GB by workgroups).
 struct ExtendPlan {
     int m;          // rows of a tile (0: nothing is launched)
     int per_seq;    // tiles of every sequence, or 0: as many as its rows need, packed
@@ -18,10 +20,12 @@ struct ExtendPlan {
     int64_t share;  // workgroups that the call's positions are divided over by their lengths, or 0: by range
     int least;      // ... with at least so many steps each
     int rows_from, rows_to;  // the sequences that are taken: by their rows (of a KV head)
+    int64_t packed;          // rows of a KV head that the call has, where the workspace is by these; or 0
     int64_t workgroups() const { return share ? share + units : units * ranges; }
+    int64_t part_rows(const gdn_kv_cache& c) const { return packed ? ranges * c.h_kv * packed : workgroups() * m; }
     size_t workspace(const gdn_kv_cache& c) const
     {
-        return m == 0 || ranges == 1 ? 0 : (size_t)(workgroups() * m) * (c.d * sizeof(float) + sizeof(float4));
+        return m == 0 || ranges == 1 ? 0 : (size_t)part_rows(c) * (c.d * sizeof(float) + sizeof(float4));
     }
 };
 
@@ -30,6 +34,7 @@ struct ExtendArgs {
     int64_t range;
     int ranges, slots, per_seq, rows_from, rows_to, page_shift;
     int share, least, longest;  // longest: virtual positions that a tile may have
+    int64_t packed;
     float* part_o;
     float4* part_ml;
 };
@@ -57,8 +62,9 @@ inline ExtendArgs extend_args(const ExtendCall& c, const ExtendPlan& p, void* ws
     a.share = (int)p.share;
     a.least = p.least;
     a.longest = (int)extend_longest(c.c, c.d, p.m);
+    a.packed = p.packed;
     a.part_o = static_cast<float*>(ws);
-    a.part_ml = reinterpret_cast<float4*>(a.part_o + p.workgroups() * p.m * c.c.d);
+    a.part_ml = reinterpret_cast<float4*>(a.part_o + p.part_rows(c.c) * c.c.d);
     return a;
 }
 
@@ -260,8 +266,8 @@ __device__ __forceinline__ bool find_span(const ExtendArgs& a, uint32_t unit, Sp
 }
 
 // What a workgroup takes of a tile: virtual positions [rg * range, rg * range + range). Its sums, where the
-// tile has others, go to part `at` of the workspace; for the join, at is that of range 0, the next lie `step`
-// after one another.
+// tile has others, go to the workspace's rows from `at` on; for the join, at is that of range 0, the next lie
+// `step` after one another.
 struct Part {
     Span t;
     int64_t range, at, step;
@@ -337,13 +343,12 @@ template <int M>
 __device__ __forceinline__ bool find_part(const ExtendArgs& a, uint32_t index, Part* x)
 {
     const ExtendCall& p = a.c;
-    x->at = index;
     if (!a.share) {
         // ranges of one index lie together in the grid: late ones, which few tiles have, spread over all XCDs
         const uint32_t units = (uint32_t)a.slots * (uint32_t)p.c.h_kv;
         if (index >= units * (uint64_t)a.ranges) return false;  // past the grid's end
         index = together(a, index);
-        x->at = index;
+        x->at = (int64_t)index * M;
         const uint32_t unit = index % units;
         x->rg = (int)(index / units);
         x->range = a.range;
@@ -362,9 +367,15 @@ __device__ __forceinline__ bool find_part(const ExtendArgs& a, uint32_t index, P
         return false;
     x->rg = (int)w.rg;
     x->t.head = (int)w.head;
-    x->at = w.at;
+    x->at = (int64_t)w.at * M;
     x->range = sh.range(s);
     return sh.span(a, s, (int)w.tile, &x->t);
+}
+
+// The first row of a tile in a workspace by rows, of range 0.
+__device__ __forceinline__ int64_t packed_row(const ExtendArgs& a, const Span& t)
+{
+    return t.head * a.packed + t.q0 * t.g + t.row0;
 }
 
 // The parts of a unit, a tile of a KV head, or false where it has one or none; rg is their number.
@@ -374,8 +385,8 @@ __device__ __forceinline__ bool find_parts(const ExtendArgs& a, uint32_t unit, P
     const ExtendCall& p = a.c;
     if (!a.share) {
         if (!find_span<M>(a, unit, &x->t)) return false;
-        x->at = unit;
-        x->step = (int64_t)a.slots * p.c.h_kv;
+        x->at = a.packed ? packed_row(a, x->t) : (int64_t)unit * M;
+        x->step = a.packed ? a.packed * p.c.h_kv : (int64_t)a.slots * p.c.h_kv * M;
         x->range = a.range;
     } else {
         const Shares<M> sh(a);
@@ -390,8 +401,8 @@ __device__ __forceinline__ bool find_parts(const ExtendArgs& a, uint32_t unit, P
         if (!block_fits((uint32_t)before, (uint32_t)tiles, (uint32_t)__builtin_amdgcn_readlane(sh.ranges, s), (uint32_t)p.c.h_kv,
                         (uint32_t)a.share + (uint32_t)a.slots * (uint32_t)p.c.h_kv))
             return false;  // nobody wrote its sums
-        x->step = (int64_t)tiles * p.c.h_kv;
-        x->at = (int64_t)before + (int64_t)local * p.c.h_kv + x->t.head;
+        x->step = (int64_t)tiles * p.c.h_kv * M;
+        x->at = ((int64_t)before + (int64_t)local * p.c.h_kv + x->t.head) * M;
         x->range = sh.range(s);
     }
     if (x->t.len <= x->range) return false;  // written by its only workgroup

@@ -561,7 +561,8 @@ gdn_status gdn_kv_append(const gdn_kv_cache* cache, const gdn_norm_rope* f, int6
  * the sizes, the bounds and, for up to 64 sequences of few rows, the batch's lengths: the same call gives
  * the same bits, and a sequence in another batch the same to the rounding of its sums. workspace then has
  * gdn_attn_extend_workspace_bytes(cache, dims) bytes (0 when nothing is divided, and for invalid
- * arguments).
+ * arguments). That does not grow steadily with the sizes; (10240 * r + 262144) * (4 * d + 16) bytes, r = 32 with
+ * d = 256 and 64 otherwise, serve every call.
  */
 typedef struct {
     int64_t total_q; /* rows of q, out and lse; total_q * h_q / h_kv below 2^31 - 2^16   */

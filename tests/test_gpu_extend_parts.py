@@ -1,10 +1,13 @@
 """GPU: attention of new tokens over the cache stays within its workspace where the offsets ask for more rows than
 there are (tests/test_extend_parts_cpu.py replays which parts are written)."""
+import random
+
 import pytest
 import torch
 
 import gated_deltanet_linear_prefill_amd as gdn
-from test_gpu_attn_extend import BF, DEV, F32, F8, Cache, fill, ints, queries
+from test_gpu_attn_extend import BF, DEV, F32, F8, Cache, fill, ints, offsets, queries
+from test_gpu_extend_shapes import sampled
 
 pytestmark = pytest.mark.gpu
 
@@ -27,3 +30,25 @@ def test_overlapping_sequences_stay_in_the_workspace(store, dtype):
     out = gdn.gdn_attn_extend(q, *cache.args(), ints(lens), ints(cu), max_q=total, max_len=7168, workspace=room[:need], **cache.scales())
     new = gdn.gdn_attn_extend(q, *cache.args(), ints(lens), ints(cu), max_q=total, max_len=7168, **cache.scales())
     assert torch.equal(out, new) and bool((room[need:] == 7).all())
+
+
+@pytest.mark.parametrize("store,dtype", [(F32, F32), (BF, BF), (F8, BF)])
+@pytest.mark.parametrize("n,hq,hk,d", [(40, 8, 2, 128), (200, 4, 1, 256), (300, 8, 2, 64)])
+def test_a_long_piece_among_many_tokens(n, hq, hk, d, store, dtype):
+    """Tiles of many rows whose keys are divided, in a workspace of just the size that is asked for."""
+    rng = random.Random(n)
+    lens_q = [1] * n
+    lens = [rng.randint(1, 60) for _ in range(n)]
+    lens_q[n // 3], lens[n // 3] = 150, 9000
+    lens_q[n // 2], lens[n // 2] = 70, 2500
+    cache = Cache(lens, 16, hk, d, store, extra_width=0)
+    fill(cache, 2, nan_behind=lens)
+    q = queries(sum(lens_q), hq, d, dtype)
+    need = gdn.gdn_attn_extend_workspace_bytes(n, cache.page_table.shape[1], 16, len(q), hq, hk, d, max_q=150, max_len=9000, dtype=dtype, store=store)
+    assert need > 0
+    room = torch.full((need + (8 << 20),), 7, dtype=torch.uint8, device=DEV)
+    lse = torch.full(q.shape[:2], 5.0, device=DEV)
+    out = gdn.gdn_attn_extend(q.to(DEV), *cache.args(), ints(lens), ints(offsets(lens_q)), max_q=150, max_len=9000, lse=lse, workspace=room[:need],
+                              **cache.scales())
+    sampled(cache, q, lens_q, lens, out, lse, 0, 0, rng, heads=1)
+    assert bool((room[need:] == 7).all())
