@@ -13,9 +13,10 @@
 // lane's pieces lie beside its neighbours', the next row is loaded while one is worked on, and stores of
 // whole lines bypass the caches: without these three 133, 49 and 91 us of the first, third and last.
 //
-// Angles. freq * pos is formed in 64 bits and reduced there to a fraction of a turn in
-// [-1/2, 1/2]; what its rounding to fp32 leaves out is put back by one term of the addition
-// theorems, so that sine and cosine are good to about an ulp at any position.
+// Angles. freq * pos, in turns, is formed in two 64-bit numbers (the product, and what its roundings leave: without it
+// 4e-7 radians are lost by 2^31) and reduced there to a fraction of a turn in [-1/2, 1/2]; what its rounding to fp32
+// leaves out is put back by one term of the addition theorems, so that sine and cosine are as good as the library's
+// functions of an exact angle at any position.
 #include "gdn_kv_rows.hpp"
 
 namespace gdn {
@@ -27,8 +28,9 @@ constexpr int kTokens = 16;  // of a workgroup, at most
 // scale * (cos, sin) of freq * pos.
 __device__ __forceinline__ float2 turn(double pos, float freq, float scale)
 {
-    double t = pos * (double)freq * 0.15915494309189533577;  // turns
-    t -= __builtin_rint(t);
+    constexpr double kTurn = 0.15915494309189535, kRest = -9.839338337591243e-18;  // 1 / (2 pi) and what its rounding leaves
+    const double angle = pos * (double)freq, left = __builtin_fma(pos, (double)freq, -angle);
+    const double t = __builtin_fma(angle, kTurn, -__builtin_rint(angle * kTurn)) + (angle * kRest + left * kTurn);
     const float r = (float)t;
     const float rest = (float)(t - (double)r) * 6.2831853f;
     float s, c;

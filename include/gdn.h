@@ -504,7 +504,8 @@ gdn_status gdn_attn_decode(const gdn_kv_cache* cache, int32_t h_q, int32_t dtype
  * The other elements stay as they are. A model with one position per token has axes = 1 and axis
  * NULL; images and video have several (time, height, width, say), and axis gives each pair's, in any
  * arrangement (values from axes on count as axes - 1). Everything is computed in fp32, the angle in
- * 64 bits and reduced there, so that far positions lose nothing, and rounded once at the end.
+ * 64 bits, together with what its roundings leave, and reduced there, so that far positions lose nothing, and
+ * rounded once at the end.
  * A NaN in a row reaches all of it through its norm; without one, its pair.
  */
 typedef struct {
