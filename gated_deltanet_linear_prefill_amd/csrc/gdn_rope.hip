@@ -149,10 +149,10 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(RopeCall p, int tok, int
                 return x;
             };
             // Squares that leave fp32's range are taken of the row times a power of two, which is exact:
-            // the norm has no other effect than on eps.
+            // the norm has no other effect than on eps. 2^100 brings the smallest squares far into fp32's range.
             float unit = 1.f, sum = sum_of(1.f);
             if (!(sum <= 3.4028234e38f) || (sum < 0x1p-100f && p.f.eps < 0x1p-100f)) {
-                unit = sum < 1.f ? 0x1p70f : 0x1p-70f;
+                unit = sum < 1.f ? 0x1p100f : 0x1p-70f;
                 sum = sum_of(unit);
             }
             const float inv = 1.f / sqrtf(sum * (1.f / D) + p.f.eps * unit * unit);
