@@ -7,7 +7,9 @@ import subprocess
 
 import pytest
 
-from test_sanitize_abi_cpu import CLANG, PKG, ROOT
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+PKG = os.path.join(ROOT, "gated_deltanet_linear_prefill_amd")
+CLANG = "/opt/rocm/lib/llvm/bin/clang++"
 
 
 @pytest.mark.skipif(shutil.which("hipcc") is None or shutil.which("nm") is None or not os.path.exists(CLANG), reason="needs the ROCm toolchain")
