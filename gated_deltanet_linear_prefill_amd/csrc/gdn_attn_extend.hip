@@ -747,7 +747,7 @@ bool narrow_tiles(const gdn_kv_cache& c, const gdn_extend_dims& d, int64_t rows)
     const int64_t tiles = (each <= sparse / c.n ? c.n * each : sparse) * c.h_kv;
     const int64_t step_bytes = (int64_t)kRange * 2 * c.d * (c.store == GDN_FP8 ? 1 : c.store == GDN_F32 ? 4 : 2);
     const int64_t steps = (extend_longest(c, d, 16) + kRange - 1) / kRange;
-    if (c.n > 64) return false;  // whose tiles of a sequence lie apart
+    if (c.n > 64) return false;  // more than Shares takes: a sequence's tiles would lie apart; no measured crossing
     if (rows <= 64 && c.d == 256 && c.store == GDN_FP8 && d.dtype == GDN_BF16) return true;
     const int64_t most = c.store != GDN_F32 ? 192 : rows <= 64 ? 512 : 2048;
     return tiles <= 768 && tiles * steps <= (most << 20) / step_bytes;
@@ -776,7 +776,8 @@ ExtendPlan stream_plan(const gdn_kv_cache& c, const gdn_extend_dims& d, int64_t 
     // four steps stay together, which spares the second launch.
     // Up to 64 sequences are divided by their lengths, on the GPU, instead of by max_len (us, by max_len / by
     // lengths; all drawn up to the bound): 16 of 4 tokens as above 82 / 72, 64 of one token, up to 8192, d = 128, 32/8
-    // heads 234 / 212, 40 of them 160 / 143, 32 behind a window 59 / 59.
+    // heads 234 / 212, 40 of them 160 / 143, 32 behind a window 59 / 59. More than 64, which have no lane each, are
+    // divided by max_len or not at all: 64 of one token after up to 16000, d = 256, 16/2 heads take 214, 65 take 438.
     const int64_t fill = (c.d == 256 && !(c.store == GDN_FP8 && p.m == 16)) || p.m == 64 ? 256 : 512;
     int64_t ranges = real >= fill ? (real * steps / 8 < 4096 ? real * steps / 8 : 4096) / real : fill / real;
     if (ranges > (steps + 1) / 2) ranges = (steps + 1) / 2;
