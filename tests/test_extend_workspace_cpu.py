@@ -20,6 +20,7 @@ MIXED = [
     (512, 732, 8, 8, 256, 128, 131072, BF, F8), (1000, 1100, 1, 1, 256, 101, 131072, BF, BF), (256, 768, 8, 1, 256, 513, 131072, BF, F8),
     (256, 767, 32, 8, 128, 512, 131072, BF, BF), (193, 3107, 8, 8, 256, 3107, 84046, BF, F8), (512, 800, 16, 2, 256, 289, 65536, F32, F32),
     (100, 600, 16, 2, 256, 501, 131072, F32, F8), (2000, 2500, 32, 8, 128, 501, 131072, BF, F8), (65, 200, 16, 16, 64, 136, 131072, BF, BF),
+    (1 << 22, 800, 8, 8, 256, 129, 131072, BF, F8),  # the grid of a join would pass 2^31 workgroups
 ]
 
 

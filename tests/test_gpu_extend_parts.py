@@ -52,3 +52,36 @@ def test_a_long_piece_among_many_tokens(n, hq, hk, d, store, dtype):
                               **cache.scales())
     sampled(cache, q, lens_q, lens, out, lse, 0, 0, rng, heads=1)
     assert bool((room[need:] == 7).all())
+
+
+@pytest.mark.parametrize("store,dtype", [(F32, F32), (BF, BF), (F8, BF)])
+def test_captured_with_other_lengths_later(store, dtype):
+    """Two graphs that share a workspace, their offsets and lengths changed between replays: the divided tiles' rows move."""
+    n, total, width = 12, 240, 500
+    cache = Cache([8000] * n, 16, 2, 128, store, extra_width=0)
+    fill(cache, 2)
+    q = queries(total, 8, 128, dtype).to(DEV)
+    need = gdn.gdn_attn_extend_workspace_bytes(n, width, 16, total, 8, 2, 128, max_q=200, max_len=8000, dtype=dtype, store=store)
+    assert need > 0 and cache.page_table.shape[1] == width
+    room = torch.empty(need, dtype=torch.uint8, device=DEV)
+    cu, lens, outs, graphs = ints([0] * n + [total]), ints([8000] * n), [torch.empty_like(q) for _ in range(2)], []
+    call = lambda out, **kw: gdn.gdn_attn_extend(q, *cache.args(), lens, cu, max_q=200, max_len=8000, out=out, **kw, **cache.scales())
+    call(outs[0], workspace=room)
+    torch.cuda.synchronize()
+    for out in outs:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            call(out, workspace=room)
+    rng = random.Random(3)
+    for step in range(4):
+        lens_q = [1] * n
+        lens_q[rng.randrange(n)] += total - n - 30 - (step == 2) * 10
+        lens_q[rng.randrange(n)] += 30
+        cu.copy_(ints(offsets(lens_q)))
+        lens.copy_(ints([max(m, rng.randint(1, 8000)) for m in lens_q]))
+        for out, graph in zip(outs, graphs):
+            out.fill_(3.0)
+            graph.replay()
+        torch.cuda.synchronize()
+        new = call(torch.full_like(q, 3.0))
+        assert torch.equal(outs[0], new) and torch.equal(outs[1], new), step
